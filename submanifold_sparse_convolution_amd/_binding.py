@@ -21,6 +21,8 @@ SUBM_POOL_MAX, SUBM_POOL_MEAN = 1, 2
 SUBM_COARSE, SUBM_FINE, SUBM_PARENT = 0, 1, 2
 SUBM_SUBDIVIDE, SUBM_DOWNSAMPLE, SUBM_UPSAMPLE_MASKED = 0, 1, 2
 SUBM_ACT_NONE, SUBM_ACT_SILU, SUBM_ACT_RELU = 0, 1, 2
+SUBM_ROPE_INTERLEAVED, SUBM_ROPE_HALF = 0, 1
+SUBM_ROPE_PLAIN, SUBM_ROPE_LINEAR, SUBM_ROPE_BASE, SUBM_ROPE_PARTS = 0, 1, 2, 3
 _DTYPE_CODES = {torch.float32: SUBM_F32, torch.float16: SUBM_F16, torch.bfloat16: SUBM_BF16}
 TAPS = 27
 
@@ -58,9 +60,23 @@ C_FUNCTIONS = (
     "sparse_indice_map_subdivide",
     "sparse_group_norm_act",
     "subm_conv3d_forward_group_norm_act",
+    "sparse_layer_norm_forward",
+    "sparse_layer_norm_backward",
+    "sparse_rope_frequencies",
+    "sparse_rope_forward",
+    "sparse_rope_backward",
+    "sparse_attention_forward",
+    "sparse_attention_backward",
     "subm_status_string",
     "subm_last_error",
 )
+
+
+class _HeadsArg(ctypes.Structure):
+    """subm_heads_t of include/sparse_transformer.h."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
 
 _lib = None
 _lib_lock = threading.Lock()
@@ -121,6 +137,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.sparse_group_norm_act.argtypes = [vp, i64, ci, ci, vp, ci, ci, vp, vp, ctypes.c_float, ci, vp, vp]
         lib.subm_conv3d_forward_group_norm_act.argtypes = [vp, i64, ci, ci, ci, ci, vp, vp, vp, vp, ci, ci, vp, vp,
                                                            ctypes.c_float, ci, vp, vp]
+        cf, cd, hp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_HeadsArg)
+        lib.sparse_layer_norm_forward.argtypes = [vp, i64, ci, ci, vp, vp, cf, vp, vp, vp, vp]
+        lib.sparse_layer_norm_backward.argtypes = [vp, vp, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp]
+        lib.sparse_rope_frequencies.argtypes = [ci, cd, ci, cd, cd, ctypes.POINTER(cf), ctypes.POINTER(cf)]
+        for rope in (lib.sparse_rope_forward, lib.sparse_rope_backward):
+            rope.argtypes = [hp, i64, ci, ci, ci, vp, i64, ci, vp, ci, ci, cf, hp, vp]
+        lib.sparse_attention_forward.argtypes = [hp, hp, hp, i64, i64, vp, vp, ci, ci, ci, ci, ci, cf, hp, vp, vp]
+        lib.sparse_attention_backward.argtypes = [hp, hp, hp, hp, hp, vp, i64, i64, vp, vp, ci, ci, ci, ci, ci, cf, hp,
+                                                  hp, hp, vp]
         for name in C_FUNCTIONS[:-2]:
             getattr(lib, name).restype = ci
         lib.subm_status_string.argtypes = [ci]
@@ -691,3 +716,229 @@ def sparse_group_norm_act(x: torch.Tensor, item_offsets: torch.Tensor, groups: i
                                        out.data_ptr(), _stream_ptr(stream, x.device))
     _check(lib, "sparse_group_norm_act", st)
     return out
+
+
+# --------------------------------------------------------------------------- transformer block
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on (its memory is then reused in that
+    stream's order)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _vector(t, shape, dtype, device, what):
+    """data_ptr of an optional contiguous device tensor of that shape and dtype."""
+    if t is None:
+        return None
+    _device_tensor(t, what)
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{what} must be {list(shape)} {dtype} on {device}")
+    return t.data_ptr()
+
+
+def sparse_layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                              eps: float = 1e-5, stats: bool = False, out: torch.Tensor | None = None, stream=None):
+    """Layer norm of the rows of x [N, C]: (y, mean, rstd), the float32 statistics [N] only with
+    stats=True (else None), which the backward pass needs.  out may be x (in place)."""
+    _device_tensor(x, "x")
+    if x.dim() != 2 or x.dtype not in _DTYPE_CODES:
+        raise ValueError("x must be [N, C] float32 / float16 / bfloat16")
+    n, c = x.shape
+    g = _vector(gamma, (c,), x.dtype, x.device, "gamma")
+    b = _vector(beta, (c,), x.dtype, x.device, "beta")
+    y = _empty((n, c), x.dtype, x.device, stream) if out is None else out
+    if out is not None:
+        _vector(out, (n, c), x.dtype, x.device, "out")
+    mean = rstd = mean_ptr = rstd_ptr = None
+    if stats:
+        both = _empty((2, n), torch.float32, x.device, stream)
+        mean, rstd = both[0], both[1]
+        mean_ptr = both.data_ptr()
+        rstd_ptr = mean_ptr + 4 * n
+    lib = load_library()
+    with _on_device(x.device):
+        st = lib.sparse_layer_norm_forward(x.data_ptr(), n, c, _DTYPE_CODES[x.dtype], g, b, eps, y.data_ptr(), mean_ptr,
+                                           rstd_ptr, _stream_ptr(stream, x.device))
+    _check(lib, "sparse_layer_norm_forward", st)
+    return y, mean, rstd
+
+
+def sparse_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                               gamma: torch.Tensor | None = None, weight_grads: bool = True,
+                               out: torch.Tensor | None = None, stream=None):
+    """Gradients of sparse_layer_norm_forward: (dx, dgamma, dbeta), the last two None with
+    weight_grads=False.  mean, rstd: the forward pass's.  out may be dy (in place)."""
+    _device_tensor(x, "x")
+    if x.dim() != 2 or x.dtype not in _DTYPE_CODES:
+        raise ValueError("x must be [N, C] float32 / float16 / bfloat16")
+    if dy is None or mean is None or rstd is None:
+        raise ValueError("dy, mean and rstd are required")
+    n, c = x.shape
+    dy_ptr = _vector(dy, (n, c), x.dtype, x.device, "dy")
+    m = _vector(mean, (n,), torch.float32, x.device, "mean")
+    r = _vector(rstd, (n,), torch.float32, x.device, "rstd")
+    g = _vector(gamma, (c,), x.dtype, x.device, "gamma")
+    dx = _empty((n, c), x.dtype, x.device, stream) if out is None else out
+    if out is not None:
+        _vector(out, (n, c), x.dtype, x.device, "out")
+    dgamma = dbeta = dg_ptr = db_ptr = None
+    if weight_grads:
+        dgamma = _empty((c,), x.dtype, x.device, stream)
+        dbeta = _empty((c,), x.dtype, x.device, stream)
+        dg_ptr, db_ptr = dgamma.data_ptr(), dbeta.data_ptr()
+    lib = load_library()
+    with _on_device(x.device):
+        st = lib.sparse_layer_norm_backward(dy_ptr, x.data_ptr(), n, c, _DTYPE_CODES[x.dtype], g, m, r, dx.data_ptr(),
+                                            dg_ptr, db_ptr, _stream_ptr(stream, x.device))
+    _check(lib, "sparse_layer_norm_backward", st)
+    return dx, dgamma, dbeta
+
+
+def _heads_arg(t, what, like=None):
+    """subm_heads_t of a [N, heads, head_dim] view whose channels are contiguous; `like`: the
+    tensor whose dtype and device it must share."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what} must be a device tensor (got {t.device})")
+    if t.dim() != 3 or t.dtype not in _DTYPE_CODES:
+        raise ValueError(f"{what} must be [N, heads, head_dim] float32 / float16 / bfloat16")
+    row, head, channel = t.stride()
+    n, heads, dim = t.shape
+    if channel != 1 and dim > 1:
+        raise ValueError(f"{what}: the channels of a head must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} must be {like.dtype} on {like.device}")
+    # (a stride that no step takes is free: torch reports any value for it)
+    return _HeadsArg(t.data_ptr(), row if n > 1 else heads * dim, head if heads > 1 else dim)
+
+
+def sparse_rope_frequencies(count: int, base: float = 10000.0, scaling: int = SUBM_ROPE_PLAIN, factor: float = 1.0,
+                            trained_length: float = 1.0):
+    """(float32 CPU tensor [count], magnitude): the frequencies of one axis and the factor of the
+    rotated channels; scaling is one of SUBM_ROPE_PLAIN / _LINEAR / _BASE / _PARTS."""
+    freq = torch.empty(max(int(count), 1), dtype=torch.float32)
+    magnitude = ctypes.c_float()
+    lib = load_library()
+    st = lib.sparse_rope_frequencies(int(count), float(base), int(scaling), float(factor), float(trained_length),
+                                     ctypes.cast(freq.data_ptr(), ctypes.POINTER(ctypes.c_float)),
+                                     ctypes.byref(magnitude))
+    _check(lib, "sparse_rope_frequencies", st)
+    return freq, magnitude.value
+
+
+def _rope(func, x, positions, freq, layout, magnitude, out, stream):
+    xa = _heads_arg(x, "x")
+    n, heads, dim = x.shape
+    if not isinstance(positions, torch.Tensor) or positions.device != x.device or positions.dtype != torch.int32 or \
+            positions.dim() != 2 or positions.shape[0] != n or (positions.shape[1] > 1 and positions.stride(1) != 1):
+        raise ValueError("positions must be int32 [N, axes] on x's device, the axes contiguous")
+    _device_tensor(freq, "freq")
+    if freq.dtype != torch.float32 or freq.dim() != 1 or freq.device != x.device:
+        raise ValueError("freq must be float32 [num_freq] on x's device")
+    y = _empty((n, heads, dim), x.dtype, x.device, stream) if out is None else out
+    ya = _heads_arg(y, "out", x)
+    if y.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    lib = load_library()
+    with _on_device(x.device):
+        st = getattr(lib, func)(xa, n, heads, dim, _DTYPE_CODES[x.dtype], positions.data_ptr(), positions.stride(0),
+                                positions.shape[1], freq.data_ptr(), freq.shape[0], layout, magnitude, ya,
+                                _stream_ptr(stream, x.device))
+    _check(lib, func, st)
+    return y
+
+
+def sparse_rope_forward(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, layout: int,
+                        magnitude: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of x [N, heads, head_dim] (any row and head strides): positions int32
+    [N, axes] (voxel coordinates: coords[:, 1:]), freq float32 [num_freq] of each axis, layout
+    SUBM_ROPE_INTERLEAVED or SUBM_ROPE_HALF.  out may be x (in place)."""
+    return _rope("sparse_rope_forward", x, positions, freq, layout, magnitude, out, stream)
+
+
+def sparse_rope_backward(dy: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, layout: int,
+                         magnitude: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of sparse_rope_forward: the rotation the other way."""
+    return _rope("sparse_rope_backward", dy, positions, freq, layout, magnitude, out, stream)
+
+
+def _attention_args(q, k, v, q_offsets, k_offsets, scale):
+    qa, ka, va = _heads_arg(q, "q"), _heads_arg(k, "k", q), _heads_arg(v, "v", q)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [Nq, heads, head_dim], k and v [Nk, kv_heads, head_dim]")
+    _offsets_arg(q_offsets)
+    if k_offsets is None:
+        if k.shape[0] != q.shape[0]:
+            raise ValueError("k_offsets is required when q and k have different rows")
+        k_offsets = q_offsets
+    elif k_offsets is not q_offsets:
+        _offsets_arg(k_offsets)
+        if k_offsets.shape != q_offsets.shape:
+            raise ValueError("q_offsets and k_offsets must have the same items")
+    if q_offsets.device != q.device or k_offsets.device != q.device:
+        raise ValueError("offsets must be on q's device")
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+    return qa, ka, va, k_offsets, scale
+
+
+def sparse_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                             k_offsets: torch.Tensor | None = None, scale: float | None = None,
+                             out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Attention within items: (out [Nq, heads, head_dim], lse float32 [Nq, heads]).
+
+    q [Nq, heads, head_dim], k and v [Nk, kv_heads, head_dim] with any row and head strides;
+    q_offsets, k_offsets int64 [items + 1] on the device (k_offsets None: self attention); scale
+    defaults to head_dim ** -0.5.  A query whose item has no keys gets out 0, lse -infinity."""
+    qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
+    nq, heads, dim = q.shape
+    if out is None:
+        out = _empty((nq, heads, dim), q.dtype, q.device, stream)
+    oa = _heads_arg(out, "out", q)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = _empty((nq, heads), torch.float32, q.device, stream)
+        lse_ptr = lse.data_ptr()
+    else:
+        lse_ptr = _vector(lse, (nq, heads), torch.float32, q.device, "lse")
+    lib = load_library()
+    with _on_device(q.device):
+        st = lib.sparse_attention_forward(qa, ka, va, nq, k.shape[0], q_offsets.data_ptr(), k_offsets.data_ptr(),
+                                          q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype], scale,
+                                          oa, lse_ptr, _stream_ptr(stream, q.device))
+    _check(lib, "sparse_attention_forward", st)
+    return out, lse
+
+
+def sparse_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              out: torch.Tensor, lse: torch.Tensor, q_offsets: torch.Tensor,
+                              k_offsets: torch.Tensor | None = None, scale: float | None = None,
+                              dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                              dv: torch.Tensor | None = None, stream=None):
+    """(dq, dk, dv) of sparse_attention_forward from dout and the forward pass's out and lse.  dq,
+    dk and dv may be given as views of a packed buffer."""
+    qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
+    nq, heads, dim = q.shape
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(k.shape, q.dtype, q.device, stream) if dv is None else dv
+    ga, oa = _heads_arg(dout, "dout", q), _heads_arg(out, "out", q)
+    dqa, dka, dva = _heads_arg(dq, "dq", q), _heads_arg(dk, "dk", q), _heads_arg(dv, "dv", q)
+    if not (dout.shape == out.shape == dq.shape == q.shape) or not (dk.shape == dv.shape == k.shape):
+        raise ValueError("dout, out and dq must have q's shape, dk and dv k's")
+    if lse is None:
+        raise ValueError("lse is required")
+    lse_ptr = _vector(lse, (nq, heads), torch.float32, q.device, "lse")
+    lib = load_library()
+    with _on_device(q.device):
+        st = lib.sparse_attention_backward(ga, qa, ka, va, oa, lse_ptr, nq, k.shape[0], q_offsets.data_ptr(),
+                                           k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim,
+                                           _DTYPE_CODES[q.dtype], scale, dqa, dka, dva, _stream_ptr(stream, q.device))
+    _check(lib, "sparse_attention_backward", st)
+    return dq, dk, dv

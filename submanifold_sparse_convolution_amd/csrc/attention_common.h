@@ -1,0 +1,248 @@
+// What the attention kernels share: the ragged tiling, tiles of rows in LDS, and the fragments of
+// the 32x32x16 matrix instruction.
+//
+// Rows.  There is no mask inside an item, so the G query heads that share a key head are simply
+// G times as many rows of that head: packed row r of item b and key head j is token
+// q_offsets[b] + r / G, head j G + r % G.  Grouped heads, single tokens and long sequences are
+// then one problem [rows, d] x [keys, d] for each (item, key head), and the gradients of a shared
+// key head come out summed over its query heads.
+//
+// Tiles without a plan.  A grid over blocks of B packed rows of ragged items needs no prefix sum:
+// item b owns the slots floor(s / B) + b .. floor(e / B) + b, with s, e its first and past-the-end
+// packed rows, of which the first ceil((e - s) / B) hold its tiles and the rest (at most one)
+// exit.  The starts rise strictly with b, so a slot finds its item by binary search, and there are
+// floor(total / B) + items slots, which the host knows.
+//
+// Products.  Every kernel keeps its own rows as the columns of the accumulator, so a lane holds 16
+// scores of one own row: element i of the tile of rows 0 .. 31 is row 8 (i / 4) + 4 (lane / 32) +
+// i % 4.  Those 16 values, converted, are the B operand of the next product as they lie: the
+// contraction takes rows in the order (lane half, element), and the A operand is read from LDS in
+// that same order.  No score crosses lanes except for the maximum and sum of two halves.
+#pragma once
+
+#include "device_common.h"
+#include "internal.h"
+#include "sparse_transformer.h"
+
+namespace submconv {
+
+// Eight contraction values of a lane: lane l holds row (or column) l % 32, values 8 (l / 32) + j.
+template <DT D> struct Frag { uint4 v[Elem<D>::kSize / 2]; };
+
+template <DT D> __device__ __forceinline__ f32x16_t mma(const Frag<D>& a, const Frag<D>& b, f32x16_t c) {
+  if constexpr (D == DT::F32) {
+    // The same 16 contraction steps as the 16-bit form, two at a time (one of each lane half).
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.v[i].x), __uint_as_float(b.v[i].x), c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.v[i].y), __uint_as_float(b.v[i].y), c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.v[i].z), __uint_as_float(b.v[i].z), c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.v[i].w), __uint_as_float(b.v[i].w), c, 0, 0, 0);
+    }
+    return c;
+  } else {
+    return mfma32<D>(a.v[0], b.v[0], c);
+  }
+}
+
+__device__ __forceinline__ f32x16_t zero16() {
+  f32x16_t z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// Elements 8 s .. 8 s + 7 of a score tile as the contraction step s (of 2) of the next product.
+template <DT D> __device__ __forceinline__ Frag<D> to_frag(const f32x16_t& p, int s) {
+  Frag<D> f;
+  if constexpr (D == DT::F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      f.v[i] = make_uint4(__float_as_uint(p[8 * s + 4 * i]), __float_as_uint(p[8 * s + 4 * i + 1]),
+                          __float_as_uint(p[8 * s + 4 * i + 2]), __float_as_uint(p[8 * s + 4 * i + 3]));
+  } else {
+    const uint2 lo = pack4<D>(p[8 * s], p[8 * s + 1], p[8 * s + 2], p[8 * s + 3]);
+    const uint2 hi = pack4<D>(p[8 * s + 4], p[8 * s + 5], p[8 * s + 6], p[8 * s + 7]);
+    f.v[0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+  return f;
+}
+
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+
+// One tensor as the kernels see it.
+template <DT D> struct Heads {
+  typename Elem<D>::T* data;
+  int64_t row, head;
+};
+
+template <DT D> __device__ __forceinline__ Heads<D> heads_of(const subm_heads_t& t) {
+  return Heads<D>{static_cast<typename Elem<D>::T*>(t.data), t.row_stride, t.head_stride};
+}
+
+// The rows of one (item, key head): q-like tensors take G heads of a token as G rows.
+struct RowMap {
+  int64_t first;  // first token of the item
+  int head0;      // first head
+  int group;      // heads a token
+  template <DT D> __device__ __forceinline__ typename Elem<D>::T* at(const Heads<D>& t, int row) const {
+    const int tok = group == 1 ? row : row / group;
+    const int h = group == 1 ? 0 : row - tok * group;
+    return t.data + (first + tok) * t.row + (int64_t)(head0 + h) * t.head;
+  }
+  // index into a float [tokens, heads] array
+  __device__ __forceinline__ int64_t stat(int row, int heads) const {
+    const int tok = group == 1 ? row : row / group;
+    return (first + tok) * heads + head0 + (row - tok * group);
+  }
+};
+
+// The item of slot `slot` in a tiling by `block` packed rows of `offsets` (each token `group`
+// rows), and the slot's tile in it.
+__device__ __forceinline__ int find_item(const int64_t* offsets, int64_t total, int items, int group, int block, int64_t slot,
+                                         int* tile) {
+  const auto start = [&](int b) {
+    const int64_t o = offsets[b];
+    return (o < 0 ? 0 : o > total ? total : o) * group / block + b;
+  };
+  int lo = 0, hi = items - 1;  // the last item whose first slot is at or before `slot`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (start(mid) <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t t = slot - start(lo);
+  *tile = t < 0 ? INT32_MAX / block : (int)t;  // (only for offsets that do not rise: no such rows)
+  return lo;
+}
+
+__device__ __forceinline__ void item_rows(const int64_t* offsets, int64_t total, int b, int64_t* first, int* count) {
+  int64_t s = offsets[b], e = offsets[b + 1];
+  s = s < 0 ? 0 : s > total ? total : s;
+  e = e < s ? s : e > total ? total : e;
+  *first = s;
+  *count = (int)(e - s);
+}
+
+// ------------------------------------------------------------------------ tiles in LDS
+//
+// A tile is R rows of DP channels, row-major in 16-byte chunks, chunk c of row r at position
+// c ^ (r & 7): the 8 lanes that a wide read serves at once sit on 8 consecutive rows at one
+// chunk, and without the swizzle all 8 would fall on the same banks.
+
+template <DT D, int DP> constexpr int kRowChunks = DP * Elem<D>::kSize / 16;
+template <DT D, int DP> constexpr int kRowBytes = DP * Elem<D>::kSize;
+
+// A operand of step kk (channels 16 kk .. 16 kk + 15) over tile rows r0 .. r0 + 31.
+template <DT D, int DP>
+__device__ __forceinline__ Frag<D> row_frag(const unsigned char* tile, int r0, int kk, int lane) {
+  constexpr int kPer = Elem<D>::kSize / 2;  // chunks of 8 values
+  const int r = r0 + (lane & 31);
+  Frag<D> f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = (kk * 2 + (lane >> 5)) * kPer + i;
+    f.v[i] = *reinterpret_cast<const uint4*>(tile + r * kRowBytes<D, DP> + ((c ^ (r & 7)) << 4));
+  }
+  return f;
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+// A operand of the transposed tile: row = channel 32 db + lane % 32, contraction over tile rows
+// r0 + 8 (j / 4) + 4 (lane / 32) + j % 4 (r0 a multiple of 16), the order of to_frag.
+template <DT D, int DP>
+__device__ __forceinline__ Frag<D> column_frag(const unsigned char* tile, int r0, int db, int lane) {
+  Frag<D> f;
+  if constexpr (D == DT::F32) {
+    const int col = db * 32 + (lane & 31);
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = r0 + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+      x[j] = *reinterpret_cast<const float*>(tile + r * kRowBytes<D, DP> + (((col >> 2) ^ (r & 7)) << 4) + ((col & 3) << 2));
+    }
+    f.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    f.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+  } else {
+    // The transposing read: 16 lanes hand in 4 rows of 16 channels (lane t: row t / 4, channels
+    // 4 (t % 4) .. + 3) and lane t gets channel t of the 4 rows.
+    const int t = lane & 15;
+    const int col = db * 32 + ((lane >> 4) & 1) * 16 + (t & 3) * 4;
+    uint2 half[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + 8 * i + 4 * (lane >> 5) + (t >> 2);
+      const unsigned char* p = tile + r * kRowBytes<D, DP> + (((col >> 3) ^ (r & 7)) << 4) + ((col & 7) << 1);
+      half[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uintptr_t)lds_offset(p)));
+    }
+    f.v[0] = make_uint4(half[0].x, half[0].y, half[1].x, half[1].y);
+  }
+  return f;
+}
+
+// Stages rows r0 .. r0 + R - 1 (of `rows`) into a tile, zeros past the last row and past head_dim.
+template <DT D, int DP, int R, int THREADS>
+__device__ __forceinline__ void stage_rows(unsigned char* tile, const Heads<D>& t, const RowMap& map, int r0, int rows,
+                                           int head_dim) {
+  constexpr int C = kRowChunks<D, DP>;
+  constexpr int kVals = 16 / Elem<D>::kSize;
+  for (int i = threadIdx.x; i < R * C; i += THREADS) {
+    const int r = i / C, c = i % C;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r0 + r < rows && c * kVals < head_dim) v = *reinterpret_cast<const uint4*>(map.at<D>(t, r0 + r) + c * kVals);
+    *reinterpret_cast<uint4*>(tile + r * kRowBytes<D, DP> + ((c ^ (r & 7)) << 4)) = v;
+  }
+}
+
+// A lane's own row as the B operand of step kk, straight from global memory.
+template <DT D>
+__device__ __forceinline__ Frag<D> own_frag(const typename Elem<D>::T* row, bool there, int kk, int head_dim, int lane) {
+  constexpr int kPer = Elem<D>::kSize / 2;
+  constexpr int kVals = 16 / Elem<D>::kSize;
+  Frag<D> f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = (kk * 2 + (lane >> 5)) * kPer + i;
+    f.v[i] = there && c * kVals < head_dim ? *reinterpret_cast<const uint4*>(row + c * kVals) : make_uint4(0, 0, 0, 0);
+  }
+  return f;
+}
+
+// Four consecutive channels of an own row, rounded once.
+template <DT D> __device__ __forceinline__ void store4(typename Elem<D>::T* p, float a, float b, float c, float d) {
+  if constexpr (D == DT::F32) *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+  else *reinterpret_cast<uint2*>(p) = pack4<D>(a, b, c, d);
+}
+
+// Accumulator tiles [DP / 32] (row = channel, column = own row) to the row, times `f`.
+template <DT D, int DP>
+__device__ __forceinline__ void store_row(typename Elem<D>::T* row, const f32x16_t (&acc)[DP / 32], float f, int head_dim,
+                                          int lane) {
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int c = db * 32 + 8 * a + 4 * (lane >> 5);
+      if (c < head_dim)
+        store4<D>(row + c, acc[db][4 * a] * f, acc[db][4 * a + 1] * f, acc[db][4 * a + 2] * f, acc[db][4 * a + 3] * f);
+    }
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Host: the checks that the forward and backward entry points share (attention.hip).
+struct AttentionShape {
+  int64_t nq, nk;
+  const int64_t *q_offsets, *k_offsets;
+  int items, heads, kv_heads, head_dim, dtype;
+  float scale;
+};
+Status check_attention(const AttentionShape& s);
+Status check_heads(const subm_heads_t* t, int64_t rows, int heads, const AttentionShape& s, bool written, const char* what);
+
+}  // namespace submconv
