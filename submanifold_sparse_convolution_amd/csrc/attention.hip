@@ -25,97 +25,180 @@ struct FwdArgs {
   float scale;
 };
 
-constexpr int kFwdWaves = 4;
-constexpr int kFwdRows = 32 * kFwdWaves;  // packed rows of a workgroup, 32 a wave
-constexpr int kFwdKeys = 64;              // keys of a tile
+constexpr float kNone = -1.7e38f;  // a running maximum before any score (finite: differences stay numbers)
+constexpr float kSlack = 8.f;      // a new maximum up to 2^8 above the base leaves the base
 
-template <DT D, int DP>
-__global__ __launch_bounds__(kFwdWaves * 64) void attention_forward_kernel(FwdArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char s_k[kFwdKeys * kRowBytes<D, DP>];
-  __shared__ __attribute__((aligned(16))) unsigned char s_v[kFwdKeys * kRowBytes<D, DP>];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The running softmax of one own row (held by the lanes l and l + 32, half its scores each):
+// scores are kept as c * s - base in powers of two; base is a maximum that may lag behind the
+// true one by kSlack, so that most tiles do not rescale the accumulator (p stays below 2^8, which
+// every storage type holds).
+struct RowState {
+  float base = kNone;
+  float sum = 0.f;  // of this lane's half
+};
+
+// Scores (raw) -> probabilities in place; returns the factor that earlier sums shrink by, and
+// whether any row of the wave does shrink.
+template <int KB>
+__device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowState& st, float* shrink) {
+  float top = fmaxf(s[0][0], s[0][1]);
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = kb == 0 ? 2 : 0; i < 16; i += 2) top = fmaxf(top, fmaxf(s[kb][i], s[kb][i + 1]));
+  top = half_max(top) * c;
+  const bool moves = __builtin_amdgcn_ballot_w64(top > st.base + kSlack) != 0;
+  const float base = moves ? fmaxf(st.base, top) : st.base;
+  *shrink = exp2_fast(st.base - base);
+  st.base = base;
+  float sum = 0.f;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[kb][i] = exp2_fast(fmaf(s[kb][i], c, -base));
+      sum += s[kb][i];
+    }
+  st.sum = fmaf(st.sum, *shrink, sum);
+  return moves;
+}
+
+// Streams the keys through LDS in tiles of KEYS, S of them in flight; one step of the loop holds
+// three independent pieces of work, so that the matrix cores run while the exponentials do:
+//   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
+template <DT D, int DP, int W, int KEYS, int S>
+__global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
+  constexpr int KB = KEYS / 32;
+  constexpr int kTile = KEYS * kRowBytes<D, DP>;
+  constexpr int kRows = 32 * W;
+  using Loader = TileLoader<D, DP, KEYS, W>;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[2 * S * kTile];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads, head = blockIdx.y;
   int tile;
-  const int item = find_item(a.q_offsets, a.nq, a.items, group, kFwdRows, blockIdx.x, &tile);
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, blockIdx.x, &tile);
   int64_t q0, k0;
   int nq, nk;
   item_rows(a.q_offsets, a.nq, item, &q0, &nq);
   item_rows(a.k_offsets, a.nk, item, &k0, &nk);
   const int rows = nq * group;
-  if ((int64_t)tile * kFwdRows >= rows) return;
-  const RowMap qmap{q0, head * group, group}, kmap{k0, head, 1};
+  if ((int64_t)tile * kRows >= rows) return;
+  const RowMap qmap{q0, head * group, group};
   const Heads<D> q = heads_of<D>(a.q), k = heads_of<D>(a.k), v = heads_of<D>(a.v), out = heads_of<D>(a.out);
+  const typename Elem<D>::T* kp = k.data + k0 * k.row + (int64_t)head * k.head;
+  const typename Elem<D>::T* vp = v.data + k0 * v.row + (int64_t)head * v.head;
 
-  const int row = tile * kFwdRows + wave * 32 + (lane & 31);
+  const int row = tile * kRows + wave * 32 + (lane & 31);
   const bool there = row < rows;
   Frag<D> qf[DP / 16];
   const typename Elem<D>::T* qrow = qmap.at<D>(q, there ? row : 0);
+  // a negative scale goes into q, so that the largest score is the largest product
+  const uint32_t flip = a.scale < 0.f ? (D == DT::F32 ? 0x80000000u : 0x80008000u) : 0u;
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) qf[kk] = own_frag<D>(qrow, there, kk, a.head_dim, lane);
+  for (int kk = 0; kk < DP / 16; ++kk) {
+    qf[kk] = own_frag<D>(qrow, there, kk, a.head_dim, lane);
+#pragma unroll
+    for (int i = 0; i < Elem<D>::kSize / 2; ++i) {
+      qf[kk].v[i].x ^= flip;
+      qf[kk].v[i].y ^= flip;
+      qf[kk].v[i].z ^= flip;
+      qf[kk].v[i].w ^= flip;
+    }
+  }
+  // (a scale of 0 becomes tiny: a key past the end must still score -infinity)
+  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
 
-  const float c = a.scale * kLog2e;
+  Loader lk, lv;
+  lk.init(k.row, a.head_dim, wave, lane);
+  lv.init(v.row, a.head_dim, wave, lane);
+  const uint32_t lds = lds_offset(s_kv);
+  const int tiles = (nk + KEYS - 1) / KEYS;
+  const auto load_k = [&](int t) { lk.load(kp + (int64_t)t * KEYS * k.row, nk - t * KEYS, lds + (t % S) * kTile, wave, lane); };
+  const auto load_v = [&](int t) { lv.load(vp + (int64_t)t * KEYS * v.row, nk - t * KEYS, lds + (S + t % S) * kTile, wave, lane); };
+  const auto scores = [&](int t, f32x16_t (&s)[KB]) {
+    const unsigned char* tk = s_kv + (t % S) * kTile;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      s[kb] = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) s[kb] = mma<D>(row_frag<D, DP>(tk, kb * 32, kk, lane), qf[kk], s[kb]);
+    }
+  };
+  const auto cut = [&](int t, f32x16_t (&s)[KB]) {  // keys past the end
+    if ((t + 1) * KEYS <= nk) return;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[kb][i] = -INFINITY;
+  };
   f32x16_t acc[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) acc[db] = zero16();
-  float m = -INFINITY, l = 0.f;  // m: the running maximum of c * score; l: this lane half's sum
+  const auto product = [&](int t, const Frag<D> (&p)[2 * KB]) {
+    const unsigned char* tv = s_kv + (S + t % S) * kTile;
+#pragma unroll
+    for (int st = 0; st < 2 * KB; ++st)
+#pragma unroll
+      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(column_frag<D, DP>(tv, st * 16, db, lane), p[st], acc[db]);
+  };
 
-  for (int key = 0; key < nk; key += kFwdKeys) {
-    __syncthreads();
-    stage_rows<D, DP, kFwdKeys, kFwdWaves * 64>(s_k, k, kmap, key, nk, a.head_dim);
-    stage_rows<D, DP, kFwdKeys, kFwdWaves * 64>(s_v, v, kmap, key, nk, a.head_dim);
-    __syncthreads();
-    f32x16_t s[2] = {zero16(), zero16()};
+  RowState state;
+  if (tiles > 0) {
+    // Step t reads k of tile t + 1 and v of tile t - 1 and starts the loads of k of tile t + S and
+    // v of tile t + S - 2, whose slots step t - 1 read last.
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int t = 0; t < S; ++t) load_k(t);
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) s[kb] = mma<D>(row_frag<D, DP>(s_k, kb * 32, kk, lane), qf[kk], s[kb]);
-    float top = -INFINITY;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int j = key + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-        s[kb][i] = j < nk ? s[kb][i] * c : -INFINITY;
-        top = fmaxf(top, s[kb][i]);
-      }
-    const float m_new = fmaxf(m, fmaxf(top, other_half(top)));
-    // (scores that are all -infinity so far: the difference below must not become NaN)
-    const float base = m_new == -INFINITY ? 0.f : m_new;
-    const float shrink = exp2_fast(m - base);
-    m = m_new;
-    l *= shrink;
-#pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[db][i] *= shrink;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kb][i] = exp2_fast(s[kb][i] - base);
-        l += s[kb][i];
-      }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const Frag<D> p = to_frag<D>(s[kb], st);
+    for (int t = 0; t < S - 2; ++t) load_v(t);
+    wait_vmcnt<(2 * S - 3) * Loader::N>();
+    barrier_no_fence();
+    f32x16_t s[KB];
+    Frag<D> p[2 * KB];
+    scores(0, s);
+    for (int t = 0; t < tiles; ++t) {
+      wait_lgkmcnt0();  // this wave's reads of the slots that are about to be loaded have returned
+      // the loads of steps t - S + 2 .. t - 1 may be in flight (at the start: of the prologue)
+      if (t == 0) wait_vmcnt<(2 * S - 4) * Loader::N>();
+      else wait_vmcnt<(S - 2) * 2 * Loader::N>();
+      barrier_no_fence();
+      load_k(t + S);
+      load_v(t + S - 2);
+      cut(t, s);
+      f32x16_t next[KB];
+      scores(t + 1, next);
+      float shrink;
+      const bool moves = softmax_tile<KB>(s, c, state, &shrink);
+      if (t > 0) product(t - 1, p);
+      if (moves) {
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db)
-          acc[db] = mma<D>(column_frag<D, DP>(s_v, kb * 32 + st * 16, db, lane), p, acc[db]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[db][i] *= shrink;
       }
+#pragma unroll
+      for (int st = 0; st < 2 * KB; ++st) p[st] = to_frag<D>(s[st / 2], st % 2);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) s[kb] = next[kb];
+    }
+    wait_lgkmcnt0();
+    wait_vmcnt<0>();
+    barrier_no_fence();
+    product(tiles - 1, p);
   }
-  l += other_half(l);
+  const float sum = half_sum(state.sum);
   if (!there) return;
-  store_row<D, DP>(qmap.at<D>(out, row), acc, nk > 0 ? 1.f / l : 0.f, a.head_dim, lane);
-  if (a.lse != nullptr && lane < 32) a.lse[qmap.stat(row, a.heads)] = nk > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+  store_row<D, DP>(qmap.at<D>(out, row), acc, tiles > 0 ? 1.f / sum : 0.f, a.head_dim, lane);
+  if (a.lse != nullptr && lane < 32)
+    a.lse[qmap.stat(row, a.heads)] = tiles > 0 ? (state.base + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <DT D, int DP>
 hipError_t launch(const FwdArgs& a, hipStream_t stream) {
+  constexpr int W = D == DT::F32 ? 4 : 8, KEYS = D == DT::F32 ? 32 : 64, S = 3;
   const int group = a.heads / a.kv_heads;
-  const int64_t slots = a.nq * group / kFwdRows + a.items;
-  attention_forward_kernel<D, DP><<<dim3((unsigned)slots, (unsigned)a.kv_heads), kFwdWaves * 64, 0, stream>>>(a);
+  const int64_t slots = a.nq * group / (32 * W) + a.items;
+  attention_forward_kernel<D, DP, W, KEYS, S><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 

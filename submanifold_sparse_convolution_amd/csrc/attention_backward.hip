@@ -101,11 +101,11 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a)
     d = dot_frag<D>(gf[kk], own_frag<D>(orow, there, kk, a.head_dim, lane), d);
     if constexpr (D == DT::F16) peak = fmaxf(peak, absmax_frag<D>(gf[kk]));
   }
-  d += other_half(d);
+  d = half_sum(d);
   if (there && lane < 32) a.delta[qmap.stat(row, a.heads)] = d;
   float unit = 1.f;
   if constexpr (D == DT::F16) {
-    peak = fmaxf(peak, other_half(peak));
+    peak = half_max(peak);
     unit = unit_scale(peak);
 #pragma unroll
     for (int mk = 16; mk >= 1; mk >>= 1) peak = fmaxf(peak, __shfl_xor(peak, mk, 64));
