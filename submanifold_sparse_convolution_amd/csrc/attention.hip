@@ -25,6 +25,20 @@ struct FwdArgs {
   float scale;
 };
 
+// (fmaxf would first quiet every operand)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// Keeps the values computed here: the compiler would sink them past the next branch, away from the
+// matrix products that they overlap with.
+template <DT D> __device__ __forceinline__ void pin(Frag<D>& f) {
+#pragma unroll
+  for (int i = 0; i < Elem<D>::kSize / 2; ++i) asm volatile("" : "+v"(f.v[i].x), "+v"(f.v[i].y), "+v"(f.v[i].z), "+v"(f.v[i].w));
+}
+
 constexpr float kNone = -1.7e38f;  // a running maximum before any score (finite: differences stay numbers)
 constexpr float kSlack = 8.f;      // a new maximum up to 2^8 above the base leaves the base
 
@@ -41,14 +55,15 @@ struct RowState {
 // whether any row of the wave does shrink.
 template <int KB>
 __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowState& st, float* shrink) {
-  float top = fmaxf(s[0][0], s[0][1]);
+  float top = s[0][0];
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-    for (int i = kb == 0 ? 2 : 0; i < 16; i += 2) top = fmaxf(top, fmaxf(s[kb][i], s[kb][i + 1]));
+    for (int i = 0; i < 16; i += 2) top = max3(top, s[kb][i], s[kb][i + 1]);
   top = half_max(top) * c;
   const bool moves = __builtin_amdgcn_ballot_w64(top > st.base + kSlack) != 0;
-  const float base = moves ? fmaxf(st.base, top) : st.base;
+  // (a scalar gate instead of a branch, which would part the matrix products from the exponentials)
+  const float base = fmaxf(st.base, top + (moves ? 0.f : -INFINITY));
   *shrink = exp2_fast(st.base - base);
   st.base = base;
   float sum = 0.f;
@@ -112,79 +127,97 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
   lk.init(k.row, a.head_dim, wave, lane);
   lv.init(v.row, a.head_dim, wave, lane);
   const uint32_t lds = lds_offset(s_kv);
+  const TileReader<D, DP> rd(lane, lds, lds + S * kTile);
   const int tiles = (nk + KEYS - 1) / KEYS;
-  const auto load_k = [&](int t) { lk.load(kp + (int64_t)t * KEYS * k.row, nk - t * KEYS, lds + (t % S) * kTile, wave, lane); };
-  const auto load_v = [&](int t) { lv.load(vp + (int64_t)t * KEYS * v.row, nk - t * KEYS, lds + (S + t % S) * kTile, wave, lane); };
-  const auto scores = [&](int t, f32x16_t (&s)[KB]) {
-    const unsigned char* tk = s_kv + (t % S) * kTile;
+  // (t and slot apart: inside the loop the slot is a constant)
+  const auto load_k = [&](int t, int slot) { lk.load(kp + (int64_t)t * KEYS * k.row, nk - t * KEYS, lds + slot * kTile, wave, lane); };
+  const auto load_v = [&](int t, int slot) {
+    lv.load(vp + (int64_t)t * KEYS * v.row, t < 0 ? 0 : nk - t * KEYS, lds + (S + slot) * kTile, wave, lane);
+  };
+  const auto scores = [&](int slot, f32x16_t (&s)[KB]) {
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       s[kb] = zero16();
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) s[kb] = mma<D>(row_frag<D, DP>(tk, kb * 32, kk, lane), qf[kk], s[kb]);
+      for (int kk = 0; kk < DP / 16; ++kk) s[kb] = mma<D>(rd.row_frag(slot * kTile, kb * 32, kk), qf[kk], s[kb]);
     }
-  };
-  const auto cut = [&](int t, f32x16_t (&s)[KB]) {  // keys past the end
-    if ((t + 1) * KEYS <= nk) return;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[kb][i] = -INFINITY;
   };
   f32x16_t acc[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) acc[db] = zero16();
-  const auto product = [&](int t, const Frag<D> (&p)[2 * KB]) {
-    const unsigned char* tv = s_kv + (S + t % S) * kTile;
+  const auto product = [&](int slot, const Frag<D> (&p)[2 * KB]) {
 #pragma unroll
     for (int st = 0; st < 2 * KB; ++st)
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(column_frag<D, DP>(tv, st * 16, db, lane), p[st], acc[db]);
+      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), p[st], acc[db]);
   };
 
   RowState state;
   if (tiles > 0) {
     // Step t reads k of tile t + 1 and v of tile t - 1 and starts the loads of k of tile t + S and
-    // v of tile t + S - 2, whose slots step t - 1 read last.
+    // v of tile t + S - 2, whose slots step t - 1 read last; so S - 2 steps' loads stay in flight
+    // across its barrier.  v of tile -1 is zeros.
+    load_k(0, 0);
 #pragma unroll
-    for (int t = 0; t < S; ++t) load_k(t);
-#pragma unroll
-    for (int t = 0; t < S - 2; ++t) load_v(t);
-    wait_vmcnt<(2 * S - 3) * Loader::N>();
+    for (int t = 1; t < S; ++t) {
+      load_k(t, t);
+      load_v(t - 2, (t - 2 + S) % S);
+    }
+    wait_vmcnt<(2 * S - 2) * Loader::N>();
     barrier_no_fence();
-    f32x16_t s[KB];
+    f32x16_t s0[KB], s1[KB];
     Frag<D> p[2 * KB];
-    scores(0, s);
-    for (int t = 0; t < tiles; ++t) {
+#pragma unroll
+    for (int st = 0; st < 2 * KB; ++st)
+#pragma unroll
+      for (int i = 0; i < Elem<D>::kSize / 2; ++i) p[st].v[i] = make_uint4(0, 0, 0, 0);
+    scores(0, s0);
+    const auto step = [&](int t, int slot, f32x16_t (&s)[KB], f32x16_t (&next)[KB]) {
       wait_lgkmcnt0();  // this wave's reads of the slots that are about to be loaded have returned
-      // the loads of steps t - S + 2 .. t - 1 may be in flight (at the start: of the prologue)
-      if (t == 0) wait_vmcnt<(2 * S - 4) * Loader::N>();
-      else wait_vmcnt<(S - 2) * 2 * Loader::N>();
+      wait_vmcnt<(S - 2) * 2 * Loader::N>();
       barrier_no_fence();
-      load_k(t + S);
-      load_v(t + S - 2);
-      cut(t, s);
-      f32x16_t next[KB];
-      scores(t + 1, next);
+      load_k(t + S, slot);
+      load_v(t + S - 2, (slot + S - 2) % S);
+      if ((t + 1) * KEYS > nk) {  // keys past the end
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[kb][i] = -INFINITY;
+      }
+      scores((slot + 1) % S, next);
       float shrink;
       const bool moves = softmax_tile<KB>(s, c, state, &shrink);
-      if (t > 0) product(t - 1, p);
+      product((slot + S - 1) % S, p);
+#pragma unroll
+      for (int st = 0; st < 2 * KB; ++st) {
+        p[st] = to_frag<D>(s[st / 2], st % 2);
+        pin<D>(p[st]);
+      }
       if (moves) {
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[db][i] *= shrink;
       }
-#pragma unroll
-      for (int st = 0; st < 2 * KB; ++st) p[st] = to_frag<D>(s[st / 2], st % 2);
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb] = next[kb];
+    };
+    static_assert(S == 2 || S == 4, "the scores alternate between two sets of registers");
+    for (int t = 0;;) {
+      step(t, 0, s0, s1);
+      if (++t == tiles) break;
+      step(t, 1, s1, s0);
+      if (++t == tiles) break;
+      if constexpr (S == 4) {
+        step(t, 2, s0, s1);
+        if (++t == tiles) break;
+        step(t, 3, s1, s0);
+        if (++t == tiles) break;
+      }
     }
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
-    product(tiles - 1, p);
+    product((tiles - 1) % S, p);
   }
   const float sum = half_sum(state.sum);
   if (!there) return;
@@ -195,7 +228,7 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
 
 template <DT D, int DP>
 hipError_t launch(const FwdArgs& a, hipStream_t stream) {
-  constexpr int W = D == DT::F32 ? 4 : 8, KEYS = D == DT::F32 ? 32 : 64, S = 3;
+  constexpr int W = D == DT::F32 ? 4 : 8, KEYS = D == DT::F32 ? 32 : 64, S = D == DT::F32 && DP == 128 ? 2 : 4;
   const int group = a.heads / a.kv_heads;
   const int64_t slots = a.nq * group / (32 * W) + a.items;
   attention_forward_kernel<D, DP, W, KEYS, S><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);

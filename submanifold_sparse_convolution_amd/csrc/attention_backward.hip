@@ -118,6 +118,8 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a)
     }
   }
   const float c = a.scale * kLog2e;
+  const TileReader<D, DP> rd(lane, lds_offset(s_k), lds_offset(s_k));
+  const int to_v = (int)(lds_offset(s_v) - lds_offset(s_k));
   // log2 of the row's normaliser, less the power of two that e is scaled by
   const float base = there ? a.lse[qmap.stat(row, a.heads)] * kLog2e : 0.f;
   f32x16_t acc[DP / 32];
@@ -131,8 +133,8 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a)
     f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-      s = mma<D>(row_frag<D, DP>(s_k, 0, kk, lane), qf[kk], s);
-      dp = mma<D>(row_frag<D, DP>(s_v, 0, kk, lane), gf[kk], dp);
+      s = mma<D>(rd.row_frag(0, 0, kk), qf[kk], s);
+      dp = mma<D>(rd.row_frag(to_v, 0, kk), gf[kk], dp);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -144,7 +146,7 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a)
     for (int st = 0; st < 2; ++st) {
       const Frag<D> e = to_frag<D>(s, st);
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(column_frag<D, DP>(s_k, st * 16, db, lane), e, acc[db]);
+      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(rd.column_frag(0, st * 16, db), e, acc[db]);
     }
   }
   if (there) store_row<D, DP>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
@@ -198,6 +200,8 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dkv_kernel(BwdArgs a
     vf[kk] = own_frag<D>(vrow, there, kk, a.head_dim, lane);
   }
   const float c = a.scale * kLog2e;
+  const TileReader<D, DP> rd(lane, lds_offset(s_q), lds_offset(s_q));
+  const int to_g = (int)(lds_offset(s_g) - lds_offset(s_q));
   f32x16_t dk[DP / 32], dv[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) dk[db] = dv[db] = zero16();
@@ -215,8 +219,8 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dkv_kernel(BwdArgs a
     f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-      s = mma<D>(row_frag<D, DP>(s_q, 0, kk, lane), kf[kk], s);
-      dp = mma<D>(row_frag<D, DP>(s_g, 0, kk, lane), vf[kk], dp);
+      s = mma<D>(rd.row_frag(0, 0, kk), kf[kk], s);
+      dp = mma<D>(rd.row_frag(to_g, 0, kk), vf[kk], dp);
     }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -235,8 +239,8 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dkv_kernel(BwdArgs a
       const Frag<D> p = to_frag<D>(s, st), e = to_frag<D>(dp, st);
 #pragma unroll
       for (int db = 0; db < DP / 32; ++db) {
-        dv[db] = mma<D>(column_frag<D, DP>(s_g, st * 16, db, lane), p, dv[db]);
-        dk[db] = mma<D>(column_frag<D, DP>(s_q, st * 16, db, lane), e, dk[db]);
+        dv[db] = mma<D>(rd.column_frag(to_g, st * 16, db), p, dv[db]);
+        dk[db] = mma<D>(rd.column_frag(0, st * 16, db), e, dk[db]);
       }
     }
   }

@@ -150,54 +150,80 @@ template <DT D, int DP> __device__ __forceinline__ int swizzle(int r) {
   else return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);  // (two rows in 256 bytes)
 }
 
-// A operand of step kk (channels 16 kk .. 16 kk + 15) over tile rows r0 .. r0 + 31.
-template <DT D, int DP>
-__device__ __forceinline__ Frag<D> row_frag(const unsigned char* tile, int r0, int kk, int lane) {
-  constexpr int kPer = Elem<D>::kSize / 2;  // chunks of 8 values
-  const int r = r0 + (lane & 31);
-  Frag<D> f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int c = (kk * 2 + (lane >> 5)) * kPer + i;
-    f.v[i] = *reinterpret_cast<const uint4*>(tile + r * kRowBytes<D, DP> + ((c ^ swizzle<D, DP>(r)) << 4));
-  }
-  return f;
-}
-
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+typedef __attribute__((address_space(3))) float lds_float_t;
 
-// A operand of the transposed tile: row = channel 32 db + lane % 32, contraction over tile rows
-// r0 + 8 (j / 4) + 4 (lane / 32) + j % 4 (r0 a multiple of 16), the order of to_frag.
-template <DT D, int DP>
-__device__ __forceinline__ Frag<D> column_frag(const unsigned char* tile, int r0, int db, int lane) {
-  Frag<D> f;
-  if constexpr (D == DT::F32) {
-    const int col = db * 32 + (lane & 31);
-    float x[8];
+// A lane's LDS addresses for the two ways to read tiles: rows of tiles that start at `row_base`
+// and transposed columns of tiles that start at `col_base`, plus a constant for the tile and its
+// rows r0 (swizzles repeat every 16 rows), which goes into the instruction while it is below 64 KB.
+template <DT D, int DP> struct TileReader {
+  static constexpr int kPer = Elem<D>::kSize / 2;  // chunks of 8 values
+  uint32_t row[DP / 16 * kPer];
+  uint32_t col[D == DT::F32 ? 1 : DP / 16];
+  int lane;
+
+  uint32_t col_base;
+
+  __device__ __forceinline__ TileReader(int lane_, uint32_t row_base, uint32_t col_base_) : lane(lane_), col_base(col_base_) {
+    const int r = lane & 31;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = r0 + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
-      x[j] = *reinterpret_cast<const float*>(tile + r * kRowBytes<D, DP> + (((col >> 2) ^ swizzle<D, DP>(r)) << 4) + ((col & 3) << 2));
+    for (int i = 0; i < DP / 16 * kPer; ++i) {
+      const int c = (i / kPer * 2 + (lane >> 5)) * kPer + i % kPer;
+      row[i] = row_base + r * kRowBytes<D, DP> + ((c ^ swizzle<D, DP>(r)) << 4);
     }
-    f.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    f.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
-  } else {
-    // The transposing read: 16 lanes hand in 4 rows of 16 channels (lane t: row t / 4, channels
-    // 4 (t % 4) .. + 3) and lane t gets channel t of the 4 rows.
-    const int t = lane & 15;
-    const int col = db * 32 + ((lane >> 4) & 1) * 16 + (t & 3) * 4;
-    uint2 half[2];
+    if constexpr (D != DT::F32) {
+      const int t = lane & 15;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + 8 * i + 4 * (lane >> 5) + (t >> 2);
-      const unsigned char* p = tile + r * kRowBytes<D, DP> + (((col >> 3) ^ swizzle<D, DP>(r)) << 4) + ((col & 7) << 1);
-      half[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(uintptr_t)lds_offset(p)));
+      for (int i = 0; i < DP / 16; ++i) {
+        const int cc = i / 2 * 32 + ((lane >> 4) & 1) * 16 + (t & 3) * 4;
+        const int rr = 8 * (i % 2) + 4 * (lane >> 5) + (t >> 2);
+        col[i] = col_base + rr * kRowBytes<D, DP> + (((cc >> 3) ^ swizzle<D, DP>(rr)) << 4) + ((cc & 7) << 1);
+      }
     }
-    f.v[0] = make_uint4(half[0].x, half[0].y, half[1].x, half[1].y);
   }
-  return f;
-}
+
+  // A operand of step kk (channels 16 kk .. 16 kk + 15) over tile rows r0 .. r0 + 31.
+  __device__ __forceinline__ Frag<D> row_frag(int tile, int r0, int kk) const {
+    Frag<D> f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const u32x4_t w = *(const lds_u32x4_t*)(uintptr_t)(row[kk * kPer + i] + (tile + r0 * kRowBytes<D, DP>));
+      f.v[i] = make_uint4(w.x, w.y, w.z, w.w);
+    }
+    return f;
+  }
+
+  // A operand of the transposed tile: row = channel 32 db + lane % 32, contraction over tile rows
+  // r0 + 8 (j / 4) + 4 (lane / 32) + j % 4 (r0 a multiple of 16), the order of to_frag.
+  __device__ __forceinline__ Frag<D> column_frag(int tile, int r0, int db) const {
+    Frag<D> f;
+    if constexpr (D == DT::F32) {
+      const int c = db * 32 + (lane & 31);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+        const uint32_t at = col_base + r * kRowBytes<D, DP> + (((c >> 2) ^ swizzle<D, DP>(r)) << 4) + ((c & 3) << 2);
+        x[j] = *(const lds_float_t*)(uintptr_t)(at + (tile + r0 * kRowBytes<D, DP>));
+      }
+      f.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      f.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    } else {
+      // The transposing read: 16 lanes hand in 4 rows of 16 channels (lane t: row t / 4, channels
+      // 4 (t % 4) .. + 3) and lane t gets channel t of the 4 rows.
+      uint2 half[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        half[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                (lds_s16x4_t*)(uintptr_t)(col[db * 2 + i] + (tile + r0 * kRowBytes<D, DP>))));
+      f.v[0] = make_uint4(half[0].x, half[0].y, half[1].x, half[1].y);
+    }
+    return f;
+  }
+};
 
 // Direct global-to-LDS loads of a tile of R rows by W waves: 1 KB an instruction, kLoads<..> of
 // them a wave and tile, always that many (rows past the end and channels past head_dim read
