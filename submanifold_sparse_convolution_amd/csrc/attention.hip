@@ -78,16 +78,17 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
   return moves;
 }
 
-// Streams the keys through LDS in tiles of KEYS, S of them in flight; one step of the loop holds
+// Streams the keys through LDS in tiles of KEYS, two of k and two of v; one step of the loop holds
 // three independent pieces of work, so that the matrix cores run while the exponentials do:
 //   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
-template <DT D, int DP, int W, int KEYS, int S>
-__global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
+// (Four tiles of each in flight: the same time.)
+template <DT D, int DP, int W, int KEYS, int OCC>
+__global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs a) {
   constexpr int KB = KEYS / 32;
   constexpr int kTile = KEYS * kRowBytes<D, DP>;
   constexpr int kRows = 32 * W;
   using Loader = TileLoader<D, DP, KEYS, W>;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[2 * S * kTile];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[4 * kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads, head = blockIdx.y;
   int tile;
@@ -124,15 +125,17 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
   const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
 
   Loader lk, lv;
-  lk.init(k.row, a.head_dim, wave, lane);
-  lv.init(v.row, a.head_dim, wave, lane);
+  lk.wave = lv.wave = wave;
+  lk.lane = lv.lane = lane;
+  lk.place(k, a.head_dim, 1, 0);
+  lv.place(v, a.head_dim, 1, 0);
   const uint32_t lds = lds_offset(s_kv);
-  const TileReader<D, DP> rd(lane, lds, lds + S * kTile);
+  const TileReader<D, DP> rd(lane, lds, lds + 2 * kTile);
   const int tiles = (nk + KEYS - 1) / KEYS;
   // (t and slot apart: inside the loop the slot is a constant)
-  const auto load_k = [&](int t, int slot) { lk.load(kp + (int64_t)t * KEYS * k.row, nk - t * KEYS, lds + slot * kTile, wave, lane); };
+  const auto load_k = [&](int t, int slot) { lk.load(kp + (int64_t)t * KEYS * k.row, nk - t * KEYS, lds + slot * kTile); };
   const auto load_v = [&](int t, int slot) {
-    lv.load(vp + (int64_t)t * KEYS * v.row, t < 0 ? 0 : nk - t * KEYS, lds + (S + slot) * kTile, wave, lane);
+    lv.load(vp + (int64_t)t * KEYS * v.row, t < 0 ? 0 : nk - t * KEYS, lds + (2 + slot) * kTile);
   };
   const auto scores = [&](int slot, f32x16_t (&s)[KB]) {
 #pragma unroll
@@ -154,16 +157,12 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
 
   RowState state;
   if (tiles > 0) {
-    // Step t reads k of tile t + 1 and v of tile t - 1 and starts the loads of k of tile t + S and
-    // v of tile t + S - 2, whose slots step t - 1 read last; so S - 2 steps' loads stay in flight
-    // across its barrier.  v of tile -1 is zeros.
+    // Step t reads k of tile t + 1 and v of tile t - 1 and starts the loads of k of tile t + 2 and
+    // v of tile t, whose slots step t - 1 read last.  v of tile -1 is zeros.
     load_k(0, 0);
-#pragma unroll
-    for (int t = 1; t < S; ++t) {
-      load_k(t, t);
-      load_v(t - 2, (t - 2 + S) % S);
-    }
-    wait_vmcnt<(2 * S - 2) * Loader::N>();
+    load_k(1, 1);
+    load_v(-1, 1);
+    wait_vmcnt<2 * Loader::N>();
     barrier_no_fence();
     f32x16_t s0[KB], s1[KB];
     Frag<D> p[2 * KB];
@@ -174,10 +173,10 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
     scores(0, s0);
     const auto step = [&](int t, int slot, f32x16_t (&s)[KB], f32x16_t (&next)[KB]) {
       wait_lgkmcnt0();  // this wave's reads of the slots that are about to be loaded have returned
-      wait_vmcnt<(S - 2) * 2 * Loader::N>();
+      wait_vmcnt<0>();
       barrier_no_fence();
-      load_k(t + S, slot);
-      load_v(t + S - 2, (slot + S - 2) % S);
+      load_k(t + 2, slot);
+      load_v(t, slot);
       if ((t + 1) * KEYS > nk) {  // keys past the end
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -185,10 +184,10 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
           for (int i = 0; i < 16; ++i)
             if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[kb][i] = -INFINITY;
       }
-      scores((slot + 1) % S, next);
+      scores(slot ^ 1, next);
       float shrink;
       const bool moves = softmax_tile<KB>(s, c, state, &shrink);
-      product((slot + S - 1) % S, p);
+      product(slot ^ 1, p);
 #pragma unroll
       for (int st = 0; st < 2 * KB; ++st) {
         p[st] = to_frag<D>(s[st / 2], st % 2);
@@ -201,23 +200,16 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
           for (int i = 0; i < 16; ++i) acc[db][i] *= shrink;
       }
     };
-    static_assert(S == 2 || S == 4, "the scores alternate between two sets of registers");
     for (int t = 0;;) {
       step(t, 0, s0, s1);
       if (++t == tiles) break;
       step(t, 1, s1, s0);
       if (++t == tiles) break;
-      if constexpr (S == 4) {
-        step(t, 2, s0, s1);
-        if (++t == tiles) break;
-        step(t, 3, s1, s0);
-        if (++t == tiles) break;
-      }
     }
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
-    product((tiles - 1) % S, p);
+    product((tiles - 1) % 2, p);
   }
   const float sum = half_sum(state.sum);
   if (!there) return;
@@ -228,10 +220,13 @@ __global__ __launch_bounds__(W * 64) void attention_forward_kernel(FwdArgs a) {
 
 template <DT D, int DP>
 hipError_t launch(const FwdArgs& a, hipStream_t stream) {
-  constexpr int W = D == DT::F32 ? 4 : 8, KEYS = D == DT::F32 ? 32 : 64, S = D == DT::F32 && DP == 128 ? 2 : 4;
+  // 128 channels: 8 waves on one tile stream halve what each row reads of it (24,576 tokens, 16
+  // heads: 2.33 ms, 4 waves 2.80).  64 channels: 4 waves and three workgroups a compute unit, whose
+  // exponentials, the bound there, overlap (9,371 rows, 12 heads: 47.9 us, 8 waves 66.7).
+  constexpr int W = D != DT::F32 && DP == 128 ? 8 : 4, KEYS = D == DT::F32 ? 32 : 64, OCC = D != DT::F32 && DP == 64 ? 3 : 1;
   const int group = a.heads / a.kv_heads;
   const int64_t slots = a.nq * group / (32 * W) + a.items;
-  attention_forward_kernel<D, DP, W, KEYS, S><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
+  attention_forward_kernel<D, DP, W, KEYS, OCC><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -273,6 +268,9 @@ Status check_heads(const subm_heads_t* t, int64_t rows, int heads, const Attenti
   const int64_t limit = (int64_t(1) << 22) / size;
   if (t->row_stride < 0 || t->head_stride < 0 || t->row_stride > limit || t->head_stride > limit)
     return make_status(SUBM_ERR_UNSUPPORTED, name + ": strides must be 0 .. 2^22 bytes");
+  // (a tile of 32 rows is addressed with 31 bits from its first token)
+  if (t->head_stride * size * (heads / std::max(s.kv_heads, 1)) > (int64_t(1) << 30))
+    return make_status(SUBM_ERR_UNSUPPORTED, name + ": the heads of one key head span more than 2^30 bytes");
   if (written && ((rows > 1 && t->row_stride == 0) || (heads > 1 && t->head_stride == 0)))
     return make_status(SUBM_ERR_INVALID_ARG, name + " is written and must not overlap itself");
   return Status{};

@@ -22,7 +22,7 @@ namespace {
 struct BwdArgs {
   subm_heads_t dout, q, k, v, out, dq, dk, dv;
   const float* lse;
-  float* delta;     // [nq, heads]: d
+  float *norm, *delta;  // [kv_heads, nq * group]: log2 of each packed row's normaliser (less kF16Shift), and d
   float* peak;      // [kv_heads, slots]: the largest |dout| of each query block (float16 only)
   const int64_t *q_offsets, *k_offsets;
   int64_t nq, nk, q_slots;
@@ -30,9 +30,11 @@ struct BwdArgs {
   float scale;
 };
 
-constexpr int kBwdWaves = 4;
-constexpr int kOwn = 32 * kBwdWaves;  // own rows of a workgroup (query rows or keys), 32 a wave
-constexpr int kStep = 32;             // rows of the walked tile
+// Waves of a workgroup, 32 own rows (query rows or keys) each: 8 share a tile stream at 128
+// channels, where two waves a SIMD are all that fit; 4 at 64 channels, three workgroups a compute unit.
+template <DT D, int DP> constexpr int kWaves = D != DT::F32 && DP == 128 ? 8 : 4;
+template <DT D, int DP> constexpr int kResident = D != DT::F32 && DP == 64 ? 3 : 1;  // waves a SIMD asked for
+constexpr int kStep = 32;  // rows of the walked tile
 
 constexpr float kF16Shift = 15.f;  // p is scaled by 2^15 in float16 products
 
@@ -67,26 +69,32 @@ template <DT D> __device__ __forceinline__ float dot_frag(const Frag<D>& a, cons
   return s;
 }
 
-// d of the own query rows, then dq over the keys.
-template <DT D, int DP>
-__global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char s_k[kStep * kRowBytes<D, DP>];
-  __shared__ __attribute__((aligned(16))) unsigned char s_v[kStep * kRowBytes<D, DP>];
-  __shared__ float s_peak[kBwdWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// d of the own query rows, then dq over the keys, which stream through LDS in tiles of 32.  As in
+// the forward pass a step holds independent pieces of work:
+//   scores and dp of tile t + 1 (k, v),  e of tile t,  product of tile t - 1 (k).
+template <DT D, int DP, int W, int OCC>
+__global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
+  constexpr int kRows = 32 * W;
+  constexpr int kTile = kStep * kRowBytes<D, DP>;
+  using Loader = TileLoader<D, DP, kStep, W>;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[6 * kTile];  // four tiles of k, two of v
+  __shared__ float s_peak[W];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads, head = blockIdx.y;
   int tile;
-  const int item = find_item(a.q_offsets, a.nq, a.items, group, kOwn, blockIdx.x, &tile);
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, blockIdx.x, &tile);
   int64_t q0, k0;
   int nq, nk;
   item_rows(a.q_offsets, a.nq, item, &q0, &nq);
   item_rows(a.k_offsets, a.nk, item, &k0, &nk);
   const int rows = nq * group;
-  if ((int64_t)tile * kOwn >= rows) return;
-  const RowMap qmap{q0, head * group, group}, kmap{k0, head, 1};
+  if ((int64_t)tile * kRows >= rows) return;
+  const RowMap qmap{q0, head * group, group};
   const Heads<D> k = heads_of<D>(a.k), v = heads_of<D>(a.v);
+  const typename Elem<D>::T* kp = k.data + k0 * k.row + (int64_t)head * k.head;
+  const typename Elem<D>::T* vp = v.data + k0 * v.row + (int64_t)head * v.head;
 
-  const int row = tile * kOwn + wave * 32 + (lane & 31);
+  const int row = tile * kRows + wave * 32 + (lane & 31);
   const bool there = row < rows;
   const int safe = there ? row : 0;
   Frag<D> qf[DP / 16], gf[DP / 16];  // own rows of q and dout
@@ -102,7 +110,12 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a)
     if constexpr (D == DT::F16) peak = fmaxf(peak, absmax_frag<D>(gf[kk]));
   }
   d = half_sum(d);
-  if (there && lane < 32) a.delta[qmap.stat(row, a.heads)] = d;
+  const float base = there ? a.lse[qmap.stat(row, a.heads)] * kLog2e : 0.f;  // log2 of the row's normaliser
+  if (there && lane < 32) {
+    const int64_t at = head * (a.nq * group) + q0 * group + row;
+    a.norm[at] = D == DT::F16 ? base - kF16Shift : base;
+    a.delta[at] = d;
+  }
   float unit = 1.f;
   if constexpr (D == DT::F16) {
     peak = half_max(peak);
@@ -113,137 +126,238 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dq_kernel(BwdArgs a)
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-      for (int w = 1; w < kBwdWaves; ++w) peak = fmaxf(peak, s_peak[w]);
+      for (int w = 0; w < W; ++w) peak = fmaxf(peak, s_peak[w]);
       a.peak[head * a.q_slots + blockIdx.x] = peak;
     }
   }
   const float c = a.scale * kLog2e;
-  const TileReader<D, DP> rd(lane, lds_offset(s_k), lds_offset(s_k));
-  const int to_v = (int)(lds_offset(s_v) - lds_offset(s_k));
-  // log2 of the row's normaliser, less the power of two that e is scaled by
-  const float base = there ? a.lse[qmap.stat(row, a.heads)] * kLog2e : 0.f;
+
+  Loader lk, lv;
+  lk.wave = lv.wave = wave;
+  lk.lane = lv.lane = lane;
+  lk.place(k, a.head_dim, 1, 0);
+  lv.place(v, a.head_dim, 1, 0);
+  const uint32_t lds = lds_offset(s_kv);
+  const TileReader<D, DP> rd(lane, lds, lds);
+  const int tiles = (nk + kStep - 1) / kStep;
+  const auto load_k = [&](int t, int slot) {
+    lk.load(kp + (int64_t)t * kStep * k.row, t < 0 ? 0 : nk - t * kStep, lds + slot * kTile);
+  };
+  const auto load_v = [&](int t, int slot) { lv.load(vp + (int64_t)t * kStep * v.row, nk - t * kStep, lds + (4 + slot) * kTile); };
+  const auto scores = [&](int slot, f32x16_t& s, f32x16_t& dp) {
+    s = zero16();
+    dp = zero16();
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      s = mma<D>(rd.row_frag(slot * kTile, 0, kk), qf[kk], s);
+      dp = mma<D>(rd.row_frag((4 + slot % 2) * kTile, 0, kk), gf[kk], dp);
+    }
+  };
   f32x16_t acc[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) acc[db] = zero16();
-  for (int key = 0; key < nk; key += kStep) {
-    __syncthreads();
-    stage_rows<D, DP, kStep, kBwdWaves * 64>(s_k, k, kmap, key, nk, a.head_dim);
-    stage_rows<D, DP, kStep, kBwdWaves * 64>(s_v, v, kmap, key, nk, a.head_dim);
-    __syncthreads();
-    f32x16_t s = zero16(), dp = zero16();
+  const auto product = [&](int slot, const Frag<D> (&e)[2]) {
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
-      s = mma<D>(rd.row_frag(0, 0, kk), qf[kk], s);
-      dp = mma<D>(rd.row_frag(to_v, 0, kk), gf[kk], dp);
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), e[st], acc[db]);
+  };
+  if (tiles > 0) {
+    // Step t reads k and v of tile t + 1 and k of tile t - 1 and starts the loads of tile t + 2.
+    load_k(0, 0);
+    load_v(0, 0);
+    load_k(-1, 3);  // (zeros)
+    load_k(1, 1);
+    load_v(1, 1);
+    wait_vmcnt<3 * Loader::N>();
+    barrier_no_fence();
+    f32x16_t s0, dp0, s1, dp1;
+    Frag<D> e[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int i = 0; i < Elem<D>::kSize / 2; ++i) e[st].v[i] = make_uint4(0, 0, 0, 0);
+    scores(0, s0, dp0);
+    const auto step = [&](int t, int slot, f32x16_t& s, f32x16_t& dp, f32x16_t& s_next, f32x16_t& dp_next) {
+      wait_lgkmcnt0();  // this wave's reads of the slots that are about to be loaded have returned
+      wait_vmcnt<0>();
+      barrier_no_fence();
+      load_k(t + 2, (slot + 2) % 4);
+      load_v(t + 2, slot % 2);
+      scores((slot + 1) % 4, s_next, dp_next);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], c, -base)) * (dp[i] - d) * unit;
+      if ((t + 1) * kStep > nk) {  // (a key past the end scores 0, which p need not take to 0)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (t * kStep + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[i] = 0.f;
+      }
+      product((slot + 3) % 4, e);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) e[st] = to_frag<D>(s, st);
+    };
+    for (int t = 0;;) {
+      step(t, 0, s0, dp0, s1, dp1);
+      if (++t == tiles) break;
+      step(t, 1, s1, dp1, s0, dp0);
+      if (++t == tiles) break;
+      step(t, 2, s0, dp0, s1, dp1);
+      if (++t == tiles) break;
+      step(t, 3, s1, dp1, s0, dp0);
+      if (++t == tiles) break;
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int j = key + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-      const float e = exp2_fast(fmaf(s[i], c, -base)) * (dp[i] - d) * unit;
-      s[i] = j < nk ? e : 0.f;  // (a key past the end scores 0, which p need not take to 0)
-    }
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const Frag<D> e = to_frag<D>(s, st);
-#pragma unroll
-      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(rd.column_frag(0, st * 16, db), e, acc[db]);
-    }
+    wait_lgkmcnt0();
+    wait_vmcnt<0>();
+    product((tiles - 1) % 4, e);
   }
   if (there) store_row<D, DP>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
 }
 
-// dk and dv of the own keys, over the query rows of all heads that share the key head.
-template <DT D, int DP>
-__global__ __launch_bounds__(kBwdWaves * 64) void attention_dkv_kernel(BwdArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char s_q[kStep * kRowBytes<D, DP>];
-  __shared__ __attribute__((aligned(16))) unsigned char s_g[kStep * kRowBytes<D, DP>];
-  __shared__ __attribute__((aligned(16))) float s_lse[kStep], s_delta[kStep];
-  __shared__ float s_peak[kBwdWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The next 32 of `left` floats (zeros past them) straight to LDS, which takes 64 of them.
+__device__ __forceinline__ void load_stats(const float* p, int left, uint32_t lds, int lane) {
+  const i32x4_t rsrc = make_rsrc(p, kOutOfRange);
+  const uint32_t at = lane < 32 && lane < left ? lane * 4u : kOutOfRange;
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %0, %1, 0 offen lds"
+      :
+      : "v"(at), "s"(rsrc), "s"(lds));
+}
+
+// dk and dv of the own keys, over the query rows of all heads that share the key head, which
+// stream through LDS in tiles of 32.  Two waves a SIMD overlap each other's exponentials and
+// products.  At 128 channels in 16 bits the own rows of v stay in LDS: with the two accumulators
+// and k there is no room for them in 256 registers.
+template <DT D, int DP, int W, int OCC>
+__global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
+  constexpr int kKeys = 32 * W, kRows = 32 * kWaves<D, DP>;
+  constexpr int kTile = kStep * kRowBytes<D, DP>;
+  constexpr bool kParked = D != DT::F32 && DP == 128;
+  using Loader = TileLoader<D, DP, kStep, W>;
+  using Parker = TileLoader<D, DP, kKeys, W>;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_qg[4 * kTile + (kParked ? W * kTile : 0)];  // q, q, dout, dout, own v
+  __shared__ __attribute__((aligned(16))) float s_stat[2 * 2 * 64];  // norm and d of two tiles
+  __shared__ float s_peak[W];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads, head = blockIdx.y;
   int tile;
-  const int item = find_item(a.k_offsets, a.nk, a.items, 1, kOwn, blockIdx.x, &tile);
+  const int item = find_item(a.k_offsets, a.nk, a.items, 1, kKeys, blockIdx.x, &tile);
   int64_t q0, k0;
   int nq, nk;
   item_rows(a.q_offsets, a.nq, item, &q0, &nq);
   item_rows(a.k_offsets, a.nk, item, &k0, &nk);
   const int rows = nq * group;
-  if ((int64_t)tile * kOwn >= nk) return;
-  const RowMap qmap{q0, head * group, group}, kmap{k0, head, 1};
-  const Heads<D> q = heads_of<D>(a.q), g = heads_of<D>(a.dout);
+  if ((int64_t)tile * kKeys >= nk) return;
+  const RowMap kmap{k0, head, 1};
+  const Heads<D> q = heads_of<D>(a.q), g = heads_of<D>(a.dout), v = heads_of<D>(a.v);
+  const typename Elem<D>::T* qp = q.data + q0 * q.row + (int64_t)head * group * q.head;
+  const typename Elem<D>::T* gp = g.data + q0 * g.row + (int64_t)head * group * g.head;
+  const float* norm = a.norm + head * (a.nq * group) + q0 * group;
+  const float* delta = a.delta + head * (a.nq * group) + q0 * group;
 
   float unit = 1.f;
   if constexpr (D == DT::F16) {  // the largest |dout| of the item and head, from its query blocks
-    const int64_t first = q0 * group / kOwn + item;
+    const int64_t first = q0 * group / kRows + item;
     float peak = 0.f;
-    for (int t = threadIdx.x; t < (rows + kOwn - 1) / kOwn; t += kBwdWaves * 64)
+    for (int t = threadIdx.x; t < (rows + kRows - 1) / kRows; t += W * 64)
       peak = fmaxf(peak, a.peak[head * a.q_slots + first + t]);
 #pragma unroll
     for (int mk = 32; mk >= 1; mk >>= 1) peak = fmaxf(peak, __shfl_xor(peak, mk, 64));
     if (lane == 0) s_peak[wave] = peak;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kBwdWaves; ++w) peak = fmaxf(peak, s_peak[w]);
+    for (int w = 0; w < W; ++w) peak = fmaxf(peak, s_peak[w]);
     unit = unit_scale(peak);
   }
-  const float shift = D == DT::F16 ? kF16Shift : 0.f;
   const float p_unit = D == DT::F16 ? 1.f / 32768.f : 1.f;
 
-  const int key = tile * kOwn + wave * 32 + (lane & 31);
+  const uint32_t lds = lds_offset(s_qg);
+  const int key = tile * kKeys + wave * 32 + (lane & 31);
   const bool there = key < nk;
-  Frag<D> kf[DP / 16], vf[DP / 16];
+  Frag<D> kf[DP / 16], vf[kParked ? 1 : DP / 16];
   const typename Elem<D>::T* krow = kmap.at<D>(heads_of<D>(a.k), there ? key : 0);
-  const typename Elem<D>::T* vrow = kmap.at<D>(heads_of<D>(a.v), there ? key : 0);
+  const typename Elem<D>::T* vrow = kmap.at<D>(v, there ? key : 0);
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk) {
     kf[kk] = own_frag<D>(krow, there, kk, a.head_dim, lane);
-    vf[kk] = own_frag<D>(vrow, there, kk, a.head_dim, lane);
+    if constexpr (!kParked) vf[kk] = own_frag<D>(vrow, there, kk, a.head_dim, lane);
   }
+  if constexpr (kParked) {
+    Parker park;
+    park.wave = wave;
+    park.lane = lane;
+    park.place(v, a.head_dim, 1, 0);
+    park.load(kmap.at<D>(v, tile * kKeys), nk - tile * kKeys, lds + 4 * kTile);
+  }
+  Loader lq, lg;
+  lq.wave = lg.wave = wave;
+  lq.lane = lg.lane = lane;
+  lq.place(q, a.head_dim, group, 0);
+  lg.place(g, a.head_dim, group, 0);
+  const TileReader<D, DP> rd(lane, lds, lds);
+  const uint32_t own = wave * kTile;  // (this wave's rows of the parked tile)
+  const uint32_t stat = __builtin_amdgcn_readfirstlane(lds_offset(s_stat));
+  const auto load = [&](int t, int slot) {
+    const int r0 = t * kStep, tok = group == 1 ? r0 : r0 / group;
+    if (kStep % group != 0) {  // (uniform) the tile starts inside a token
+      lq.place(q, a.head_dim, group, r0 - tok * group);
+      lg.place(g, a.head_dim, group, r0 - tok * group);
+    }
+    lq.load(qp + (int64_t)tok * q.row, rows - r0, lds + slot * kTile);
+    lg.load(gp + (int64_t)tok * g.row, rows - r0, lds + (2 + slot) * kTile);
+    if (wave == 0) load_stats(norm + r0, rows - r0, stat + slot * 512, lane);
+    if (wave == 1) load_stats(delta + r0, rows - r0, stat + slot * 512 + 256, lane);
+  };
   const float c = a.scale * kLog2e;
-  const TileReader<D, DP> rd(lane, lds_offset(s_q), lds_offset(s_q));
-  const int to_g = (int)(lds_offset(s_g) - lds_offset(s_q));
   f32x16_t dk[DP / 32], dv[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) dk[db] = dv[db] = zero16();
-  for (int r0 = 0; r0 < rows; r0 += kStep) {
-    __syncthreads();
-    stage_rows<D, DP, kStep, kBwdWaves * 64>(s_q, q, qmap, r0, rows, a.head_dim);
-    stage_rows<D, DP, kStep, kBwdWaves * 64>(s_g, g, qmap, r0, rows, a.head_dim);
-    if (threadIdx.x < kStep) {
-      const int r = r0 + threadIdx.x;
-      const int64_t at = qmap.stat(r < rows ? r : 0, a.heads);
-      s_lse[threadIdx.x] = r < rows ? a.lse[at] * kLog2e - shift : INFINITY;  // p = 0 past the last row
-      s_delta[threadIdx.x] = r < rows ? a.delta[at] : 0.f;
-    }
-    __syncthreads();
+  const auto step = [&](int t, int slot) {
+    wait_lgkmcnt0();
+    wait_vmcnt<0>();
+    barrier_no_fence();
+    load(t + 1, slot ^ 1);
     f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-      s = mma<D>(rd.row_frag(0, 0, kk), kf[kk], s);
-      dp = mma<D>(rd.row_frag(to_g, 0, kk), vf[kk], dp);
+      s = mma<D>(rd.row_frag(slot * kTile, 0, kk), kf[kk], s);
+      if constexpr (kParked) dp = mma<D>(rd.row_frag((2 + slot) * kTile, 0, kk), rd.row_frag(4 * kTile + own, 0, kk), dp);
+      else dp = mma<D>(rd.row_frag((2 + slot) * kTile, 0, kk), vf[kk], dp);
     }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const float4 ls = *reinterpret_cast<const float4*>(s_lse + 8 * b + 4 * (lane >> 5));
-      const float4 dl = *reinterpret_cast<const float4*>(s_delta + 8 * b + 4 * (lane >> 5));
+      const float4 ls = *reinterpret_cast<const float4*>(s_stat + slot * 128 + 8 * b + 4 * (lane >> 5));
+      const float4 dl = *reinterpret_cast<const float4*>(s_stat + slot * 128 + 64 + 8 * b + 4 * (lane >> 5));
       const float lse4[4] = {ls.x, ls.y, ls.z, ls.w}, del4[4] = {dl.x, dl.y, dl.z, dl.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p = exp2_fast(fmaf(s[4 * b + i], c, -lse4[i]));
         s[4 * b + i] = p;
-        dp[4 * b + i] = p * (dp[4 * b + i] - del4[i]) * (unit * p_unit);
+        dp[4 * b + i] = p * (dp[4 * b + i] - del4[i]);
+        if constexpr (D == DT::F16) dp[4 * b + i] *= unit * p_unit;
       }
     }
+    // (rows past the end: q, dout, norm and d read 0, so p is 1 and meets a dout of 0, and e is 0)
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       const Frag<D> p = to_frag<D>(s, st), e = to_frag<D>(dp, st);
 #pragma unroll
       for (int db = 0; db < DP / 32; ++db) {
-        dv[db] = mma<D>(rd.column_frag(to_g, st * 16, db), p, dv[db]);
-        dk[db] = mma<D>(rd.column_frag(0, st * 16, db), e, dk[db]);
+        dv[db] = mma<D>(rd.column_frag((2 + slot) * kTile, st * 16, db), p, dv[db]);
+        dk[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), e, dk[db]);
       }
     }
+  };
+  const int steps = (rows + kStep - 1) / kStep;
+  if (steps > 0) {
+    load(0, 0);
+    for (int t = 0; t < steps; t += 2) {  // (an odd end takes a step of zeros: a second exit costs registers)
+      step(t, 0);
+      step(t + 1, 1);
+    }
   }
+  wait_vmcnt<0>();  // (the loads past the end)
   if (!there) return;
   store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, lane);
   store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, lane);
@@ -251,21 +365,28 @@ __global__ __launch_bounds__(kBwdWaves * 64) void attention_dkv_kernel(BwdArgs a
 
 template <DT D, int DP>
 hipError_t launch(const BwdArgs& a, hipStream_t stream) {
+  constexpr int W = kWaves<D, DP>;
   hipError_t e = hipSuccess;
   if (a.nq > 0) {
-    attention_dq_kernel<D, DP><<<dim3((unsigned)a.q_slots, (unsigned)a.kv_heads), kBwdWaves * 64, 0, stream>>>(a);
+    attention_dq_kernel<D, DP, W, kResident<D, DP>><<<dim3((unsigned)a.q_slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
     e = hipGetLastError();
   }
   if (e == hipSuccess && a.nk > 0) {
-    const int64_t slots = a.nk / kOwn + a.items;
-    attention_dkv_kernel<D, DP><<<dim3((unsigned)slots, (unsigned)a.kv_heads), kBwdWaves * 64, 0, stream>>>(a);
+    const int64_t slots = a.nk / (32 * W) + a.items;
+    attention_dkv_kernel<D, DP, W, D == DT::F32 ? 1 : 2><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
     e = hipGetLastError();
   }
   return e;
 }
 
-template <DT D> hipError_t launch_dim(const BwdArgs& a, hipStream_t stream) {
-  return a.head_dim <= 64 ? launch<D, 64>(a, stream) : launch<D, 128>(a, stream);
+template <DT D> hipError_t launch_dim(BwdArgs a, hipStream_t stream) {
+  const int64_t rows = a.nq * (a.heads / a.kv_heads);
+  if (a.head_dim <= 64) {
+    a.q_slots = rows / (32 * kWaves<D, 64>) + a.items;
+    return launch<D, 64>(a, stream);
+  }
+  a.q_slots = rows / (32 * kWaves<D, 128>) + a.items;
+  return launch<D, 128>(a, stream);
 }
 
 }  // namespace
@@ -294,19 +415,20 @@ extern "C" int sparse_attention_backward(const subm_heads_t* dout, const subm_he
   if (nq > 0 && lse == nullptr) return fail(SUBM_ERR_INVALID_ARG, "lse is NULL");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
   if (nq == 0 && nk == 0) return SUBM_OK;
-  BwdArgs a{*dout, *q, *k, *v, *out, *dq, *dk, *dv, lse, nullptr, nullptr, q_offsets, k_offsets, nq, nk, 0,
+  BwdArgs a{*dout, *q, *k, *v, *out, *dq, *dk, *dv, lse, nullptr, nullptr, nullptr, q_offsets, k_offsets, nq, nk, 0,
             items, heads, kv_heads, head_dim, scale};
-  a.q_slots = nq * (heads / kv_heads) / kOwn + items;
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return fail(hip_status(e, "hipGetDevice"));
-  const size_t delta_bytes = ((size_t)nq * heads * sizeof(float) + 255) / 256 * 256;
-  const size_t peak_bytes = (size_t)a.q_slots * kv_heads * sizeof(float);
+  // norm and d of every query row, and a peak for each of the smallest query blocks (128 rows)
+  const size_t stat_bytes = ((size_t)nq * heads * sizeof(float) + 255) / 256 * 256;
+  const size_t peak_bytes = (size_t)(nq * (heads / kv_heads) / 128 + items) * kv_heads * sizeof(float);
   void* scratch = nullptr;
-  st = stream_scratch(dev, stream, delta_bytes + peak_bytes, &scratch);
+  st = stream_scratch(dev, stream, 2 * stat_bytes + peak_bytes, &scratch);
   if (!st.ok()) return fail(st);
-  a.delta = static_cast<float*>(scratch);
-  a.peak = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + delta_bytes);
+  a.norm = static_cast<float*>(scratch);
+  a.delta = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + stat_bytes);
+  a.peak = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + 2 * stat_bytes);
   if (dtype == SUBM_F32) e = launch_dim<DT::F32>(a, stream);
   else if (dtype == SUBM_F16) e = launch_dim<DT::F16>(a, stream);
   else e = launch_dim<DT::BF16>(a, stream);

@@ -162,19 +162,23 @@ typedef __attribute__((address_space(3))) float lds_float_t;
 template <DT D, int DP> struct TileReader {
   static constexpr int kPer = Elem<D>::kSize / 2;  // chunks of 8 values
   uint32_t row[DP / 16 * kPer];
-  uint32_t col[D == DT::F32 ? 1 : DP / 16];
-  int lane;
+  uint32_t col[D == DT::F32 ? 16 : DP / 16];
 
-  uint32_t col_base;
-
-  __device__ __forceinline__ TileReader(int lane_, uint32_t row_base, uint32_t col_base_) : lane(lane_), col_base(col_base_) {
+  __device__ __forceinline__ TileReader(int lane, uint32_t row_base, uint32_t col_base) {
     const int r = lane & 31;
 #pragma unroll
     for (int i = 0; i < DP / 16 * kPer; ++i) {
       const int c = (i / kPer * 2 + (lane >> 5)) * kPer + i % kPer;
       row[i] = row_base + r * kRowBytes<D, DP> + ((c ^ swizzle<D, DP>(r)) << 4);
     }
-    if constexpr (D != DT::F32) {
+    if constexpr (D == DT::F32) {  // col[2 j + db % 2]: element j of channel block db
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = i >> 1, cc = (i & 1) * 32 + (lane & 31);
+        const int rr = 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+        col[i] = col_base + rr * kRowBytes<D, DP> + (((cc >> 2) ^ swizzle<D, DP>(rr)) << 4) + ((cc & 3) << 2);
+      }
+    } else {
       const int t = lane & 15;
 #pragma unroll
       for (int i = 0; i < DP / 16; ++i) {
@@ -201,14 +205,10 @@ template <DT D, int DP> struct TileReader {
   __device__ __forceinline__ Frag<D> column_frag(int tile, int r0, int db) const {
     Frag<D> f;
     if constexpr (D == DT::F32) {
-      const int c = db * 32 + (lane & 31);
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
-        const uint32_t at = col_base + r * kRowBytes<D, DP> + (((c >> 2) ^ swizzle<D, DP>(r)) << 4) + ((c & 3) << 2);
-        x[j] = *(const lds_float_t*)(uintptr_t)(at + (tile + r0 * kRowBytes<D, DP>));
-      }
+      for (int j = 0; j < 8; ++j)
+        x[j] = *(const lds_float_t*)(uintptr_t)(col[2 * j + db % 2] + (tile + r0 * kRowBytes<D, DP> + db / 2 * 256));
       f.v[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
       f.v[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
     } else {
@@ -235,48 +235,37 @@ template <DT D, int DP, int R, int W> struct TileLoader {
   static_assert(N >= 1 && N * W * 1024 == R * kRowBytes<D, DP>, "whole instructions");
   static constexpr int C = kRowChunks<D, DP>;
   static constexpr int kRowsPer = 64 / C;  // rows of an instruction
-  uint32_t offset[N];  // of this lane, from the tile's first row
-  uint32_t lds0;       // of this wave's first kilobyte, from the tile
+  uint32_t offset[N];  // of this lane, from the tile's first token
+  int wave, lane;
 
-  __device__ __forceinline__ int row(int n, int wave, int lane) const { return (n * W + wave) * kRowsPer + lane / C; }
+  __device__ __forceinline__ int row(int n) const { return (n * W + wave) * kRowsPer + lane / C; }
 
-  __device__ __forceinline__ void init(int64_t row_stride, int head_dim, int wave, int lane) {
+  // Tiles of packed rows, `group` a token, that start `rem` rows into a token; keys: group 1.
+  __device__ __forceinline__ void place(const Heads<D>& t, int head_dim, int group, int rem) {
     constexpr int size = Elem<D>::kSize;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = row(n, wave, lane);
+      const int r = row(n);
       const int c = (lane % C) ^ swizzle<D, DP>(r);
-      offset[n] = c * 16 < head_dim * size ? (uint32_t)(r * (int)row_stride * size + c * 16) : kOutOfRange;
+      const int tok = group == 1 ? r : (r + rem) / group;
+      const int h = group == 1 ? 0 : r + rem - tok * group;
+      offset[n] = c * 16 < head_dim * size ? (uint32_t)((tok * (int)t.row + h * (int)t.head) * size + c * 16) : kOutOfRange;
     }
-    lds0 = wave * 1024;
   }
-  // `left`: rows from the tile's first to the last there is (any value; <= 0 reads nothing).
-  __device__ __forceinline__ void load(const typename Elem<D>::T* tile_rows, int left, uint32_t lds, int wave, int lane) const {
-    const i32x4_t rsrc = make_rsrc(tile_rows, kOutOfRange);
+  // `first`: the tile's first token; `left`: rows from the tile's first to the last there is (any
+  // value; <= 0 reads nothing); `lds`: where the tile goes.
+  __device__ __forceinline__ void load(const typename Elem<D>::T* first, int left, uint32_t lds) const {
+    const i32x4_t rsrc = make_rsrc(first, kOutOfRange);
+    lds = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
     if (left >= R) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) lds_dma16(rsrc, offset[n], lds + lds0 + n * W * 1024);
+      for (int n = 0; n < N; ++n) lds_dma16(rsrc, offset[n], lds + n * W * 1024);
     } else {
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-        lds_dma16(rsrc, row(n, wave, lane) < left ? offset[n] : kOutOfRange, lds + lds0 + n * W * 1024);
+      for (int n = 0; n < N; ++n) lds_dma16(rsrc, row(n) < left ? offset[n] : kOutOfRange, lds + n * W * 1024);
     }
   }
 };
-
-// (the staging of the kernels that do not stream)
-template <DT D, int DP, int R, int THREADS>
-__device__ __forceinline__ void stage_rows(unsigned char* tile, const Heads<D>& t, const RowMap& map, int r0, int rows,
-                                           int head_dim) {
-  constexpr int C = kRowChunks<D, DP>;
-  constexpr int kVals = 16 / Elem<D>::kSize;
-  for (int i = threadIdx.x; i < R * C; i += THREADS) {
-    const int r = i / C, c = i % C;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r0 + r < rows && c * kVals < head_dim) v = *reinterpret_cast<const uint4*>(map.at<D>(t, r0 + r) + c * kVals);
-    *reinterpret_cast<uint4*>(tile + r * kRowBytes<D, DP> + ((c ^ swizzle<D, DP>(r)) << 4)) = v;
-  }
-}
 
 // A lane's own row as the B operand of step kk, straight from global memory.
 template <DT D>
