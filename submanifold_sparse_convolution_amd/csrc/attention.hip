@@ -23,6 +23,11 @@ struct FwdArgs {
   int64_t nq, nk;
   int items, heads, kv_heads, head_dim;
   float scale;
+  // Keys split over `splits` workgroups: each leaves the unnormalised sums of its packed rows,
+  // part [splits, kv_heads, nq * group, DP] and their (base, sum), for the joining kernel.
+  int splits;
+  float* part;
+  float2* state;
 };
 
 // (fmaxf would first quiet every operand)
@@ -82,7 +87,7 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
 // three independent pieces of work, so that the matrix cores run while the exponentials do:
 //   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
 // (Four tiles of each in flight: the same time.)
-template <DT D, int DP, int W, int KEYS, int OCC>
+template <DT D, int DP, int W, int KEYS, int OCC, bool SPLIT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs a) {
   constexpr int KB = KEYS / 32;
   constexpr int kTile = KEYS * kRowBytes<D, DP>;
@@ -131,11 +136,19 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
   lv.place(v, a.head_dim, 1, 0);
   const uint32_t lds = lds_offset(s_kv);
   const TileReader<D, DP> rd(lane, lds, lds + 2 * kTile);
-  const int tiles = (nk + KEYS - 1) / KEYS;
+  // this workgroup's keys: all, or its share of whole tiles (a share may be empty)
+  int tiles = (nk + KEYS - 1) / KEYS, left = nk;
+  if constexpr (SPLIT) {
+    const int share = (tiles + a.splits - 1) / a.splits, t0 = min(tiles, share * (int)blockIdx.z);
+    tiles = min(share, tiles - t0);
+    left = min(nk - t0 * KEYS, tiles * KEYS);
+    kp += (int64_t)t0 * KEYS * k.row;
+    vp += (int64_t)t0 * KEYS * v.row;
+  }
   // (t and slot apart: inside the loop the slot is a constant)
-  const auto load_k = [&](int t, int slot) { lk.load(kp + (int64_t)t * KEYS * k.row, nk - t * KEYS, lds + slot * kTile); };
+  const auto load_k = [&](int t, int slot) { lk.load(kp + (int64_t)t * KEYS * k.row, left - t * KEYS, lds + slot * kTile); };
   const auto load_v = [&](int t, int slot) {
-    lv.load(vp + (int64_t)t * KEYS * v.row, t < 0 ? 0 : nk - t * KEYS, lds + (2 + slot) * kTile);
+    lv.load(vp + (int64_t)t * KEYS * v.row, t < 0 ? 0 : left - t * KEYS, lds + (2 + slot) * kTile);
   };
   const auto scores = [&](int slot, f32x16_t (&s)[KB]) {
 #pragma unroll
@@ -177,12 +190,12 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
       barrier_no_fence();
       load_k(t + 2, slot);
       load_v(t, slot);
-      if ((t + 1) * KEYS > nk) {  // keys past the end
+      if ((t + 1) * KEYS > left) {  // keys past the end
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[kb][i] = -INFINITY;
+            if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= left) s[kb][i] = -INFINITY;
       }
       scores(slot ^ 1, next);
       float shrink;
@@ -213,24 +226,108 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
   }
   const float sum = half_sum(state.sum);
   if (!there) return;
+  if constexpr (SPLIT) {
+    const int64_t at = ((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row;
+    if (lane < 32) a.state[at] = make_float2(nk > 0 ? state.base : -INFINITY, sum);
+    if (tiles == 0) return;
+    float* o = a.part + at * DP;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(o + db * 32 + 8 * i + 4 * (lane >> 5)) =
+            make_float4(acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]);
+    return;
+  }
   store_row<D, DP>(qmap.at<D>(out, row), acc, tiles > 0 ? 1.f / sum : 0.f, a.head_dim, lane);
   if (a.lse != nullptr && lane < 32)
     a.lse[qmap.stat(row, a.heads)] = tiles > 0 ? (state.base + log2f(sum)) * kLn2 : -INFINITY;
 }
 
+// Joins the splits of a row: DP / 4 threads a row, four channels each.
 template <DT D, int DP>
-hipError_t launch(const FwdArgs& a, hipStream_t stream) {
-  // 128 channels: 8 waves on one tile stream halve what each row reads of it (24,576 tokens, 16
-  // heads: 2.33 ms, 4 waves 2.80).  64 channels: 4 waves and three workgroups a compute unit, whose
-  // exponentials, the bound there, overlap (9,371 rows, 12 heads: 47.9 us, 8 waves 66.7).
-  constexpr int W = D != DT::F32 && DP == 128 ? 8 : 4, KEYS = D == DT::F32 ? 32 : 64, OCC = D != DT::F32 && DP == 64 ? 3 : 1;
+__global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
+  constexpr int kThreads = DP / 4;
   const int group = a.heads / a.kv_heads;
-  const int64_t slots = a.nq * group / (32 * W) + a.items;
-  attention_forward_kernel<D, DP, W, KEYS, OCC><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
+  const int64_t rows = a.nq * group, all = rows * a.kv_heads;
+  const int64_t at = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+  if (at >= all) return;
+  const int c = threadIdx.x % kThreads * 4;
+  float base = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) base = fmaxf(base, a.state[s * all + at].x);
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 st = a.state[s * all + at];
+    if (st.y == 0.f) continue;  // (no keys in this share, or all its scores -infinity)
+    const float w = exp2_fast(st.x - base);
+    const float4 p = *reinterpret_cast<const float4*>(a.part + (s * all + at) * DP + c);
+    sum = fmaf(w, st.y, sum);
+    o.x = fmaf(w, p.x, o.x);
+    o.y = fmaf(w, p.y, o.y);
+    o.z = fmaf(w, p.z, o.z);
+    o.w = fmaf(w, p.w, o.w);
+  }
+  const bool none = base == -INFINITY;  // the item has no keys
+  const float f = none ? 0.f : 1.f / sum;
+  const int head = (int)(at / rows);
+  const int64_t r = at - head * rows, tok = r / group;
+  const int h = head * group + (int)(r - tok * group);
+  const Heads<D> out = heads_of<D>(a.out);
+  if (c < a.head_dim) store4<D>(out.data + tok * out.row + (int64_t)h * out.head + c, o.x * f, o.y * f, o.z * f, o.w * f);
+  if (a.lse != nullptr && c == 0) a.lse[tok * a.heads + h] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
+}
+
+template <DT D, int DP, int W, bool SPLIT>
+hipError_t launch_tiles(const FwdArgs& a, hipStream_t stream) {
+  constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
+  const int64_t slots = a.nq * (a.heads / a.kv_heads) / (32 * W) + a.items;
+  attention_forward_kernel<D, DP, W, KEYS, OCC, SPLIT>
+      <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.splits : 1u), W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <DT D> hipError_t launch_dim(const FwdArgs& a, hipStream_t stream) {
+template <DT D, int DP>
+Status launch(FwdArgs a, hipStream_t stream) {
+  // 128 channels: 8 waves on one tile stream halve what each row reads of it (24,576 tokens, 16
+  // heads: 2.33 ms, 4 waves 2.80), where they fill the compute units.  64 channels: 4 waves and
+  // three workgroups a compute unit, whose exponentials, the bound there, overlap (9,371 rows,
+  // 12 heads: 47.9 us, 8 waves 66.7).
+  constexpr int kUnits = 256;
+  const int64_t rows = a.nq * (a.heads / a.kv_heads);
+  if constexpr (D != DT::F32 && DP == 128) {
+    if ((rows / 256 + a.items) * a.kv_heads >= kUnits && rows / a.items >= 256) {
+      SUBM_HIP_TRY((launch_tiles<D, DP, 8, false>(a, stream)));
+      return Status{};
+    }
+  }
+  // Too few workgroups to fill the compute units: split the keys, as long as a share keeps
+  // kShare keys on average (the join costs a launch and a float32 copy of the rows a share).
+  constexpr int kShare = 512;
+  const int64_t blocks = (rows / 128 + a.items) * a.kv_heads;
+  const int64_t want = std::min<int64_t>(3 * kUnits / blocks, a.nk / a.items / kShare);
+  if (want < 2) {
+    SUBM_HIP_TRY((launch_tiles<D, DP, 4, false>(a, stream)));
+    return Status{};
+  }
+  a.splits = (int)want;
+  int dev = 0;
+  SUBM_HIP_TRY(hipGetDevice(&dev));
+  const size_t state_bytes = ((size_t)a.splits * rows * a.kv_heads * sizeof(float2) + 255) / 256 * 256;
+  void* scratch = nullptr;
+  Status st = stream_scratch(dev, stream, state_bytes + (size_t)a.splits * rows * a.kv_heads * DP * sizeof(float), &scratch);
+  if (!st.ok()) return st;
+  a.state = static_cast<float2*>(scratch);
+  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + state_bytes);
+  SUBM_HIP_TRY((launch_tiles<D, DP, 4, true>(a, stream)));
+  constexpr int kRowsPer = 256 / (DP / 4);
+  const int64_t joins = (rows * a.kv_heads + kRowsPer - 1) / kRowsPer;
+  attention_join_kernel<D, DP><<<(unsigned)joins, 256, 0, stream>>>(a);
+  SUBM_HIP_TRY(hipGetLastError());
+  return Status{};
+}
+
+template <DT D> Status launch_dim(const FwdArgs& a, hipStream_t stream) {
   return a.head_dim <= 64 ? launch<D, 64>(a, stream) : launch<D, 128>(a, stream);
 }
 
@@ -294,11 +391,10 @@ extern "C" int sparse_attention_forward(const subm_heads_t* q, const subm_heads_
   if (!st.ok()) return fail(st);
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
   if (nq == 0) return SUBM_OK;
-  const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads, head_dim, scale};
-  hipError_t e;
-  if (dtype == SUBM_F32) e = launch_dim<DT::F32>(a, stream);
-  else if (dtype == SUBM_F16) e = launch_dim<DT::F16>(a, stream);
-  else e = launch_dim<DT::BF16>(a, stream);
-  if (e != hipSuccess) return fail(hip_status(e, "sparse_attention_forward launch"));
+  const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads, head_dim, scale, 1, nullptr, nullptr};
+  if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
+  else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
+  else st = launch_dim<DT::BF16>(a, stream);
+  if (!st.ok()) return fail(st);
   return SUBM_OK;
 }
