@@ -305,7 +305,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   // kShare keys on average (the join costs a launch and a float32 copy of the rows a share).
   constexpr int kShare = 512;
   const int64_t blocks = (rows / 128 + a.items) * a.kv_heads;
-  const int64_t want = std::min<int64_t>(3 * kUnits / blocks, a.nk / a.items / kShare);
+  const int64_t want = std::min<int64_t>(2 * kUnits / blocks, a.nk / a.items / kShare);
   if (want < 2) {
     SUBM_HIP_TRY((launch_tiles<D, DP, 4, false>(a, stream)));
     return Status{};

@@ -21,10 +21,21 @@ namespace {
 
 // TPR lanes (a wave, or a workgroup of TPR threads) hold one row, ITEMS chunks of V values each.
 
+template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over a wave, the same in every lane, in VALU instructions alone (an LDS permutation a step
+// would cost a row some 12 LDS round trips in the backward pass).
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  v = dpp_add<0xB1>(v);   // quads: lanes 1 0 3 2
+  v = dpp_add<0x4E>(v);   // quads: lanes 2 3 0 1
+  v = dpp_add<0x141>(v);  // half rows mirrored
+  v = dpp_add<0x140>(v);  // rows of 16 mirrored
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
 }
 
 // Sum over the TPR lanes of a row, the same in all of them.  For TPR > 64 every thread of the
@@ -43,9 +54,13 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
   return v;
 }
 
+// Workgroups of the backward pass, each a partial weight gradient: the four a compute unit that are
+// resident at 1,024 16-bit channels (135,826 rows: 160 us; two 238, three 180, eight 170).
+constexpr int kPartsLimit = 256 * 4;
+
 constexpr int threads_for(int tpr) { return tpr > 256 ? tpr : 256; }
 
-template <DT D, int TPR, int ITEMS>
+template <DT D, int TPR, int ITEMS, bool TAIL>
 __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_forward_kernel(
     const typename Elem<D>::T* __restrict__ x, int64_t n, int channels, const typename Elem<D>::T* __restrict__ gamma,
     const typename Elem<D>::T* __restrict__ beta, float eps, typename Elem<D>::T* y, float* __restrict__ mean,
@@ -59,8 +74,8 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_forward_kernel(
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int c0 = (i * TPR + lane) * V;
-    if (gamma != nullptr) load_chunk<D>(gamma, c0, channels, g[i]);
-    if (beta != nullptr) load_chunk<D>(beta, c0, channels, b[i]);
+    if (gamma != nullptr) load_chunk<D, TAIL>(gamma, c0, channels, g[i]);
+    if (beta != nullptr) load_chunk<D, TAIL>(beta, c0, channels, b[i]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (gamma == nullptr) g[i][j] = 1.f;
@@ -73,7 +88,7 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_forward_kernel(
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      load_chunk<D>(px, (i * TPR + lane) * V, channels, v[i]);
+      load_chunk<D, TAIL>(px, (i * TPR + lane) * V, channels, v[i]);
 #pragma unroll
       for (int j = 0; j < V; ++j) sum += v[i][j];
     }
@@ -91,7 +106,7 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_forward_kernel(
     for (int i = 0; i < ITEMS; ++i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[i][j] = fmaf(v[i][j] * r, g[i][j], b[i][j]);
-      store_chunk<D>(y + row * channels, (i * TPR + lane) * V, channels, v[i]);
+      store_chunk<D, TAIL>(y + row * channels, (i * TPR + lane) * V, channels, v[i]);
     }
     if (mean != nullptr && lane == 0) {
       mean[row] = mu;
@@ -102,7 +117,7 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_forward_kernel(
 
 // dx, and this workgroup's partial row sums of dy h and dy into part[blockIdx.x][2][channels]
 // (part may be NULL: no weight gradients).
-template <DT D, int TPR, int ITEMS>
+template <DT D, int TPR, int ITEMS, bool TAIL>
 __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_backward_kernel(
     const typename Elem<D>::T* dy, const typename Elem<D>::T* __restrict__ x, int64_t n, int channels,
     const typename Elem<D>::T* __restrict__ gamma, const float* __restrict__ mean, const float* __restrict__ rstd,
@@ -116,7 +131,7 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_backward_kernel(
   float g[ITEMS][V], dg[ITEMS][V], db[ITEMS][V];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    if (gamma != nullptr) load_chunk<D>(gamma, (i * TPR + lane) * V, channels, g[i]);
+    if (gamma != nullptr) load_chunk<D, TAIL>(gamma, (i * TPR + lane) * V, channels, g[i]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (gamma == nullptr) g[i][j] = 1.f;
@@ -124,32 +139,42 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_backward_kernel(
       db[i][j] = 0.f;
     }
   }
+  // (Waves of other rows hide a row's memory latency: prefetching the next row into registers
+  // takes one of three resident workgroups away and measured 186 us for 155.)
   for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; row < n; row += (int64_t)gridDim.x * kRows) {
+    Chunk<typename Elem<D>::T, V> cx[ITEMS], cdy[ITEMS];  // (every load before the first use)
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      cx[i] = load_raw<D, TAIL>(x + row * channels, (i * TPR + lane) * V, channels);
+      cdy[i] = load_raw<D, TAIL>(dy + row * channels, (i * TPR + lane) * V, channels);  // (zeros beyond the row)
+    }
     const float mu = mean[row], r = rstd[row];
     float h[ITEMS][V], a[ITEMS][V];
     float sa = 0.f, sah = 0.f;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int c0 = (i * TPR + lane) * V;
-      load_chunk<D>(x + row * channels, c0, channels, h[i]);
-      load_chunk<D>(dy + row * channels, c0, channels, a[i]);  // (zeros beyond the row)
+    for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        h[i][j] = (h[i][j] - mu) * r;
+        h[i][j] = (to_float<D>(cx[i].v[j]) - mu) * r;
+        a[i][j] = to_float<D>(cdy[i].v[j]);
+      }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
         dg[i][j] = fmaf(a[i][j], h[i][j], dg[i][j]);
         db[i][j] += a[i][j];
         a[i][j] *= g[i][j];
         sa += a[i][j];
         sah = fmaf(a[i][j], h[i][j], sah);
       }
-    }
     const float ma = row_sum<TPR>(sa, s_a) * inv_c;
     const float mah = row_sum<TPR>(sah, s_b) * inv_c;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
 #pragma unroll
       for (int j = 0; j < V; ++j) a[i][j] = r * (a[i][j] - ma - h[i][j] * mah);
-      store_chunk<D>(dx + row * channels, (i * TPR + lane) * V, channels, a[i]);
+      store_chunk<D, TAIL>(dx + row * channels, (i * TPR + lane) * V, channels, a[i]);
     }
   }
   if (part == nullptr) return;
@@ -191,31 +216,38 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_backward_kernel(
 }
 
 // Sums of the workgroups' partial rows: 16 columns of dgamma | dbeta (2 channels in all) a
-// workgroup, 16 threads a column each taking every 16th partial row, then those 16 in order.
-constexpr int kSumColumns = 16;
+// workgroup, 64 threads a column each taking every 64th partial row, then those 64 in halves.
+constexpr int kSumColumns = 16, kSumRows = 64;
 template <DT D>
-__global__ __launch_bounds__(256) void layer_norm_weight_grad_kernel(const float* __restrict__ part, int parts,
-                                                                     int channels,
-                                                                     typename Elem<D>::T* __restrict__ dgamma,
-                                                                     typename Elem<D>::T* __restrict__ dbeta) {
-  __shared__ float s[16][kSumColumns];
+__global__ __launch_bounds__(kSumColumns * kSumRows) void layer_norm_weight_grad_kernel(
+    const float* __restrict__ part, int parts, int channels, typename Elem<D>::T* __restrict__ dgamma,
+    typename Elem<D>::T* __restrict__ dbeta) {
+  __shared__ float s[kSumRows][kSumColumns];
   const int col = threadIdx.x % kSumColumns, k = threadIdx.x / kSumColumns;
   const int c = blockIdx.x * kSumColumns + col;
   float sum = 0.f;
-  if (c < 2 * channels)
-    for (int p = k; p < parts; p += 16) sum += part[(int64_t)p * 2 * channels + c];
+  if (c < 2 * channels) {
+    float v[kPartsLimit / kSumRows];
+#pragma unroll
+    for (int i = 0; i < kPartsLimit / kSumRows; ++i)
+      v[i] = k + i * kSumRows < parts ? part[(int64_t)(k + i * kSumRows) * 2 * channels + c] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kPartsLimit / kSumRows; ++i) sum += v[i];
+  }
   s[k][col] = sum;
   __syncthreads();
-  if (k != 0 || c >= 2 * channels) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) sum += s[i][col];
-  if (c < channels) dgamma[c] = from_float<D>(sum);
-  else dbeta[c - channels] = from_float<D>(sum);
+  for (int half = kSumRows / 2; half >= 1; half /= 2) {
+    if (k < half) s[k][col] += s[k + half][col];
+    __syncthreads();
+  }
+  if (k != 0 || c >= 2 * channels) return;
+  if (c < channels) dgamma[c] = from_float<D>(s[0][col]);
+  else dbeta[c - channels] = from_float<D>(s[0][col]);
 }
 
 constexpr int kMaxChannels = 16384;
-constexpr int kGridLimit = 256 * 8;   // workgroups of the forward pass (eight a compute unit)
-constexpr int kPartsLimit = 256 * 2;  // workgroups of the backward pass, each a partial weight gradient
+constexpr int kGridLimit = 256 * 4;  // workgroups of the forward pass (135,826 x 1024 bf16: 101 us; eight a compute unit 119)
 
 struct Forward {
   const void *x, *gamma, *beta;
@@ -232,48 +264,68 @@ struct Backward {
 
 int rows_per_block(int tpr) { return threads_for(tpr) / tpr; }
 
-template <DT D, int TPR, int ITEMS>
+template <DT D, int TPR, int ITEMS, bool TAIL>
 void launch(const Forward& f, int64_t n, int channels, int blocks, hipStream_t stream) {
   using T = typename Elem<D>::T;
-  layer_norm_forward_kernel<D, TPR, ITEMS><<<blocks, threads_for(TPR), 0, stream>>>(
+  layer_norm_forward_kernel<D, TPR, ITEMS, TAIL><<<blocks, threads_for(TPR), 0, stream>>>(
       static_cast<const T*>(f.x), n, channels, static_cast<const T*>(f.gamma), static_cast<const T*>(f.beta), f.eps,
       static_cast<T*>(f.y), f.mean, f.rstd);
 }
-template <DT D, int TPR, int ITEMS>
+template <DT D, int TPR, int ITEMS, bool TAIL>
 void launch(const Backward& b, int64_t n, int channels, int blocks, hipStream_t stream) {
   using T = typename Elem<D>::T;
-  layer_norm_backward_kernel<D, TPR, ITEMS><<<blocks, threads_for(TPR), 0, stream>>>(
+  layer_norm_backward_kernel<D, TPR, ITEMS, TAIL><<<blocks, threads_for(TPR), 0, stream>>>(
       static_cast<const T*>(b.dy), static_cast<const T*>(b.x), n, channels, static_cast<const T*>(b.gamma), b.mean,
       b.rstd, static_cast<T*>(b.dx), b.part);
 }
 
-// Lanes of a row: a wave up to 4 chunks a lane, then 256 threads up to 4, then 1024 (16,384
-// channels: 2 chunks a lane in 16 bits, 4 in float32; more would not stay in registers).
-int lanes_for(int chunks) { return chunks <= 256 ? 64 : chunks <= 1024 ? 256 : 1024; }
+// Lanes of a row.  A lane holds up to 4 chunks in the forward pass and 2 in the backward pass,
+// whose gradients and weights stay in registers too (up to 16,384 channels; beyond, float32 rows
+// would not fit).
+int lanes_for(const Forward&, int chunks) { return chunks <= 256 ? 64 : chunks <= 1024 ? 256 : 1024; }
+int lanes_for(const Backward&, int chunks) { return chunks <= 128 ? 64 : chunks <= 512 ? 256 : 1024; }
 
-template <DT D, typename A>
-hipError_t launch_rows(const A& a, int64_t n, int channels, int blocks, hipStream_t stream) {
-  const int chunks = (channels + kChunk<D> - 1) / kChunk<D>;
-  if (chunks <= 64) launch<D, 64, 1>(a, n, channels, blocks, stream);
-  else if (chunks <= 128) launch<D, 64, 2>(a, n, channels, blocks, stream);
-  else if (chunks <= 256) launch<D, 64, 4>(a, n, channels, blocks, stream);
-  else if (chunks <= 512) launch<D, 256, 2>(a, n, channels, blocks, stream);
-  else if (chunks <= 1024) launch<D, 256, 4>(a, n, channels, blocks, stream);
-  else if (chunks <= 2048) launch<D, 1024, 2>(a, n, channels, blocks, stream);
-  else if constexpr (D == DT::F32) launch<D, 1024, 4>(a, n, channels, blocks, stream);
+template <DT D, bool TAIL>
+hipError_t launch_rows(const Forward& a, int64_t n, int channels, int chunks, int blocks, hipStream_t stream) {
+  if (chunks <= 64) launch<D, 64, 1, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 128) launch<D, 64, 2, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 256) launch<D, 64, 4, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 512) launch<D, 256, 2, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 1024) launch<D, 256, 4, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 2048) launch<D, 1024, 2, TAIL>(a, n, channels, blocks, stream);
+  else if constexpr (D == DT::F32) launch<D, 1024, 4, TAIL>(a, n, channels, blocks, stream);
   return hipGetLastError();
+}
+template <DT D, bool TAIL>
+hipError_t launch_rows(const Backward& a, int64_t n, int channels, int chunks, int blocks, hipStream_t stream) {
+  if (chunks <= 64) launch<D, 64, 1, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 128) launch<D, 64, 2, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 256) launch<D, 256, 1, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 512) launch<D, 256, 2, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 1024) launch<D, 1024, 1, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 2048) launch<D, 1024, 2, TAIL>(a, n, channels, blocks, stream);
+  else if constexpr (D == DT::F32) launch<D, 1024, 4, TAIL>(a, n, channels, blocks, stream);
+  return hipGetLastError();
+}
+
+// (whole chunks: no element-wise ends in the kernel, whose branches part the loads of a row)
+template <DT D, typename A>
+hipError_t launch_ends(const A& a, int64_t n, int channels, int blocks, hipStream_t stream) {
+  const int chunks = (channels + kChunk<D> - 1) / kChunk<D>;
+  return channels % kChunk<D> == 0 ? launch_rows<D, false>(a, n, channels, chunks, blocks, stream)
+                                   : launch_rows<D, true>(a, n, channels, chunks, blocks, stream);
 }
 
 template <typename A>
 hipError_t launch_dtype(const A& a, int64_t n, int channels, int dtype, int blocks, hipStream_t stream) {
-  if (dtype == SUBM_F32) return launch_rows<DT::F32>(a, n, channels, blocks, stream);
-  if (dtype == SUBM_F16) return launch_rows<DT::F16>(a, n, channels, blocks, stream);
-  return launch_rows<DT::BF16>(a, n, channels, blocks, stream);
+  if (dtype == SUBM_F32) return launch_ends<DT::F32>(a, n, channels, blocks, stream);
+  if (dtype == SUBM_F16) return launch_ends<DT::F16>(a, n, channels, blocks, stream);
+  return launch_ends<DT::BF16>(a, n, channels, blocks, stream);
 }
 
-int blocks_for(int64_t n, int channels, int dtype, int limit) {
+template <typename A> int blocks_for(const A& a, int64_t n, int channels, int dtype, int limit) {
   const int chunk = dtype == SUBM_F32 ? 4 : 8;
-  const int rows = rows_per_block(lanes_for((channels + chunk - 1) / chunk));
+  const int rows = rows_per_block(lanes_for(a, (channels + chunk - 1) / chunk));
   return (int)std::min<int64_t>((n + rows - 1) / rows, limit);
 }
 
@@ -309,7 +361,7 @@ extern "C" int sparse_layer_norm_forward(const void* x, int64_t n, int channels,
       misaligned(mean, 4) || misaligned(rstd, 4))
     return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
   const Forward f{x, gamma, beta, y, mean, rstd, eps};
-  const hipError_t e = launch_dtype(f, n, channels, dtype, blocks_for(n, channels, dtype, kGridLimit), stream);
+  const hipError_t e = launch_dtype(f, n, channels, dtype, blocks_for(f, n, channels, dtype, kGridLimit), stream);
   if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_forward launch"));
   return SUBM_OK;
 }
@@ -328,8 +380,8 @@ extern "C" int sparse_layer_norm_backward(const void* dy, const void* x, int64_t
       misaligned(dgamma, elem) || misaligned(dbeta, elem) || misaligned(mean, 4) || misaligned(rstd, 4))
     return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
   if (n == 0 && dgamma == nullptr) return SUBM_OK;
-  const int blocks = blocks_for(n, channels, dtype, kPartsLimit);
-  float* part = nullptr;
+  Backward b{dy, x, gamma, mean, rstd, dx, nullptr};
+  const int blocks = blocks_for(b, n, channels, dtype, kPartsLimit);
   if (dgamma != nullptr) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -337,24 +389,23 @@ extern "C" int sparse_layer_norm_backward(const void* dy, const void* x, int64_t
     void* scratch = nullptr;
     st = stream_scratch(dev, stream, std::max<size_t>((size_t)blocks * 2 * channels * sizeof(float), 16), &scratch);
     if (!st.ok()) return fail(st);
-    part = static_cast<float*>(scratch);
+    b.part = static_cast<float*>(scratch);
   }
   hipError_t e = hipSuccess;
   if (n > 0) {
-    const Backward b{dy, x, gamma, mean, rstd, dx, part};
     e = launch_dtype(b, n, channels, dtype, blocks, stream);
   }
   if (e == hipSuccess && dgamma != nullptr) {
     const int grid = (2 * channels + kSumColumns - 1) / kSumColumns;
     if (dtype == SUBM_F32)
-      layer_norm_weight_grad_kernel<DT::F32><<<grid, 256, 0, stream>>>(part, blocks, channels, static_cast<float*>(dgamma),
+      layer_norm_weight_grad_kernel<DT::F32><<<grid, kSumColumns * kSumRows, 0, stream>>>(b.part, blocks, channels, static_cast<float*>(dgamma),
                                                                        static_cast<float*>(dbeta));
     else if (dtype == SUBM_F16)
-      layer_norm_weight_grad_kernel<DT::F16><<<grid, 256, 0, stream>>>(
-          part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
+      layer_norm_weight_grad_kernel<DT::F16><<<grid, kSumColumns * kSumRows, 0, stream>>>(
+          b.part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
     else
-      layer_norm_weight_grad_kernel<DT::BF16><<<grid, 256, 0, stream>>>(
-          part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
+      layer_norm_weight_grad_kernel<DT::BF16><<<grid, kSumColumns * kSumRows, 0, stream>>>(
+          b.part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
     e = hipGetLastError();
   }
   if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_backward launch"));

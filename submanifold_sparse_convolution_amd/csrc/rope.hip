@@ -3,9 +3,9 @@
 //   (u, v) -> m (u cos t - v sin t, v cos t + u sin t);
 // the gradient is the same rotation by -t.  The other channels are copied.
 //
-// Bound by HBM: 2 values an element, 3 operations.  A thread takes one 16-byte unit of a row's
-// head, computes its sines once and then walks the heads, so the sines cost 1 / heads of what
-// they would cost an element.
+// Bound by HBM: 2 values an element, 3 operations.  A workgroup first computes the sines of its
+// rows into LDS, once for all heads (each costs some 40 instructions), and then walks the rows'
+// 16-byte units in storage order.
 #include <algorithm>
 #include <cmath>
 
@@ -24,9 +24,15 @@ struct RopeArgs {
   const int32_t* positions;
   int64_t pos_row;
   const float* freq;
-  int heads, head_dim, pairs, num_freq, heads_per_group;
+  int heads, head_dim, pairs, num_freq;
   float magnitude, sign;
+  // a workgroup takes `rows` rows of `group` heads, `units` units a head (see rope_kernel)
+  int rows, group, units;
+  uint32_t unit_magic, group_magic;  // ceil(2^32 / units), ceil(2^32 / group)
 };
+
+// i / d for i < 2^16 and magic = ceil(2^32 / d), d < 2^16 (magic 0: d is 1).
+__device__ __forceinline__ int divide(int i, uint32_t magic) { return magic == 0 ? i : (int)__umulhi((uint32_t)i, magic); }
 
 // magnitude * (cos, sin) of one pair's angle.  The turns are position * freq / (2 pi), formed and
 // reduced in float64: float32 would keep only 24 bits of an angle that passes 2^13 radians.
@@ -39,81 +45,107 @@ __device__ __forceinline__ float2 rotation(const RopeArgs& a, int64_t row, int p
   return make_float2(c * a.magnitude, s * a.magnitude * a.sign);
 }
 
-// One thread: unit `unit` of row `row`, heads [group * heads_per_group, ...).  Units of a head:
+constexpr int kThreads = 256;
+constexpr int kBatch = 2;               // units a thread has in flight
+constexpr int kSines = 4096;            // LDS: float2 of rows * pairs, 32 KB
+
+// Units of a head:
 //   interleaved: the chunks of its channels (pairs never straddle two);
 //   half-split:  the chunks of the first channels of its pairs, each with its partner chunk
 //                `pairs` further on, then the chunks of the channels past the pairs (copied).
 template <DT D, bool HALF>
-__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units, int groups) {
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   using T = typename Elem<D>::T;
   constexpr int V = kChunk<D>;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t rg = id / units;
-  const int unit = (int)(id - rg * units);
-  const int64_t row = rg / groups;
-  const int group = (int)(rg - row * groups);
-  if (row >= a.n) return;
-  const int h0 = group * a.heads_per_group;
-  const int h1 = min(a.heads, h0 + a.heads_per_group);
-  const T* x = static_cast<const T*>(a.x) + row * a.x_row;
-  T* y = static_cast<T*>(a.y) + row * a.y_row;
-  const int rotated = 2 * a.pairs;
-  if constexpr (HALF) {
-    const int turning = (a.pairs + V - 1) / V;
-    if (unit >= turning) {
-      const int c = rotated + (unit - turning) * V;
-      for (int h = h0; h < h1; ++h) store_raw<D>(y + h * a.y_head, c, a.head_dim, load_raw<D>(x + h * a.x_head, c, a.head_dim));
-      return;
-    }
-    const int c = unit * V;
-    float2 cs[V];
+  extern __shared__ float2 s_turn[];  // [rows, pairs]
+  const int64_t row0 = (int64_t)blockIdx.x * a.rows;
+  const int rows = (int)(a.n - row0 < a.rows ? a.n - row0 : a.rows);
+  const int head0 = blockIdx.y * a.group, group = min(a.group, a.heads - head0);
+  for (int i = threadIdx.x; i < rows * a.pairs; i += kThreads) {
+    const int r = i / a.pairs;
+    s_turn[i] = rotation(a, row0 + r, i - r * a.pairs);
+  }
+  __syncthreads();
+  const T* x = static_cast<const T*>(a.x) + row0 * a.x_row + head0 * a.x_head;
+  T* y = static_cast<T*>(a.y) + row0 * a.y_row + head0 * a.y_head;
+  const int rotated = 2 * a.pairs, turning = HALF ? (a.pairs + V - 1) / V : 0;
+  const int total = rows * a.group * a.units;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kBatch) {
+    Chunk<T, V> u[kBatch], v[kBatch];
+    const T* px[kBatch];
+    T* py[kBatch];
+    const float2* turn[kBatch];
+    int c[kBatch], end[kBatch];  // first channel and the end of its kind (0: no unit)
 #pragma unroll
-    for (int j = 0; j < V; ++j) cs[j] = c + j < a.pairs ? rotation(a, row, c + j) : make_float2(1.f, 0.f);
-    for (int h = h0; h < h1; ++h) {
-      float u[V], v[V], ou[V], ov[V];
-      load_chunk<D>(x + h * a.x_head, c, a.pairs, u);
-      load_chunk<D>(x + h * a.x_head + a.pairs, c, a.pairs, v);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        ou[j] = u[j] * cs[j].x - v[j] * cs[j].y;
-        ov[j] = v[j] * cs[j].x + u[j] * cs[j].y;
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kThreads;
+      const int rh = divide(i, a.unit_magic), unit = i - rh * a.units;
+      const int r = divide(rh, a.group_magic), h = rh - r * a.group;
+      px[b] = x + r * a.x_row + h * a.x_head;
+      py[b] = y + r * a.y_row + h * a.y_head;
+      turn[b] = s_turn + r * a.pairs;
+      const bool copied = HALF && unit >= turning;
+      c[b] = HALF && copied ? rotated + (unit - turning) * V : unit * V;
+      end[b] = i < total && h < group ? (HALF && !copied ? a.pairs : a.head_dim) : 0;
+      if (end[b] != 0) {
+        u[b] = load_raw<D>(px[b], c[b], end[b]);
+        if (HALF && !copied) v[b] = load_raw<D>(px[b] + a.pairs, c[b], end[b]);
       }
-      store_chunk<D>(y + h * a.y_head, c, a.pairs, ou);
-      store_chunk<D>(y + h * a.y_head + a.pairs, c, a.pairs, ov);
     }
-  } else {
-    const int c = unit * V;
-    float2 cs[V / 2];
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) cs[j] = c + 2 * j < rotated ? rotation(a, row, c / 2 + j) : make_float2(1.f, 0.f);
-    for (int h = h0; h < h1; ++h) {
-      auto w = load_raw<D>(x + h * a.x_head, c, a.head_dim);
+    for (int b = 0; b < kBatch; ++b) {
+      if (end[b] == 0) continue;
+      if constexpr (HALF) {
+        if (c[b] < rotated) {
+          float fu[V], fv[V];
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        if (c + 2 * j < rotated) {  // (channels past the pairs are copied bit for bit)
-          const float u = to_float<D>(w.v[2 * j]), v = to_float<D>(w.v[2 * j + 1]);
-          w.v[2 * j] = from_float<D>(u * cs[j].x - v * cs[j].y);
-          w.v[2 * j + 1] = from_float<D>(v * cs[j].x + u * cs[j].y);
+          for (int j = 0; j < V; ++j) {
+            const float2 t = c[b] + j < a.pairs ? turn[b][c[b] + j] : make_float2(1.f, 0.f);
+            const float p = to_float<D>(u[b].v[j]), q = to_float<D>(v[b].v[j]);
+            fu[j] = p * t.x - q * t.y;
+            fv[j] = q * t.x + p * t.y;
+          }
+          u[b] = pack_chunk<D>(fu);
+          store_raw<D>(py[b] + a.pairs, c[b], end[b], pack_chunk<D>(fv));
         }
+      } else {
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+          const float2 t = c[b] + j < rotated ? turn[b][(c[b] + j) / 2] : make_float2(1.f, 0.f);
+          const float p = to_float<D>(u[b].v[j]), q = to_float<D>(u[b].v[j + 1]);
+          f[j] = p * t.x - q * t.y;
+          f[j + 1] = q * t.x + p * t.y;
+        }
+        const Chunk<T, V> turned = pack_chunk<D>(f);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (c[b] + j < rotated) u[b].v[j] = turned.v[j];  // (channels past the pairs are copied bit for bit)
       }
-      store_raw<D>(y + h * a.y_head, c, a.head_dim, w);
+      store_raw<D>(py[b], c[b], end[b], u[b]);
     }
   }
 }
 
+uint32_t magic(int d) { return d == 1 ? 0u : (uint32_t)((0x100000000ull + d - 1) / d); }
+
 template <DT D, bool HALF>
 hipError_t launch(RopeArgs a, hipStream_t stream) {
   constexpr int V = kChunk<D>;
-  const int units = HALF ? (a.pairs + V - 1) / V + (a.head_dim - 2 * a.pairs + V - 1) / V : (a.head_dim + V - 1) / V;
-  // Heads split into groups only while the rows alone leave compute units without a workgroup:
-  // each further group computes the sines of its pairs again.
-  int groups = 1;
-  while (groups * 2 <= a.heads && a.n * units * groups < 256 * 256) groups *= 2;
-  a.heads_per_group = (a.heads + groups - 1) / groups;
-  groups = (a.heads + a.heads_per_group - 1) / a.heads_per_group;
-  const int64_t blocks = (a.n * units * groups + 255) / 256;
-  if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-  rope_kernel<D, HALF><<<(unsigned)blocks, 256, 0, stream>>>(a, units, groups);
+  a.units = HALF ? (a.pairs + V - 1) / V + (a.head_dim - 2 * a.pairs + V - 1) / V : (a.head_dim + V - 1) / V;
+  // Heads of a workgroup: all, up to 2^13 units.  Rows: some 2,048 units a workgroup, fewer while
+  // that leaves compute units without one, and no more than the sines of LDS.
+  a.group = std::min(a.heads, std::max(1, 8192 / a.units));
+  const int groups = (a.heads + a.group - 1) / a.group;
+  int64_t rows = std::max<int64_t>(1, 2048 / (a.group * a.units));
+  rows = std::min<int64_t>(rows, std::max<int64_t>(1, a.n * groups / 1024));
+  rows = std::min<int64_t>(rows, std::max(1, kSines / a.pairs));
+  a.rows = (int)rows;
+  a.unit_magic = magic(a.units);
+  a.group_magic = magic(a.group);
+  const int64_t blocks = (a.n + a.rows - 1) / a.rows;
+  const size_t lds = (size_t)a.rows * a.pairs * sizeof(float2);
+  rope_kernel<D, HALF><<<dim3((unsigned)blocks, (unsigned)groups), kThreads, lds, stream>>>(a);
   return hipGetLastError();
 }
 
