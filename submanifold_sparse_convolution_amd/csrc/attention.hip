@@ -132,8 +132,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
   Loader lk, lv;
   lk.wave = lv.wave = wave;
   lk.lane = lv.lane = lane;
-  lk.place(k, a.head_dim, 1, 0);
-  lv.place(v, a.head_dim, 1, 0);
+  lk.place(k, a.head_dim, 1, 0, 0);
+  lv.place(v, a.head_dim, 1, 0, 0);
   const uint32_t lds = lds_offset(s_kv);
   const TileReader<D, DP> rd(lane, lds, lds + 2 * kTile);
   // this workgroup's keys: all, or its share of whole tiles (a share may be empty)
@@ -253,20 +253,41 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   const int64_t at = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
   if (at >= all) return;
   const int c = threadIdx.x % kThreads * 4;
-  float base = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) base = fmaxf(base, a.state[s * all + at].x);
-  float sum = 0.f;
+  // The splits in batches, every load of a batch in flight at once, joined as a running softmax.
+  constexpr int kBatch = 8;
+  float base = -INFINITY, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 st = a.state[s * all + at];
-    if (st.y == 0.f) continue;  // (no keys in this share, or all its scores -infinity)
-    const float w = exp2_fast(st.x - base);
-    const float4 p = *reinterpret_cast<const float4*>(a.part + (s * all + at) * DP + c);
-    sum = fmaf(w, st.y, sum);
-    o.x = fmaf(w, p.x, o.x);
-    o.y = fmaf(w, p.y, o.y);
-    o.z = fmaf(w, p.z, o.z);
-    o.w = fmaf(w, p.w, o.w);
+  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+    float2 st[kBatch];
+    float4 p[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t row = min(s0 + i, a.splits - 1) * all + at;
+      st[i] = a.state[row];
+      p[i] = *reinterpret_cast<const float4*>(a.part + row * DP + c);
+    }
+    float top = base;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, st[i].x);
+    if (top == -INFINITY) continue;  // (no keys: the same in every split)
+    const float shrink = exp2_fast(base - top);
+    base = top;
+    sum *= shrink;
+    o.x *= shrink;
+    o.y *= shrink;
+    o.z *= shrink;
+    o.w *= shrink;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // a share without keys has a sum of 0 and wrote no part
+      const bool some = s0 + i < a.splits && st[i].y != 0.f;
+      const float w = some ? exp2_fast(st[i].x - base) : 0.f;
+      sum = fmaf(w, some ? st[i].y : 0.f, sum);
+      o.x = fmaf(w, some ? p[i].x : 0.f, o.x);
+      o.y = fmaf(w, some ? p[i].y : 0.f, o.y);
+      o.z = fmaf(w, some ? p[i].z : 0.f, o.z);
+      o.w = fmaf(w, some ? p[i].w : 0.f, o.w);
+    }
   }
   const bool none = base == -INFINITY;  // the item has no keys
   const float f = none ? 0.f : 1.f / sum;
@@ -303,7 +324,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   }
   // Too few workgroups to fill the compute units: split the keys, as long as a share keeps
   // kShare keys on average (the join costs a launch and a float32 copy of the rows a share).
-  constexpr int kShare = 512;
+  constexpr int kShare = D == DT::F32 ? 96 : 512;
   const int64_t blocks = (rows / 128 + a.items) * a.kv_heads;
   const int64_t want = std::min<int64_t>(2 * kUnits / blocks, a.nk / a.items / kShare);
   if (want < 2) {
@@ -342,6 +363,7 @@ Status check_attention(const AttentionShape& s) {
   if (s.heads < 1 || s.kv_heads < 1 || s.heads % s.kv_heads != 0)
     return make_status(SUBM_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
   if (s.kv_heads > 65535) return make_status(SUBM_ERR_INVALID_ARG, "kv_heads exceeds 65535");
+  if (s.heads / s.kv_heads > 128) return make_status(SUBM_ERR_UNSUPPORTED, "more than 128 query heads a key head");
   if (s.nq * s.heads > INT32_MAX) return make_status(SUBM_ERR_INVALID_ARG, "nq * heads exceeds 2^31 - 1");
   if (s.head_dim < 1) return make_status(SUBM_ERR_INVALID_ARG, "head_dim must be at least 1");
   if (s.head_dim % 8 != 0 || s.head_dim > 128)

@@ -28,12 +28,13 @@ struct BwdArgs {
   int64_t nq, nk, q_slots;
   int items, heads, kv_heads, head_dim;
   float scale;
+  int q_rows;  // packed rows of a workgroup of the dq kernel
+  // The walked rows split over workgroups: float32 copies of dq [q_splits, kv_heads, nq * group, DP]
+  // and of dk and dv [k_splits, kv_heads, nk, DP], summed by a third kernel.  NULL: not split.
+  int q_splits, k_splits;
+  float *dq_part, *dk_part, *dv_part;
 };
 
-// Waves of a workgroup, 32 own rows (query rows or keys) each: 8 share a tile stream at 128
-// channels, where two waves a SIMD are all that fit; 4 at 64 channels, three workgroups a compute unit.
-template <DT D, int DP> constexpr int kWaves = D != DT::F32 && DP == 128 ? 8 : 4;
-template <DT D, int DP> constexpr int kResident = D != DT::F32 && DP == 64 ? 3 : 1;  // waves a SIMD asked for
 constexpr int kStep = 32;  // rows of the walked tile
 
 constexpr float kF16Shift = 15.f;  // p is scaled by 2^15 in float16 products
@@ -69,10 +70,20 @@ template <DT D> __device__ __forceinline__ float dot_frag(const Frag<D>& a, cons
   return s;
 }
 
+// A row's accumulator times `f` to a float32 copy.
+template <int DP> __device__ __forceinline__ void store_part(float* row, const f32x16_t (&acc)[DP / 32], float f, int lane) {
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(row + db * 32 + 8 * i + 4 * (lane >> 5)) =
+          make_float4(acc[db][4 * i] * f, acc[db][4 * i + 1] * f, acc[db][4 * i + 2] * f, acc[db][4 * i + 3] * f);
+}
+
 // d of the own query rows, then dq over the keys, which stream through LDS in tiles of 32.  As in
 // the forward pass a step holds independent pieces of work:
 //   scores and dp of tile t + 1 (k, v),  e of tile t,  product of tile t - 1 (k).
-template <DT D, int DP, int W, int OCC>
+template <DT D, int DP, int W, int OCC, bool SPLIT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   constexpr int kRows = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
@@ -110,8 +121,9 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     if constexpr (D == DT::F16) peak = fmaxf(peak, absmax_frag<D>(gf[kk]));
   }
   d = half_sum(d);
+  const bool first = !SPLIT || blockIdx.z == 0;  // (every split needs d, one leaves it for dk and dv)
   const float base = there ? a.lse[qmap.stat(row, a.heads)] * kLog2e : 0.f;  // log2 of the row's normaliser
-  if (there && lane < 32) {
+  if (first && there && lane < 32) {
     const int64_t at = head * (a.nq * group) + q0 * group + row;
     a.norm[at] = D == DT::F16 ? base - kF16Shift : base;
     a.delta[at] = d;
@@ -124,7 +136,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     for (int mk = 16; mk >= 1; mk >>= 1) peak = fmaxf(peak, __shfl_xor(peak, mk, 64));
     if (lane == 0) s_peak[wave] = peak;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (first && threadIdx.x == 0) {
 #pragma unroll
       for (int w = 0; w < W; ++w) peak = fmaxf(peak, s_peak[w]);
       a.peak[head * a.q_slots + blockIdx.x] = peak;
@@ -135,15 +147,22 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   Loader lk, lv;
   lk.wave = lv.wave = wave;
   lk.lane = lv.lane = lane;
-  lk.place(k, a.head_dim, 1, 0);
-  lv.place(v, a.head_dim, 1, 0);
+  lk.place(k, a.head_dim, 1, 0, 0);
+  lv.place(v, a.head_dim, 1, 0, 0);
   const uint32_t lds = lds_offset(s_kv);
   const TileReader<D, DP> rd(lane, lds, lds);
-  const int tiles = (nk + kStep - 1) / kStep;
+  int tiles = (nk + kStep - 1) / kStep, left = nk;
+  if constexpr (SPLIT) {
+    const int share = (tiles + a.q_splits - 1) / a.q_splits, t0 = min(tiles, share * (int)blockIdx.z);
+    tiles = min(share, tiles - t0);
+    left = min(nk - t0 * kStep, tiles * kStep);
+    kp += (int64_t)t0 * kStep * k.row;
+    vp += (int64_t)t0 * kStep * v.row;
+  }
   const auto load_k = [&](int t, int slot) {
-    lk.load(kp + (int64_t)t * kStep * k.row, t < 0 ? 0 : nk - t * kStep, lds + slot * kTile);
+    lk.load(kp + (int64_t)t * kStep * k.row, t < 0 ? 0 : left - t * kStep, lds + slot * kTile);
   };
-  const auto load_v = [&](int t, int slot) { lv.load(vp + (int64_t)t * kStep * v.row, nk - t * kStep, lds + (4 + slot) * kTile); };
+  const auto load_v = [&](int t, int slot) { lv.load(vp + (int64_t)t * kStep * v.row, left - t * kStep, lds + (4 + slot) * kTile); };
   const auto scores = [&](int slot, f32x16_t& s, f32x16_t& dp) {
     s = zero16();
     dp = zero16();
@@ -187,10 +206,10 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
       scores((slot + 1) % 4, s_next, dp_next);
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], c, -base)) * (dp[i] - d) * unit;
-      if ((t + 1) * kStep > nk) {  // (a key past the end scores 0, which p need not take to 0)
+      if ((t + 1) * kStep > left) {  // (a key past the end scores 0, which p need not take to 0)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (t * kStep + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= nk) s[i] = 0.f;
+          if (t * kStep + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= left) s[i] = 0.f;
       }
       product((slot + 3) % 4, e);
 #pragma unroll
@@ -210,7 +229,12 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     wait_vmcnt<0>();
     product((tiles - 1) % 4, e);
   }
-  if (there) store_row<D, DP>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
+  if (!there) return;
+  if constexpr (SPLIT)
+    store_part<DP>(a.dq_part + (((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row) * DP, acc,
+                   a.scale / unit, lane);
+  else
+    store_row<D, DP>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
 }
 
 // The next 32 of `left` floats (zeros past them) straight to LDS, which takes 64 of them.
@@ -229,9 +253,9 @@ __device__ __forceinline__ void load_stats(const float* p, int left, uint32_t ld
 // stream through LDS in tiles of 32.  Two waves a SIMD overlap each other's exponentials and
 // products.  At 128 channels in 16 bits the own rows of v stay in LDS: with the two accumulators
 // and k there is no room for them in 256 registers.
-template <DT D, int DP, int W, int OCC>
+template <DT D, int DP, int W, int OCC, bool SPLIT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
-  constexpr int kKeys = 32 * W, kRows = 32 * kWaves<D, DP>;
+  constexpr int kKeys = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
   constexpr bool kParked = D != DT::F32 && DP == 128;
   using Loader = TileLoader<D, DP, kStep, W>;
@@ -258,9 +282,9 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
 
   float unit = 1.f;
   if constexpr (D == DT::F16) {  // the largest |dout| of the item and head, from its query blocks
-    const int64_t first = q0 * group / kRows + item;
+    const int64_t first = q0 * group / a.q_rows + item;
     float peak = 0.f;
-    for (int t = threadIdx.x; t < (rows + kRows - 1) / kRows; t += W * 64)
+    for (int t = threadIdx.x; t < (rows + a.q_rows - 1) / a.q_rows; t += W * 64)
       peak = fmaxf(peak, a.peak[head * a.q_slots + first + t]);
 #pragma unroll
     for (int mk = 32; mk >= 1; mk >>= 1) peak = fmaxf(peak, __shfl_xor(peak, mk, 64));
@@ -287,37 +311,54 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     Parker park;
     park.wave = wave;
     park.lane = lane;
-    park.place(v, a.head_dim, 1, 0);
+    park.place(v, a.head_dim, 1, 0, 0);
     park.load(kmap.at<D>(v, tile * kKeys), nk - tile * kKeys, lds + 4 * kTile);
   }
   Loader lq, lg;
   lq.wave = lg.wave = wave;
   lq.lane = lg.lane = lane;
-  lq.place(q, a.head_dim, group, 0);
-  lg.place(g, a.head_dim, group, 0);
+  const int magic = 65536 / group + 1;
   const TileReader<D, DP> rd(lane, lds, lds);
   const uint32_t own = wave * kTile;  // (this wave's rows of the parked tile)
   const uint32_t stat = __builtin_amdgcn_readfirstlane(lds_offset(s_stat));
-  const auto load = [&](int t, int slot) {
-    const int r0 = t * kStep, tok = group == 1 ? r0 : r0 / group;
-    if (kStep % group != 0) {  // (uniform) the tile starts inside a token
-      lq.place(q, a.head_dim, group, r0 - tok * group);
-      lg.place(g, a.head_dim, group, r0 - tok * group);
+  // this workgroup's query rows: all, or its share of whole tiles (a share may be empty)
+  int steps = (rows + kStep - 1) / kStep, r0 = 0, end = rows;
+  if constexpr (SPLIT) {
+    const int share = (steps + a.k_splits - 1) / a.k_splits, t0 = min(steps, share * (int)blockIdx.z);
+    steps = min(share, steps - t0);
+    r0 = t0 * kStep;
+    end = min(rows, r0 + steps * kStep);
+  }
+  int tok = r0 / group, rem = r0 - tok * group;  // of the next tile to load
+  const int tok_step = kStep / group, rem_step = kStep % group;
+  lq.place(q, a.head_dim, group, rem, magic);
+  lg.place(g, a.head_dim, group, rem, magic);
+  const auto load = [&](int slot) {  // the next tile
+    lq.load(qp + (int64_t)tok * q.row, end - r0, lds + slot * kTile);
+    lg.load(gp + (int64_t)tok * g.row, end - r0, lds + (2 + slot) * kTile);
+    if (wave == 0) load_stats(norm + r0, end - r0, stat + slot * 512, lane);
+    if (wave == 1) load_stats(delta + r0, end - r0, stat + slot * 512 + 256, lane);
+    r0 += kStep;
+    tok += tok_step;
+    if (rem_step != 0) {  // (uniform) tiles start inside a token
+      rem += rem_step;
+      if (rem >= group) {
+        rem -= group;
+        ++tok;
+      }
+      lq.place(q, a.head_dim, group, rem, magic);
+      lg.place(g, a.head_dim, group, rem, magic);
     }
-    lq.load(qp + (int64_t)tok * q.row, rows - r0, lds + slot * kTile);
-    lg.load(gp + (int64_t)tok * g.row, rows - r0, lds + (2 + slot) * kTile);
-    if (wave == 0) load_stats(norm + r0, rows - r0, stat + slot * 512, lane);
-    if (wave == 1) load_stats(delta + r0, rows - r0, stat + slot * 512 + 256, lane);
   };
   const float c = a.scale * kLog2e;
   f32x16_t dk[DP / 32], dv[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) dk[db] = dv[db] = zero16();
-  const auto step = [&](int t, int slot) {
+  const auto step = [&](int slot) {
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
-    load(t + 1, slot ^ 1);
+    load(slot ^ 1);
     f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
@@ -349,44 +390,134 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
       }
     }
   };
-  const int steps = (rows + kStep - 1) / kStep;
   if (steps > 0) {
-    load(0, 0);
+    load(0);
     for (int t = 0; t < steps; t += 2) {  // (an odd end takes a step of zeros: a second exit costs registers)
-      step(t, 0);
-      step(t + 1, 1);
+      step(0);
+      step(1);
     }
   }
   wait_vmcnt<0>();  // (the loads past the end)
   if (!there) return;
-  store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, lane);
-  store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, lane);
+  if constexpr (SPLIT) {
+    const int64_t at = (((int64_t)blockIdx.z * a.kv_heads + head) * a.nk + k0 + key) * DP;
+    store_part<DP>(a.dk_part + at, dk, a.scale / unit, lane);
+    store_part<DP>(a.dv_part + at, dv, p_unit, lane);
+  } else {
+    store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, lane);
+    store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, lane);
+  }
+}
+
+// The sums of split gradients, DP / 4 threads a row: blockIdx.y 0 is dq, 1 dk and 2 dv.
+template <DT D, int DP>
+__global__ __launch_bounds__(256) void attention_sum_kernel(BwdArgs a) {
+  constexpr int kThreads = DP / 4;
+  const int job = a.dq_part != nullptr ? blockIdx.y : blockIdx.y + 1;
+  const int group = job == 0 ? a.heads / a.kv_heads : 1, splits = job == 0 ? a.q_splits : a.k_splits;
+  const int64_t rows = job == 0 ? a.nq * group : a.nk, all = rows * a.kv_heads;
+  const int64_t at = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+  const int c = threadIdx.x % kThreads * 4;
+  if (at >= all || c >= a.head_dim) return;
+  const float* part = (job == 0 ? a.dq_part : job == 1 ? a.dk_part : a.dv_part) + at * DP + c;
+  float4 o = *reinterpret_cast<const float4*>(part);
+#pragma unroll 8
+  for (int s = 1; s < splits; ++s) {
+    const float4 p = *reinterpret_cast<const float4*>(part + s * all * DP);
+    o.x += p.x;
+    o.y += p.y;
+    o.z += p.z;
+    o.w += p.w;
+  }
+  const Heads<D> out = heads_of<D>(job == 0 ? a.dq : job == 1 ? a.dk : a.dv);
+  const int head = (int)(at / rows);
+  const int64_t r = at - head * rows, tok = r / group;
+  const int h = head * group + (int)(r - tok * group);
+  store4<D>(out.data + tok * out.row + (int64_t)h * out.head + c, o.x, o.y, o.z, o.w);
+}
+
+template <DT D, int DP, int W, bool SPLIT> hipError_t launch_dq(BwdArgs& a, hipStream_t stream) {
+  constexpr int OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
+  a.q_rows = 32 * W;
+  a.q_slots = a.nq * (a.heads / a.kv_heads) / a.q_rows + a.items;
+  attention_dq_kernel<D, DP, W, OCC, SPLIT>
+      <<<dim3((unsigned)a.q_slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.q_splits : 1u), W * 64, 0, stream>>>(a);
+  return hipGetLastError();
+}
+template <DT D, int DP, int W, bool SPLIT> hipError_t launch_dkv(const BwdArgs& a, hipStream_t stream) {
+  constexpr int OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
+  const int64_t slots = a.nk / (32 * W) + a.items;
+  attention_dkv_kernel<D, DP, W, OCC, SPLIT>
+      <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.k_splits : 1u), W * 64, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// How many workgroups the walked rows are split over, where `blocks` of them leave compute units
+// idle: enough for `per_unit` a compute unit, as long as each keeps `least` walked rows on average.
+int splits_for(int64_t blocks, int64_t walked, int per_unit, int least) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(per_unit * 256 / std::max<int64_t>(blocks, 1), walked / least));
 }
 
 template <DT D, int DP>
-hipError_t launch(const BwdArgs& a, hipStream_t stream) {
-  constexpr int W = kWaves<D, DP>;
-  hipError_t e = hipSuccess;
+Status launch(BwdArgs a, hipStream_t stream) {
+  const int group = a.heads / a.kv_heads;
+  const int64_t rows = a.nq * group;
+  // 128 channels in 16 bits: 8 waves share a tile stream where they fill the compute units.
+  constexpr bool kWide = D != DT::F32 && DP == 128;
+  const bool wide_q = kWide && (rows / 256 + a.items) * a.kv_heads >= 256 && rows / a.items >= 256;
+  const bool wide_k = kWide && (a.nk / 256 + a.items) * a.kv_heads >= 256 && a.nk / a.items >= 256;
+  // Measured, forward and backward: 7,813 tokens, 12 / 4 heads of 64, f16: 451 us not split, 368
+  // with 4 a unit, 376 with 3 or 6; 3,000 tokens, 12 heads of 128, bf16: 337 us with 2, 345 with 4,
+  // 385 with 3; 800 tokens, 8 heads of 64: 41.8 us with shares of 128 rows, 46.8 with 256.
+  constexpr int kPerUnit = DP == 64 ? 4 : 2, kLeast = D == DT::F32 ? 96 : 128;
+  if (!wide_q) a.q_splits = splits_for((rows / 128 + a.items) * a.kv_heads, a.nk / a.items, kPerUnit, kLeast);
+  if (!wide_k) a.k_splits = splits_for((a.nk / 128 + a.items) * a.kv_heads, rows / a.items, kPerUnit, kLeast);
+
+  int dev = 0;
+  SUBM_HIP_TRY(hipGetDevice(&dev));
+  const auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
+  // norm and d of every query row, a peak for each of the smallest query blocks, and the copies
+  const size_t stat = padded((size_t)rows * a.kv_heads * sizeof(float));
+  const size_t peak = padded((size_t)(rows / 128 + a.items) * a.kv_heads * sizeof(float));
+  const size_t part_q = a.q_splits > 1 ? (size_t)a.q_splits * rows * a.kv_heads * DP * sizeof(float) : 0;
+  const size_t part_k = a.k_splits > 1 ? (size_t)a.k_splits * a.nk * a.kv_heads * DP * sizeof(float) : 0;
+  void* scratch = nullptr;
+  Status st = stream_scratch(dev, stream, 2 * stat + peak + part_q + 2 * part_k, &scratch);
+  if (!st.ok()) return st;
+  unsigned char* p = static_cast<unsigned char*>(scratch);
+  a.norm = reinterpret_cast<float*>(p);
+  a.delta = reinterpret_cast<float*>(p + stat);
+  a.peak = reinterpret_cast<float*>(p + 2 * stat);
+  p += 2 * stat + peak;
+  if (part_q > 0) a.dq_part = reinterpret_cast<float*>(p);
+  if (part_k > 0) {
+    a.dk_part = reinterpret_cast<float*>(p + part_q);
+    a.dv_part = reinterpret_cast<float*>(p + part_q + part_k);
+  }
   if (a.nq > 0) {
-    attention_dq_kernel<D, DP, W, kResident<D, DP>><<<dim3((unsigned)a.q_slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
-    e = hipGetLastError();
+    if constexpr (kWide) {
+      if (wide_q) SUBM_HIP_TRY((launch_dq<D, DP, 8, false>(a, stream)));
+    }
+    if (!wide_q) SUBM_HIP_TRY((a.q_splits > 1 ? launch_dq<D, DP, 4, true>(a, stream) : launch_dq<D, DP, 4, false>(a, stream)));
   }
-  if (e == hipSuccess && a.nk > 0) {
-    const int64_t slots = a.nk / (32 * W) + a.items;
-    attention_dkv_kernel<D, DP, W, D == DT::F32 ? 1 : 2><<<dim3((unsigned)slots, (unsigned)a.kv_heads), W * 64, 0, stream>>>(a);
-    e = hipGetLastError();
+  if (a.nk > 0) {
+    if constexpr (kWide) {
+      if (wide_k) SUBM_HIP_TRY((launch_dkv<D, DP, 8, false>(a, stream)));
+    }
+    if (!wide_k) SUBM_HIP_TRY((a.k_splits > 1 ? launch_dkv<D, DP, 4, true>(a, stream) : launch_dkv<D, DP, 4, false>(a, stream)));
   }
-  return e;
+  const int jobs = (part_q > 0 ? 1 : 0) + (part_k > 0 ? 2 : 0);
+  if (jobs > 0) {
+    constexpr int kRowsPer = 256 / (DP / 4);
+    const int64_t most = std::max(part_q > 0 ? rows : 0, part_k > 0 ? a.nk : 0) * a.kv_heads;
+    attention_sum_kernel<D, DP><<<dim3((unsigned)((most + kRowsPer - 1) / kRowsPer), (unsigned)jobs), 256, 0, stream>>>(a);
+    SUBM_HIP_TRY(hipGetLastError());
+  }
+  return Status{};
 }
 
-template <DT D> hipError_t launch_dim(BwdArgs a, hipStream_t stream) {
-  const int64_t rows = a.nq * (a.heads / a.kv_heads);
-  if (a.head_dim <= 64) {
-    a.q_slots = rows / (32 * kWaves<D, 64>) + a.items;
-    return launch<D, 64>(a, stream);
-  }
-  a.q_slots = rows / (32 * kWaves<D, 128>) + a.items;
-  return launch<D, 128>(a, stream);
+template <DT D> Status launch_dim(const BwdArgs& a, hipStream_t stream) {
+  return a.head_dim <= 64 ? launch<D, 64>(a, stream) : launch<D, 128>(a, stream);
 }
 
 }  // namespace
@@ -415,23 +546,29 @@ extern "C" int sparse_attention_backward(const subm_heads_t* dout, const subm_he
   if (nq > 0 && lse == nullptr) return fail(SUBM_ERR_INVALID_ARG, "lse is NULL");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
   if (nq == 0 && nk == 0) return SUBM_OK;
-  BwdArgs a{*dout, *q, *k, *v, *out, *dq, *dk, *dv, lse, nullptr, nullptr, nullptr, q_offsets, k_offsets, nq, nk, 0,
-            items, heads, kv_heads, head_dim, scale};
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(hip_status(e, "hipGetDevice"));
-  // norm and d of every query row, and a peak for each of the smallest query blocks (128 rows)
-  const size_t stat_bytes = ((size_t)nq * heads * sizeof(float) + 255) / 256 * 256;
-  const size_t peak_bytes = (size_t)(nq * (heads / kv_heads) / 128 + items) * kv_heads * sizeof(float);
-  void* scratch = nullptr;
-  st = stream_scratch(dev, stream, 2 * stat_bytes + peak_bytes, &scratch);
+  BwdArgs a{};
+  a.dout = *dout;
+  a.q = *q;
+  a.k = *k;
+  a.v = *v;
+  a.out = *out;
+  a.dq = *dq;
+  a.dk = *dk;
+  a.dv = *dv;
+  a.lse = lse;
+  a.q_offsets = q_offsets;
+  a.k_offsets = k_offsets;
+  a.nq = nq;
+  a.nk = nk;
+  a.items = items;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.scale = scale;
+  a.q_splits = a.k_splits = 1;
+  if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
+  else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
+  else st = launch_dim<DT::BF16>(a, stream);
   if (!st.ok()) return fail(st);
-  a.norm = static_cast<float*>(scratch);
-  a.delta = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + stat_bytes);
-  a.peak = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + 2 * stat_bytes);
-  if (dtype == SUBM_F32) e = launch_dim<DT::F32>(a, stream);
-  else if (dtype == SUBM_F16) e = launch_dim<DT::F16>(a, stream);
-  else e = launch_dim<DT::BF16>(a, stream);
-  if (e != hipSuccess) return fail(hip_status(e, "sparse_attention_backward launch"));
   return SUBM_OK;
 }

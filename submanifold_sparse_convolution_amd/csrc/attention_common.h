@@ -241,13 +241,14 @@ template <DT D, int DP, int R, int W> struct TileLoader {
   __device__ __forceinline__ int row(int n) const { return (n * W + wave) * kRowsPer + lane / C; }
 
   // Tiles of packed rows, `group` a token, that start `rem` rows into a token; keys: group 1.
-  __device__ __forceinline__ void place(const Heads<D>& t, int head_dim, int group, int rem) {
+  // magic: 65536 / group + 1 (exact for the r + rem < 2 * 128 + 32 that occur with group <= 128).
+  __device__ __forceinline__ void place(const Heads<D>& t, int head_dim, int group, int rem, int magic) {
     constexpr int size = Elem<D>::kSize;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int r = row(n);
       const int c = (lane % C) ^ swizzle<D, DP>(r);
-      const int tok = group == 1 ? r : (r + rem) / group;
+      const int tok = group == 1 ? r : ((r + rem) * magic) >> 16;
       const int h = group == 1 ? 0 : r + rem - tok * group;
       offset[n] = c * 16 < head_dim * size ? (uint32_t)((tok * (int)t.row + h * (int)t.head) * size + c * 16) : kOutOfRange;
     }
