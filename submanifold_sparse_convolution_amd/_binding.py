@@ -719,6 +719,12 @@ def sparse_group_norm_act(x: torch.Tensor, item_offsets: torch.Tensor, groups: i
 
 
 # --------------------------------------------------------------------------- transformer block
+#
+# (The smallest calls here take as long on the host as on the device, so these functions test the
+# common case with few attribute reads and leave naming the fault to the helpers.)
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the stream the call runs on (its memory is then reused in that
@@ -728,6 +734,37 @@ def _empty(shape, dtype, device, stream):
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(t, stream):
+    """_empty of a tensor's shape, contiguous."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
+def _run(func: str, device: int, stream, *args) -> None:
+    """Call the library on a device (made current for it) and stream; raise its error."""
+    lib = _lib or load_library()
+    s = _stream_ptr(stream, torch.device("cuda", device)) if stream is not None or _raw_stream is None else _raw_stream(device)
+    if device == _current_device():
+        st = getattr(lib, func)(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib, func)(*args, s)
+    if st != 0:
+        _check(lib, func, st)
+
+
+def _matrix(t, what):
+    """(rows, columns, dtype code) of a contiguous device matrix."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _device_tensor(t, what)
+    code = _DTYPE_CODES.get(t.dtype)
+    if t.dim() != 2 or code is None:
+        raise ValueError(f"{what} must be [N, C] float32 / float16 / bfloat16")
+    n, c = t.shape
+    return n, c, code
 
 
 def _vector(t, shape, dtype, device, what):
@@ -744,27 +781,21 @@ def sparse_layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None
                               eps: float = 1e-5, stats: bool = False, out: torch.Tensor | None = None, stream=None):
     """Layer norm of the rows of x [N, C]: (y, mean, rstd), the float32 statistics [N] only with
     stats=True (else None), which the backward pass needs.  out may be x (in place)."""
-    _device_tensor(x, "x")
-    if x.dim() != 2 or x.dtype not in _DTYPE_CODES:
-        raise ValueError("x must be [N, C] float32 / float16 / bfloat16")
-    n, c = x.shape
-    g = _vector(gamma, (c,), x.dtype, x.device, "gamma")
-    b = _vector(beta, (c,), x.dtype, x.device, "beta")
-    y = _empty((n, c), x.dtype, x.device, stream) if out is None else out
-    if out is not None:
-        _vector(out, (n, c), x.dtype, x.device, "out")
+    n, c, code = _matrix(x, "x")
+    g = None if gamma is None else _vector(gamma, (c,), x.dtype, x.device, "gamma")
+    b = None if beta is None else _vector(beta, (c,), x.dtype, x.device, "beta")
+    if out is None:
+        out = _empty_like(x, stream)
+        y = out.data_ptr()
+    else:
+        y = _vector(out, (n, c), x.dtype, x.device, "out")
     mean = rstd = mean_ptr = rstd_ptr = None
     if stats:
-        both = _empty((2, n), torch.float32, x.device, stream)
-        mean, rstd = both[0], both[1]
-        mean_ptr = both.data_ptr()
-        rstd_ptr = mean_ptr + 4 * n
-    lib = load_library()
-    with _on_device(x.device):
-        st = lib.sparse_layer_norm_forward(x.data_ptr(), n, c, _DTYPE_CODES[x.dtype], g, b, eps, y.data_ptr(), mean_ptr,
-                                           rstd_ptr, _stream_ptr(stream, x.device))
-    _check(lib, "sparse_layer_norm_forward", st)
-    return y, mean, rstd
+        mean, rstd = _empty((2, n), torch.float32, x.device, stream)
+        mean_ptr = mean.data_ptr()
+        rstd_ptr = rstd.data_ptr()
+    _run("sparse_layer_norm_forward", x.get_device(), stream, x.data_ptr(), n, c, code, g, b, eps, y, mean_ptr, rstd_ptr)
+    return out, mean, rstd
 
 
 def sparse_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -772,30 +803,24 @@ def sparse_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
                                out: torch.Tensor | None = None, stream=None):
     """Gradients of sparse_layer_norm_forward: (dx, dgamma, dbeta), the last two None with
     weight_grads=False.  mean, rstd: the forward pass's.  out may be dy (in place)."""
-    _device_tensor(x, "x")
-    if x.dim() != 2 or x.dtype not in _DTYPE_CODES:
-        raise ValueError("x must be [N, C] float32 / float16 / bfloat16")
+    n, c, code = _matrix(x, "x")
     if dy is None or mean is None or rstd is None:
         raise ValueError("dy, mean and rstd are required")
-    n, c = x.shape
     dy_ptr = _vector(dy, (n, c), x.dtype, x.device, "dy")
     m = _vector(mean, (n,), torch.float32, x.device, "mean")
     r = _vector(rstd, (n,), torch.float32, x.device, "rstd")
-    g = _vector(gamma, (c,), x.dtype, x.device, "gamma")
-    dx = _empty((n, c), x.dtype, x.device, stream) if out is None else out
-    if out is not None:
-        _vector(out, (n, c), x.dtype, x.device, "out")
+    g = None if gamma is None else _vector(gamma, (c,), x.dtype, x.device, "gamma")
+    if out is None:
+        out = _empty_like(x, stream)
+        dx = out.data_ptr()
+    else:
+        dx = _vector(out, (n, c), x.dtype, x.device, "out")
     dgamma = dbeta = dg_ptr = db_ptr = None
     if weight_grads:
-        dgamma = _empty((c,), x.dtype, x.device, stream)
-        dbeta = _empty((c,), x.dtype, x.device, stream)
+        dgamma, dbeta = _empty((2, c), x.dtype, x.device, stream)
         dg_ptr, db_ptr = dgamma.data_ptr(), dbeta.data_ptr()
-    lib = load_library()
-    with _on_device(x.device):
-        st = lib.sparse_layer_norm_backward(dy_ptr, x.data_ptr(), n, c, _DTYPE_CODES[x.dtype], g, m, r, dx.data_ptr(),
-                                            dg_ptr, db_ptr, _stream_ptr(stream, x.device))
-    _check(lib, "sparse_layer_norm_backward", st)
-    return dx, dgamma, dbeta
+    _run("sparse_layer_norm_backward", x.get_device(), stream, dy_ptr, x.data_ptr(), n, c, code, g, m, r, dx, dg_ptr, db_ptr)
+    return out, dgamma, dbeta
 
 
 def _heads_arg(t, what, like=None):
@@ -803,18 +828,18 @@ def _heads_arg(t, what, like=None):
     tensor whose dtype and device it must share."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor (got {t.device})")
-    if t.dim() != 3 or t.dtype not in _DTYPE_CODES:
+    shape = t.shape
+    if len(shape) != 3 or t.dtype not in _DTYPE_CODES:
         raise ValueError(f"{what} must be [N, heads, head_dim] float32 / float16 / bfloat16")
     row, head, channel = t.stride()
-    n, heads, dim = t.shape
-    if channel != 1 and dim > 1:
+    if channel != 1 and shape[2] > 1:
         raise ValueError(f"{what}: the channels of a head must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{what} must be {like.dtype} on {like.device}")
     # (a stride that no step takes is free: torch reports any value for it)
-    return _HeadsArg(t.data_ptr(), row if n > 1 else heads * dim, head if heads > 1 else dim)
+    return _HeadsArg(t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2], head if shape[1] > 1 else shape[2])
 
 
 def sparse_rope_frequencies(count: int, base: float = 10000.0, scaling: int = SUBM_ROPE_PLAIN, factor: float = 1.0,
@@ -834,23 +859,24 @@ def sparse_rope_frequencies(count: int, base: float = 10000.0, scaling: int = SU
 def _rope(func, x, positions, freq, layout, magnitude, out, stream):
     xa = _heads_arg(x, "x")
     n, heads, dim = x.shape
-    if not isinstance(positions, torch.Tensor) or positions.device != x.device or positions.dtype != torch.int32 or \
-            positions.dim() != 2 or positions.shape[0] != n or (positions.shape[1] > 1 and positions.stride(1) != 1):
+    device = x.get_device()
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.dim() != 2 or \
+            positions.shape[0] != n or not positions.is_cuda or positions.get_device() != device or \
+            (positions.shape[1] > 1 and positions.stride(1) != 1):
         raise ValueError("positions must be int32 [N, axes] on x's device, the axes contiguous")
     _device_tensor(freq, "freq")
-    if freq.dtype != torch.float32 or freq.dim() != 1 or freq.device != x.device:
+    if freq.dtype != torch.float32 or freq.dim() != 1 or freq.get_device() != device:
         raise ValueError("freq must be float32 [num_freq] on x's device")
-    y = _empty((n, heads, dim), x.dtype, x.device, stream) if out is None else out
-    ya = _heads_arg(y, "out", x)
-    if y.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    lib = load_library()
-    with _on_device(x.device):
-        st = getattr(lib, func)(xa, n, heads, dim, _DTYPE_CODES[x.dtype], positions.data_ptr(), positions.stride(0),
-                                positions.shape[1], freq.data_ptr(), freq.shape[0], layout, magnitude, ya,
-                                _stream_ptr(stream, x.device))
-    _check(lib, func, st)
-    return y
+    if out is None:
+        out = _empty((n, heads, dim), x.dtype, x.device, stream)
+        ya = _HeadsArg(out.data_ptr(), heads * dim, dim)
+    else:
+        ya = _heads_arg(out, "out", x)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    _run(func, device, stream, xa, n, heads, dim, _DTYPE_CODES[x.dtype], positions.data_ptr(), positions.stride(0),
+         positions.shape[1], freq.data_ptr(), freq.shape[0], layout, magnitude, ya)
+    return out
 
 
 def sparse_rope_forward(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, layout: int,
@@ -880,7 +906,8 @@ def _attention_args(q, k, v, q_offsets, k_offsets, scale):
         _offsets_arg(k_offsets)
         if k_offsets.shape != q_offsets.shape:
             raise ValueError("q_offsets and k_offsets must have the same items")
-    if q_offsets.device != q.device or k_offsets.device != q.device:
+    device = q.get_device()
+    if q_offsets.get_device() != device or k_offsets.get_device() != device:
         raise ValueError("offsets must be on q's device")
     if scale is None:
         scale = q.shape[2] ** -0.5
@@ -899,20 +926,18 @@ def sparse_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     nq, heads, dim = q.shape
     if out is None:
         out = _empty((nq, heads, dim), q.dtype, q.device, stream)
-    oa = _heads_arg(out, "out", q)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+        oa = _HeadsArg(out.data_ptr(), heads * dim, dim)
+    else:
+        oa = _heads_arg(out, "out", q)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if lse is None:
         lse = _empty((nq, heads), torch.float32, q.device, stream)
         lse_ptr = lse.data_ptr()
     else:
         lse_ptr = _vector(lse, (nq, heads), torch.float32, q.device, "lse")
-    lib = load_library()
-    with _on_device(q.device):
-        st = lib.sparse_attention_forward(qa, ka, va, nq, k.shape[0], q_offsets.data_ptr(), k_offsets.data_ptr(),
-                                          q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype], scale,
-                                          oa, lse_ptr, _stream_ptr(stream, q.device))
-    _check(lib, "sparse_attention_forward", st)
+    _run("sparse_attention_forward", q.get_device(), stream, qa, ka, va, nq, k.shape[0], q_offsets.data_ptr(),
+         k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype], scale, oa, lse_ptr)
     return out, lse
 
 
@@ -935,10 +960,7 @@ def sparse_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     if lse is None:
         raise ValueError("lse is required")
     lse_ptr = _vector(lse, (nq, heads), torch.float32, q.device, "lse")
-    lib = load_library()
-    with _on_device(q.device):
-        st = lib.sparse_attention_backward(ga, qa, ka, va, oa, lse_ptr, nq, k.shape[0], q_offsets.data_ptr(),
-                                           k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim,
-                                           _DTYPE_CODES[q.dtype], scale, dqa, dka, dva, _stream_ptr(stream, q.device))
-    _check(lib, "sparse_attention_backward", st)
+    _run("sparse_attention_backward", q.get_device(), stream, ga, qa, ka, va, oa, lse_ptr, nq, k.shape[0],
+         q_offsets.data_ptr(), k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype],
+         scale, dqa, dka, dva)
     return dq, dk, dv
