@@ -87,9 +87,9 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
 // three independent pieces of work, so that the matrix cores run while the exponentials do:
 //   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
 // (Four tiles of each in flight: the same time.)
-template <DT D, int DP, int W, int KEYS, int OCC, bool SPLIT>
+template <DT D, int DC, int W, int KEYS, int OCC, bool SPLIT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs a) {
-  constexpr int KB = KEYS / 32;
+  constexpr int DP = tile_width(DC), KB = KEYS / 32;
   constexpr int kTile = KEYS * kRowBytes<D, DP>;
   constexpr int kRows = 32 * W;
   using Loader = TileLoader<D, DP, KEYS, W>;
@@ -111,12 +111,12 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
 
   const int row = tile * kRows + wave * 32 + (lane & 31);
   const bool there = row < rows;
-  Frag<D> qf[DP / 16];
+  Frag<D> qf[DC / 16];
   const typename Elem<D>::T* qrow = qmap.at<D>(q, there ? row : 0);
   // a negative scale goes into q, so that the largest score is the largest product
   const uint32_t flip = a.scale < 0.f ? (D == DT::F32 ? 0x80000000u : 0x80008000u) : 0u;
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
+  for (int kk = 0; kk < DC / 16; ++kk) {
     qf[kk] = own_frag<D>(qrow, there, kk, a.head_dim, lane);
 #pragma unroll
     for (int i = 0; i < Elem<D>::kSize / 2; ++i) {
@@ -155,17 +155,17 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
     for (int kb = 0; kb < KB; ++kb) {
       s[kb] = zero16();
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) s[kb] = mma<D>(rd.row_frag(slot * kTile, kb * 32, kk), qf[kk], s[kb]);
+      for (int kk = 0; kk < DC / 16; ++kk) s[kb] = mma<D>(rd.row_frag(slot * kTile, kb * 32, kk), qf[kk], s[kb]);
     }
   };
-  f32x16_t acc[DP / 32];
+  f32x16_t acc[DC / 32];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db) acc[db] = zero16();
+  for (int db = 0; db < DC / 32; ++db) acc[db] = zero16();
   const auto product = [&](int slot, const Frag<D> (&p)[2 * KB]) {
 #pragma unroll
     for (int st = 0; st < 2 * KB; ++st)
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), p[st], acc[db]);
+      for (int db = 0; db < DC / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), p[st], acc[db]);
   };
 
   RowState state;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
       }
       if (moves) {
 #pragma unroll
-        for (int db = 0; db < DP / 32; ++db)
+        for (int db = 0; db < DC / 32; ++db)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[db][i] *= shrink;
       }
@@ -232,14 +232,14 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
     if (tiles == 0) return;
     float* o = a.part + at * DP;
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
+    for (int db = 0; db < DC / 32; ++db)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4*>(o + db * 32 + 8 * i + 4 * (lane >> 5)) =
             make_float4(acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]);
     return;
   }
-  store_row<D, DP>(qmap.at<D>(out, row), acc, tiles > 0 ? 1.f / sum : 0.f, a.head_dim, lane);
+  store_row<D, DC>(qmap.at<D>(out, row), acc, tiles > 0 ? 1.f / sum : 0.f, a.head_dim, lane);
   if (a.lse != nullptr && lane < 32)
     a.lse[qmap.stat(row, a.heads)] = tiles > 0 ? (state.base + log2f(sum)) * kLn2 : -INFINITY;
 }
@@ -299,17 +299,19 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   if (a.lse != nullptr && c == 0) a.lse[tok * a.heads + h] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
 }
 
-template <DT D, int DP, int W, bool SPLIT>
+template <DT D, int DC, int W, bool SPLIT>
 hipError_t launch_tiles(const FwdArgs& a, hipStream_t stream) {
+  constexpr int DP = tile_width(DC);
   constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
   const int64_t slots = a.nq * (a.heads / a.kv_heads) / (32 * W) + a.items;
-  attention_forward_kernel<D, DP, W, KEYS, OCC, SPLIT>
+  attention_forward_kernel<D, DC, W, KEYS, OCC, SPLIT>
       <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.splits : 1u), W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <DT D, int DP>
+template <DT D, int DC>
 Status launch(FwdArgs a, hipStream_t stream) {
+  constexpr int DP = tile_width(DC);
   // 128 channels: 8 waves on one tile stream halve what each row reads of it (24,576 tokens, 16
   // heads: 2.33 ms, 4 waves 2.80), where they fill the compute units.  64 channels: 4 waves and
   // three workgroups a compute unit, whose exponentials, the bound there, overlap (9,371 rows,
@@ -318,7 +320,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   const int64_t rows = a.nq * (a.heads / a.kv_heads);
   if constexpr (D != DT::F32 && DP == 128) {
     if ((rows / 256 + a.items) * a.kv_heads >= kUnits && rows / a.items >= 256) {
-      SUBM_HIP_TRY((launch_tiles<D, DP, 8, false>(a, stream)));
+      SUBM_HIP_TRY((launch_tiles<D, DC, 8, false>(a, stream)));
       return Status{};
     }
   }
@@ -328,7 +330,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   const int64_t blocks = (rows / 128 + a.items) * a.kv_heads;
   const int64_t want = std::min<int64_t>(2 * kUnits / blocks, a.nk / a.items / kShare);
   if (want < 2) {
-    SUBM_HIP_TRY((launch_tiles<D, DP, 4, false>(a, stream)));
+    SUBM_HIP_TRY((launch_tiles<D, DC, 4, false>(a, stream)));
     return Status{};
   }
   a.splits = (int)want;
@@ -340,7 +342,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   if (!st.ok()) return st;
   a.state = static_cast<float2*>(scratch);
   a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + state_bytes);
-  SUBM_HIP_TRY((launch_tiles<D, DP, 4, true>(a, stream)));
+  SUBM_HIP_TRY((launch_tiles<D, DC, 4, true>(a, stream)));
   constexpr int kRowsPer = 256 / (DP / 4);
   const int64_t joins = (rows * a.kv_heads + kRowsPer - 1) / kRowsPer;
   attention_join_kernel<D, DP><<<(unsigned)joins, 256, 0, stream>>>(a);
@@ -349,7 +351,10 @@ Status launch(FwdArgs a, hipStream_t stream) {
 }
 
 template <DT D> Status launch_dim(const FwdArgs& a, hipStream_t stream) {
-  return a.head_dim <= 64 ? launch<D, 64>(a, stream) : launch<D, 128>(a, stream);
+  if (a.head_dim <= 32) return launch<D, 32>(a, stream);
+  if (a.head_dim <= 64) return launch<D, 64>(a, stream);
+  if (a.head_dim <= 96) return launch<D, 96>(a, stream);
+  return launch<D, 128>(a, stream);
 }
 
 }  // namespace

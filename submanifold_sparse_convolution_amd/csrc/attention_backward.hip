@@ -71,9 +71,9 @@ template <DT D> __device__ __forceinline__ float dot_frag(const Frag<D>& a, cons
 }
 
 // A row's accumulator times `f` to a float32 copy.
-template <int DP> __device__ __forceinline__ void store_part(float* row, const f32x16_t (&acc)[DP / 32], float f, int lane) {
+template <int DC> __device__ __forceinline__ void store_part(float* row, const f32x16_t (&acc)[DC / 32], float f, int lane) {
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
+  for (int db = 0; db < DC / 32; ++db)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4*>(row + db * 32 + 8 * i + 4 * (lane >> 5)) =
@@ -83,9 +83,9 @@ template <int DP> __device__ __forceinline__ void store_part(float* row, const f
 // d of the own query rows, then dq over the keys, which stream through LDS in tiles of 32.  As in
 // the forward pass a step holds independent pieces of work:
 //   scores and dp of tile t + 1 (k, v),  e of tile t,  product of tile t - 1 (k).
-template <DT D, int DP, int W, int OCC, bool SPLIT>
+template <DT D, int DC, int W, int OCC, bool SPLIT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
-  constexpr int kRows = 32 * W;
+  constexpr int DP = tile_width(DC), kRows = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
   using Loader = TileLoader<D, DP, kStep, W>;
   __shared__ __attribute__((aligned(1024))) unsigned char s_kv[6 * kTile];  // four tiles of k, two of v
@@ -108,13 +108,13 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   const int row = tile * kRows + wave * 32 + (lane & 31);
   const bool there = row < rows;
   const int safe = there ? row : 0;
-  Frag<D> qf[DP / 16], gf[DP / 16];  // own rows of q and dout
+  Frag<D> qf[DC / 16], gf[DC / 16];  // own rows of q and dout
   const typename Elem<D>::T* qrow = qmap.at<D>(heads_of<D>(a.q), safe);
   const typename Elem<D>::T* grow = qmap.at<D>(heads_of<D>(a.dout), safe);
   const typename Elem<D>::T* orow = qmap.at<D>(heads_of<D>(a.out), safe);
   float d = 0.f, peak = 0.f;
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
+  for (int kk = 0; kk < DC / 16; ++kk) {
     qf[kk] = own_frag<D>(qrow, there, kk, a.head_dim, lane);
     gf[kk] = own_frag<D>(grow, there, kk, a.head_dim, lane);
     d = dot_frag<D>(gf[kk], own_frag<D>(orow, there, kk, a.head_dim, lane), d);
@@ -167,19 +167,19 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     s = zero16();
     dp = zero16();
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
+    for (int kk = 0; kk < DC / 16; ++kk) {
       s = mma<D>(rd.row_frag(slot * kTile, 0, kk), qf[kk], s);
       dp = mma<D>(rd.row_frag((4 + slot % 2) * kTile, 0, kk), gf[kk], dp);
     }
   };
-  f32x16_t acc[DP / 32];
+  f32x16_t acc[DC / 32];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db) acc[db] = zero16();
+  for (int db = 0; db < DC / 32; ++db) acc[db] = zero16();
   const auto product = [&](int slot, const Frag<D> (&e)[2]) {
 #pragma unroll
     for (int st = 0; st < 2; ++st)
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), e[st], acc[db]);
+      for (int db = 0; db < DC / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), e[st], acc[db]);
   };
   if (tiles > 0) {
     // Step t reads k and v of tile t + 1 and k of tile t - 1 and starts the loads of tile t + 2.
@@ -231,10 +231,10 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   }
   if (!there) return;
   if constexpr (SPLIT)
-    store_part<DP>(a.dq_part + (((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row) * DP, acc,
+    store_part<DC>(a.dq_part + (((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row) * DP, acc,
                    a.scale / unit, lane);
   else
-    store_row<D, DP>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
+    store_row<D, DC>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
 }
 
 // The next 32 of `left` floats (zeros past them) straight to LDS, which takes 64 of them.
@@ -253,9 +253,9 @@ __device__ __forceinline__ void load_stats(const float* p, int left, uint32_t ld
 // stream through LDS in tiles of 32.  Two waves a SIMD overlap each other's exponentials and
 // products.  At 128 channels in 16 bits the own rows of v stay in LDS: with the two accumulators
 // and k there is no room for them in 256 registers.
-template <DT D, int DP, int W, int OCC, bool SPLIT>
+template <DT D, int DC, int W, int OCC, bool SPLIT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
-  constexpr int kKeys = 32 * W;
+  constexpr int DP = tile_width(DC), kKeys = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
   constexpr bool kParked = D != DT::F32 && DP == 128;
   using Loader = TileLoader<D, DP, kStep, W>;
@@ -299,11 +299,11 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   const uint32_t lds = lds_offset(s_qg);
   const int key = tile * kKeys + wave * 32 + (lane & 31);
   const bool there = key < nk;
-  Frag<D> kf[DP / 16], vf[kParked ? 1 : DP / 16];
+  Frag<D> kf[DC / 16], vf[kParked ? 1 : DC / 16];
   const typename Elem<D>::T* krow = kmap.at<D>(heads_of<D>(a.k), there ? key : 0);
   const typename Elem<D>::T* vrow = kmap.at<D>(v, there ? key : 0);
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
+  for (int kk = 0; kk < DC / 16; ++kk) {
     kf[kk] = own_frag<D>(krow, there, kk, a.head_dim, lane);
     if constexpr (!kParked) vf[kk] = own_frag<D>(vrow, there, kk, a.head_dim, lane);
   }
@@ -351,9 +351,9 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     }
   };
   const float c = a.scale * kLog2e;
-  f32x16_t dk[DP / 32], dv[DP / 32];
+  f32x16_t dk[DC / 32], dv[DC / 32];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db) dk[db] = dv[db] = zero16();
+  for (int db = 0; db < DC / 32; ++db) dk[db] = dv[db] = zero16();
   const auto step = [&](int slot) {
     wait_lgkmcnt0();
     wait_vmcnt<0>();
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     load(slot ^ 1);
     f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
+    for (int kk = 0; kk < DC / 16; ++kk) {
       s = mma<D>(rd.row_frag(slot * kTile, 0, kk), kf[kk], s);
       if constexpr (kParked) dp = mma<D>(rd.row_frag((2 + slot) * kTile, 0, kk), rd.row_frag(4 * kTile + own, 0, kk), dp);
       else dp = mma<D>(rd.row_frag((2 + slot) * kTile, 0, kk), vf[kk], dp);
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     for (int st = 0; st < 2; ++st) {
       const Frag<D> p = to_frag<D>(s, st), e = to_frag<D>(dp, st);
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db) {
+      for (int db = 0; db < DC / 32; ++db) {
         dv[db] = mma<D>(rd.column_frag((2 + slot) * kTile, st * 16, db), p, dv[db]);
         dk[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), e, dk[db]);
       }
@@ -401,11 +401,11 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   if (!there) return;
   if constexpr (SPLIT) {
     const int64_t at = (((int64_t)blockIdx.z * a.kv_heads + head) * a.nk + k0 + key) * DP;
-    store_part<DP>(a.dk_part + at, dk, a.scale / unit, lane);
-    store_part<DP>(a.dv_part + at, dv, p_unit, lane);
+    store_part<DC>(a.dk_part + at, dk, a.scale / unit, lane);
+    store_part<DC>(a.dv_part + at, dv, p_unit, lane);
   } else {
-    store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, lane);
-    store_row<D, DP>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, lane);
+    store_row<D, DC>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, lane);
+    store_row<D, DC>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, lane);
   }
 }
 
@@ -436,18 +436,18 @@ __global__ __launch_bounds__(256) void attention_sum_kernel(BwdArgs a) {
   store4<D>(out.data + tok * out.row + (int64_t)h * out.head + c, o.x, o.y, o.z, o.w);
 }
 
-template <DT D, int DP, int W, bool SPLIT> hipError_t launch_dq(BwdArgs& a, hipStream_t stream) {
-  constexpr int OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
+template <DT D, int DC, int W, bool SPLIT> hipError_t launch_dq(BwdArgs& a, hipStream_t stream) {
+  constexpr int OCC = D == DT::F32 ? 1 : DC <= 64 ? 3 : 2;
   a.q_rows = 32 * W;
   a.q_slots = a.nq * (a.heads / a.kv_heads) / a.q_rows + a.items;
-  attention_dq_kernel<D, DP, W, OCC, SPLIT>
+  attention_dq_kernel<D, DC, W, OCC, SPLIT>
       <<<dim3((unsigned)a.q_slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.q_splits : 1u), W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
-template <DT D, int DP, int W, bool SPLIT> hipError_t launch_dkv(const BwdArgs& a, hipStream_t stream) {
-  constexpr int OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
+template <DT D, int DC, int W, bool SPLIT> hipError_t launch_dkv(const BwdArgs& a, hipStream_t stream) {
+  constexpr int OCC = D == DT::F32 ? 1 : DC <= 64 ? 3 : 2;
   const int64_t slots = a.nk / (32 * W) + a.items;
-  attention_dkv_kernel<D, DP, W, OCC, SPLIT>
+  attention_dkv_kernel<D, DC, W, OCC, SPLIT>
       <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.k_splits : 1u), W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
@@ -458,8 +458,9 @@ int splits_for(int64_t blocks, int64_t walked, int per_unit, int least) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(per_unit * 256 / std::max<int64_t>(blocks, 1), walked / least));
 }
 
-template <DT D, int DP>
+template <DT D, int DC>
 Status launch(BwdArgs a, hipStream_t stream) {
+  constexpr int DP = tile_width(DC);
   const int group = a.heads / a.kv_heads;
   const int64_t rows = a.nq * group;
   // 128 channels in 16 bits: 8 waves share a tile stream where they fill the compute units.
@@ -496,15 +497,15 @@ Status launch(BwdArgs a, hipStream_t stream) {
   }
   if (a.nq > 0) {
     if constexpr (kWide) {
-      if (wide_q) SUBM_HIP_TRY((launch_dq<D, DP, 8, false>(a, stream)));
+      if (wide_q) SUBM_HIP_TRY((launch_dq<D, DC, 8, false>(a, stream)));
     }
-    if (!wide_q) SUBM_HIP_TRY((a.q_splits > 1 ? launch_dq<D, DP, 4, true>(a, stream) : launch_dq<D, DP, 4, false>(a, stream)));
+    if (!wide_q) SUBM_HIP_TRY((a.q_splits > 1 ? launch_dq<D, DC, 4, true>(a, stream) : launch_dq<D, DC, 4, false>(a, stream)));
   }
   if (a.nk > 0) {
     if constexpr (kWide) {
-      if (wide_k) SUBM_HIP_TRY((launch_dkv<D, DP, 8, false>(a, stream)));
+      if (wide_k) SUBM_HIP_TRY((launch_dkv<D, DC, 8, false>(a, stream)));
     }
-    if (!wide_k) SUBM_HIP_TRY((a.k_splits > 1 ? launch_dkv<D, DP, 4, true>(a, stream) : launch_dkv<D, DP, 4, false>(a, stream)));
+    if (!wide_k) SUBM_HIP_TRY((a.k_splits > 1 ? launch_dkv<D, DC, 4, true>(a, stream) : launch_dkv<D, DC, 4, false>(a, stream)));
   }
   const int jobs = (part_q > 0 ? 1 : 0) + (part_k > 0 ? 2 : 0);
   if (jobs > 0) {
@@ -517,7 +518,10 @@ Status launch(BwdArgs a, hipStream_t stream) {
 }
 
 template <DT D> Status launch_dim(const BwdArgs& a, hipStream_t stream) {
-  return a.head_dim <= 64 ? launch<D, 64>(a, stream) : launch<D, 128>(a, stream);
+  if (a.head_dim <= 32) return launch<D, 32>(a, stream);
+  if (a.head_dim <= 64) return launch<D, 64>(a, stream);
+  if (a.head_dim <= 96) return launch<D, 96>(a, stream);
+  return launch<D, 128>(a, stream);
 }
 
 }  // namespace

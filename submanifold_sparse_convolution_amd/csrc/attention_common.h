@@ -141,6 +141,12 @@ __device__ __forceinline__ void item_rows(const int64_t* offsets, int64_t total,
 // waves: 254 and 229 bytes a clock and compute unit at 128 channels, against 127 and 63 with the
 // plain c ^ (r & 7).
 
+//
+// The kernels come for DC = 32, 64, 96 and 128 computed channels; tiles are DP = 64 or 128 wide
+// (the channels past head_dim read zeros), and what a narrow head need not compute it skips.
+
+constexpr int tile_width(int dc) { return dc <= 64 ? 64 : 128; }
+
 template <DT D, int DP> constexpr int kRowChunks = DP * Elem<D>::kSize / 16;
 template <DT D, int DP> constexpr int kRowBytes = DP * Elem<D>::kSize;
 
@@ -288,12 +294,12 @@ template <DT D> __device__ __forceinline__ void store4(typename Elem<D>::T* p, f
   else *reinterpret_cast<uint2*>(p) = pack4<D>(a, b, c, d);
 }
 
-// Accumulator tiles [DP / 32] (row = channel, column = own row) to the row, times `f`.
-template <DT D, int DP>
-__device__ __forceinline__ void store_row(typename Elem<D>::T* row, const f32x16_t (&acc)[DP / 32], float f, int head_dim,
+// Accumulator tiles [DC / 32] (row = channel, column = own row) to the row, times `f`.
+template <DT D, int DC>
+__device__ __forceinline__ void store_row(typename Elem<D>::T* row, const f32x16_t (&acc)[DC / 32], float f, int head_dim,
                                           int lane) {
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
+  for (int db = 0; db < DC / 32; ++db)
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int c = db * 32 + 8 * a + 4 * (lane >> 5);
