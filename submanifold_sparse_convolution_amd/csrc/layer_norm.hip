@@ -55,8 +55,10 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
 }
 
 // Workgroups of the backward pass, each a partial weight gradient: the four a compute unit that are
-// resident at 1,024 16-bit channels (135,826 rows: 160 us; two 238, three 180, eight 170).
+// resident (1,024 16-bit channels, 135,826 rows: 160 us; two 238, three 180, eight 170), two with
+// three chunks a lane (60,000 x 700 float32: 95 us, four 103).
 constexpr int kPartsLimit = 256 * 4;
+int parts_limit(int chunks) { return chunks > 128 && chunks <= 192 ? 256 * 2 : kPartsLimit; }
 
 constexpr int threads_for(int tpr) { return tpr > 256 ? tpr : 256; }
 
@@ -280,10 +282,14 @@ void launch(const Backward& b, int64_t n, int channels, int blocks, hipStream_t 
 }
 
 // Lanes of a row.  A lane holds up to 4 chunks in the forward pass and 2 in the backward pass,
-// whose gradients and weights stay in registers too (up to 16,384 channels; beyond, float32 rows
-// would not fit).
+// whose gradients and weights stay in registers too, or 3 where a wave then spares a row its
+// barriers (60,000 x 700 float32: 95 us, four waves a row 107); up to 16,384 channels, beyond which
+// float32 rows would not fit.
 int lanes_for(const Forward&, int chunks) { return chunks <= 256 ? 64 : chunks <= 1024 ? 256 : 1024; }
-int lanes_for(const Backward&, int chunks) { return chunks <= 128 ? 64 : chunks <= 512 ? 256 : 1024; }
+int lanes_for(const Backward&, int chunks) { return chunks <= 192 ? 64 : chunks <= 512 ? 256 : 1024; }
+
+int limit_for(const Forward&, int) { return kGridLimit; }
+int limit_for(const Backward&, int chunks) { return parts_limit(chunks); }
 
 template <DT D, bool TAIL>
 hipError_t launch_rows(const Forward& a, int64_t n, int channels, int chunks, int blocks, hipStream_t stream) {
@@ -300,6 +306,7 @@ template <DT D, bool TAIL>
 hipError_t launch_rows(const Backward& a, int64_t n, int channels, int chunks, int blocks, hipStream_t stream) {
   if (chunks <= 64) launch<D, 64, 1, TAIL>(a, n, channels, blocks, stream);
   else if (chunks <= 128) launch<D, 64, 2, TAIL>(a, n, channels, blocks, stream);
+  else if (chunks <= 192) launch<D, 64, 3, TAIL>(a, n, channels, blocks, stream);
   else if (chunks <= 256) launch<D, 256, 1, TAIL>(a, n, channels, blocks, stream);
   else if (chunks <= 512) launch<D, 256, 2, TAIL>(a, n, channels, blocks, stream);
   else if (chunks <= 1024) launch<D, 1024, 1, TAIL>(a, n, channels, blocks, stream);
@@ -323,10 +330,10 @@ hipError_t launch_dtype(const A& a, int64_t n, int channels, int dtype, int bloc
   return launch_ends<DT::BF16>(a, n, channels, blocks, stream);
 }
 
-template <typename A> int blocks_for(const A& a, int64_t n, int channels, int dtype, int limit) {
-  const int chunk = dtype == SUBM_F32 ? 4 : 8;
-  const int rows = rows_per_block(lanes_for(a, (channels + chunk - 1) / chunk));
-  return (int)std::min<int64_t>((n + rows - 1) / rows, limit);
+template <typename A> int blocks_for(const A& a, int64_t n, int channels, int dtype) {
+  const int chunk = dtype == SUBM_F32 ? 4 : 8, chunks = (channels + chunk - 1) / chunk;
+  const int rows = rows_per_block(lanes_for(a, chunks));
+  return (int)std::min<int64_t>((n + rows - 1) / rows, limit_for(a, chunks));
 }
 
 Status check_layer_norm(int64_t n, int channels, int dtype) {
@@ -361,7 +368,7 @@ extern "C" int sparse_layer_norm_forward(const void* x, int64_t n, int channels,
       misaligned(mean, 4) || misaligned(rstd, 4))
     return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
   const Forward f{x, gamma, beta, y, mean, rstd, eps};
-  const hipError_t e = launch_dtype(f, n, channels, dtype, blocks_for(f, n, channels, dtype, kGridLimit), stream);
+  const hipError_t e = launch_dtype(f, n, channels, dtype, blocks_for(f, n, channels, dtype), stream);
   if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_forward launch"));
   return SUBM_OK;
 }
@@ -381,7 +388,7 @@ extern "C" int sparse_layer_norm_backward(const void* dy, const void* x, int64_t
     return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
   if (n == 0 && dgamma == nullptr) return SUBM_OK;
   Backward b{dy, x, gamma, mean, rstd, dx, nullptr};
-  const int blocks = blocks_for(b, n, channels, dtype, kPartsLimit);
+  const int blocks = blocks_for(b, n, channels, dtype);
   if (dgamma != nullptr) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
