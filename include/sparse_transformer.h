@@ -13,6 +13,12 @@
  * Rows (tokens) of all items are concatenated; item b holds rows offsets[b] .. offsets[b+1] - 1.
  * No call synchronises.  Every result is bitwise reproducible from run to run: no sum goes
  * through atomics.
+ *
+ * sparse_layer_norm_backward (with weight gradients), sparse_attention_forward (few query rows)
+ * and sparse_attention_backward keep partial results in scratch memory of the stream, which grows
+ * to the largest call so far and is given back by subm_release_cached_memory.  It cannot grow
+ * under graph capture (SUBM_ERR_UNSUPPORTED): make the call once on the capturing stream before.
+ * A captured call stays valid until subm_release_cached_memory; its replays run on that stream.
  */
 #ifndef SPARSE_TRANSFORMER_H
 #define SPARSE_TRANSFORMER_H
@@ -144,11 +150,13 @@ int sparse_rope_backward(const subm_heads_t* dy, int64_t n, int heads, int head_
  *   items        1 .. 65535.  Items without queries or without keys are allowed: a query without
  *                keys gets out = 0 and lse = -infinity.
  *   nq, nk       0 .. 2^31 - 1, and nq * heads <= 2^31 - 1.
+ *   heads        at most 128 a key head.
  *   head_dim     a multiple of 8, 8 .. 128.  data 16-byte aligned, strides multiples of 16 bytes
  *                (else SUBM_ERR_UNSUPPORTED); row strides of at most 2^22 bytes, head strides of at
  *                most 2^22 bytes.
  *   scale        finite.
  *   lse          device float32 [nq, heads], or NULL.
+ *   out          may be q (same strides); it must not overlap k or v.
  * Scores, the running maximum and sum, and out accumulate in float32.  With 16-bit storage the
  * probabilities are rounded to it for the product with v.  Rows of one item never meet values of
  * another, whatever they hold.  When there are few query rows the keys are split over workgroups
@@ -166,6 +174,7 @@ int sparse_attention_forward(const subm_heads_t* q, const subm_heads_t* k, const
  *   ds = scale p (dp - d),  dq = ds k,  dk = ds^T q,  dv = p^T dout,
  * dk and dv summed over the query heads that share a key head.
  *   dout, out, dq  nq rows of `heads` heads;  dk, dv  nk rows of `kv_heads` heads, overwritten.
+ *                  The gradients must not overlap an input or each other.
  *   lse            the forward pass's, required.
  * A query without keys gets dq = 0, a key without queries dk = dv = 0.  With 16-bit storage p and
  * ds are rounded to it for their products; with SUBM_F16 both are scaled by powers of two first

@@ -336,6 +336,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   a.splits = (int)want;
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));
+  const auto launches = scratch_launch_lock(dev);
   const size_t state_bytes = ((size_t)a.splits * rows * a.kv_heads * sizeof(float2) + 255) / 256 * 256;
   void* scratch = nullptr;
   Status st = stream_scratch(dev, stream, state_bytes + (size_t)a.splits * rows * a.kv_heads * DP * sizeof(float), &scratch);
@@ -408,20 +409,23 @@ extern "C" int sparse_attention_forward(const subm_heads_t* q, const subm_heads_
                                         int64_t nk, const int64_t* q_offsets, const int64_t* k_offsets, int items,
                                         int heads, int kv_heads, int head_dim, int dtype, float scale,
                                         const subm_heads_t* out, float* lse, hipStream_t stream) {
-  clear_error();
-  const AttentionShape shape{nq, nk, q_offsets, k_offsets, items, heads, kv_heads, head_dim, dtype, scale};
-  Status st = check_attention(shape);
-  if (st.ok()) st = check_heads(q, nq, heads, shape, false, "q");
-  if (st.ok()) st = check_heads(k, nk, kv_heads, shape, false, "k");
-  if (st.ok()) st = check_heads(v, nk, kv_heads, shape, false, "v");
-  if (st.ok()) st = check_heads(out, nq, heads, shape, true, "out");
-  if (!st.ok()) return fail(st);
-  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
-  if (nq == 0) return SUBM_OK;
-  const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads, head_dim, scale, 1, nullptr, nullptr};
-  if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
-  else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
-  else st = launch_dim<DT::BF16>(a, stream);
-  if (!st.ok()) return fail(st);
-  return SUBM_OK;
+  return no_throw([&]() -> int {
+    clear_error();
+    const AttentionShape shape{nq, nk, q_offsets, k_offsets, items, heads, kv_heads, head_dim, dtype, scale};
+    Status st = check_attention(shape);
+    if (st.ok()) st = check_heads(q, nq, heads, shape, false, "q");
+    if (st.ok()) st = check_heads(k, nk, kv_heads, shape, false, "k");
+    if (st.ok()) st = check_heads(v, nk, kv_heads, shape, false, "v");
+    if (st.ok()) st = check_heads(out, nq, heads, shape, true, "out");
+    if (!st.ok()) return fail(st);
+    if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+    if (nq == 0) return SUBM_OK;
+    if (out->data == k->data || out->data == v->data) return fail(SUBM_ERR_INVALID_ARG, "out must not alias k or v");
+    const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads, head_dim, scale, 1, nullptr, nullptr};
+    if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
+    else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
+    else st = launch_dim<DT::BF16>(a, stream);
+    if (!st.ok()) return fail(st);
+    return SUBM_OK;
+  });
 }

@@ -476,6 +476,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
 
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));
+  const auto launches = scratch_launch_lock(dev);
   const auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
   // norm and d of every query row, a peak for each of the smallest query blocks, and the copies
   const size_t stat = padded((size_t)rows * a.kv_heads * sizeof(float));
@@ -535,44 +536,52 @@ extern "C" int sparse_attention_backward(const subm_heads_t* dout, const subm_he
                                          int heads, int kv_heads, int head_dim, int dtype, float scale,
                                          const subm_heads_t* dq, const subm_heads_t* dk, const subm_heads_t* dv,
                                          hipStream_t stream) {
-  clear_error();
-  const AttentionShape shape{nq, nk, q_offsets, k_offsets, items, heads, kv_heads, head_dim, dtype, scale};
-  Status st = check_attention(shape);
-  if (st.ok()) st = check_heads(dout, nq, heads, shape, false, "dout");
-  if (st.ok()) st = check_heads(q, nq, heads, shape, false, "q");
-  if (st.ok()) st = check_heads(k, nk, kv_heads, shape, false, "k");
-  if (st.ok()) st = check_heads(v, nk, kv_heads, shape, false, "v");
-  if (st.ok()) st = check_heads(out, nq, heads, shape, false, "out");
-  if (st.ok()) st = check_heads(dq, nq, heads, shape, true, "dq");
-  if (st.ok()) st = check_heads(dk, nk, kv_heads, shape, true, "dk");
-  if (st.ok()) st = check_heads(dv, nk, kv_heads, shape, true, "dv");
-  if (!st.ok()) return fail(st);
-  if (nq > 0 && lse == nullptr) return fail(SUBM_ERR_INVALID_ARG, "lse is NULL");
-  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
-  if (nq == 0 && nk == 0) return SUBM_OK;
-  BwdArgs a{};
-  a.dout = *dout;
-  a.q = *q;
-  a.k = *k;
-  a.v = *v;
-  a.out = *out;
-  a.dq = *dq;
-  a.dk = *dk;
-  a.dv = *dv;
-  a.lse = lse;
-  a.q_offsets = q_offsets;
-  a.k_offsets = k_offsets;
-  a.nq = nq;
-  a.nk = nk;
-  a.items = items;
-  a.heads = heads;
-  a.kv_heads = kv_heads;
-  a.head_dim = head_dim;
-  a.scale = scale;
-  a.q_splits = a.k_splits = 1;
-  if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
-  else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
-  else st = launch_dim<DT::BF16>(a, stream);
-  if (!st.ok()) return fail(st);
-  return SUBM_OK;
+  return no_throw([&]() -> int {
+    clear_error();
+    const AttentionShape shape{nq, nk, q_offsets, k_offsets, items, heads, kv_heads, head_dim, dtype, scale};
+    Status st = check_attention(shape);
+    if (st.ok()) st = check_heads(dout, nq, heads, shape, false, "dout");
+    if (st.ok()) st = check_heads(q, nq, heads, shape, false, "q");
+    if (st.ok()) st = check_heads(k, nk, kv_heads, shape, false, "k");
+    if (st.ok()) st = check_heads(v, nk, kv_heads, shape, false, "v");
+    if (st.ok()) st = check_heads(out, nq, heads, shape, false, "out");
+    if (st.ok()) st = check_heads(dq, nq, heads, shape, true, "dq");
+    if (st.ok()) st = check_heads(dk, nk, kv_heads, shape, true, "dk");
+    if (st.ok()) st = check_heads(dv, nk, kv_heads, shape, true, "dv");
+    if (!st.ok()) return fail(st);
+    if (nq > 0 && lse == nullptr) return fail(SUBM_ERR_INVALID_ARG, "lse is NULL");
+    if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+    if (nq == 0 && nk == 0) return SUBM_OK;
+    // (the second kernel reads every input after the first has written dq)
+    for (const subm_heads_t* w : {dq, dk, dv})
+      for (const subm_heads_t* r : {dout, q, k, v, out})
+        if (w->data != nullptr && w->data == r->data) return fail(SUBM_ERR_INVALID_ARG, "a gradient must not alias an input");
+    if (nq > 0 && nk > 0 && (dq->data == dk->data || dq->data == dv->data)) return fail(SUBM_ERR_INVALID_ARG, "dq, dk and dv must not alias");
+    if (nk > 0 && dk->data == dv->data) return fail(SUBM_ERR_INVALID_ARG, "dq, dk and dv must not alias");
+    BwdArgs a{};
+    a.dout = *dout;
+    a.q = *q;
+    a.k = *k;
+    a.v = *v;
+    a.out = *out;
+    a.dq = *dq;
+    a.dk = *dk;
+    a.dv = *dv;
+    a.lse = lse;
+    a.q_offsets = q_offsets;
+    a.k_offsets = k_offsets;
+    a.nq = nq;
+    a.nk = nk;
+    a.items = items;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.head_dim = head_dim;
+    a.scale = scale;
+    a.q_splits = a.k_splits = 1;
+    if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
+    else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
+    else st = launch_dim<DT::BF16>(a, stream);
+    if (!st.ok()) return fail(st);
+    return SUBM_OK;
+  });
 }

@@ -39,6 +39,15 @@ void clear_error();
 int fail(const Status& s);
 int fail(int code, const char* msg);
 
+// Body of a C entry point: nothing is thrown across it (a failed host allocation is a status).
+template <typename F> int no_throw(F&& body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return SUBM_ERR_OUT_OF_MEMORY;
+  }
+}
+
 // Per-thread, per-device pinned host block of kPinnedBytes that the device can write (for the
 // few words a build reads back after its synchronisation).  host == nullptr on failure.
 constexpr size_t kPinnedBytes = 4096;
@@ -292,7 +301,11 @@ hipError_t launch_pool_conv(const PoolTiling& t, const void* plan, const uint32_
 
 // Per-(device, stream) scratch of at least `bytes`, reused by every call on that stream (work on
 // one stream is ordered, so a later call cannot overwrite it while an earlier one still reads
-// it); grows by a stream-ordered free and allocation (submconv_api.hip).
+// it); grows by a stream-ordered allocation and keeps what it outgrows; SUBM_ERR_UNSUPPORTED when
+// it would have to grow under graph capture (submconv_api.hip).  The caller holds
+// scratch_launch_lock from before the call until its last launch that uses the memory: launches of
+// two threads on one stream must not interleave on it.
+std::unique_lock<std::mutex> scratch_launch_lock(int dev);
 Status stream_scratch(int dev, hipStream_t stream, size_t bytes, void** ptr);
 
 }  // namespace submconv

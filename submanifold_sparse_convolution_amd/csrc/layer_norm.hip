@@ -356,65 +356,71 @@ using namespace submconv;
 extern "C" int sparse_layer_norm_forward(const void* x, int64_t n, int channels, int dtype, const void* gamma,
                                          const void* beta, float eps, void* y, float* mean, float* rstd,
                                          hipStream_t stream) {
-  clear_error();
-  Status st = check_layer_norm(n, channels, dtype);
-  if (!st.ok()) return fail(st);
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(SUBM_ERR_INVALID_ARG, "eps must be positive and finite");
-  if ((mean == nullptr) != (rstd == nullptr)) return fail(SUBM_ERR_INVALID_ARG, "mean and rstd go together");
-  if (n == 0) return SUBM_OK;
-  if (x == nullptr || y == nullptr) return fail(SUBM_ERR_INVALID_ARG, "x or y is NULL");
-  const int elem = dtype == SUBM_F32 ? 4 : 2;
-  if (misaligned(x, elem) || misaligned(y, elem) || misaligned(gamma, elem) || misaligned(beta, elem) ||
-      misaligned(mean, 4) || misaligned(rstd, 4))
-    return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
-  const Forward f{x, gamma, beta, y, mean, rstd, eps};
-  const hipError_t e = launch_dtype(f, n, channels, dtype, blocks_for(f, n, channels, dtype), stream);
-  if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_forward launch"));
-  return SUBM_OK;
+  return no_throw([&]() -> int {
+    clear_error();
+    Status st = check_layer_norm(n, channels, dtype);
+    if (!st.ok()) return fail(st);
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(SUBM_ERR_INVALID_ARG, "eps must be positive and finite");
+    if ((mean == nullptr) != (rstd == nullptr)) return fail(SUBM_ERR_INVALID_ARG, "mean and rstd go together");
+    if (n == 0) return SUBM_OK;
+    if (x == nullptr || y == nullptr) return fail(SUBM_ERR_INVALID_ARG, "x or y is NULL");
+    const int elem = dtype == SUBM_F32 ? 4 : 2;
+    if (misaligned(x, elem) || misaligned(y, elem) || misaligned(gamma, elem) || misaligned(beta, elem) ||
+        misaligned(mean, 4) || misaligned(rstd, 4))
+      return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
+    const Forward f{x, gamma, beta, y, mean, rstd, eps};
+    const hipError_t e = launch_dtype(f, n, channels, dtype, blocks_for(f, n, channels, dtype), stream);
+    if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_forward launch"));
+    return SUBM_OK;
+  });
 }
 
 extern "C" int sparse_layer_norm_backward(const void* dy, const void* x, int64_t n, int channels, int dtype,
                                           const void* gamma, const float* mean, const float* rstd, void* dx,
                                           void* dgamma, void* dbeta, hipStream_t stream) {
-  clear_error();
-  Status st = check_layer_norm(n, channels, dtype);
-  if (!st.ok()) return fail(st);
-  if ((dgamma == nullptr) != (dbeta == nullptr)) return fail(SUBM_ERR_INVALID_ARG, "dgamma and dbeta go together");
-  const int elem = dtype == SUBM_F32 ? 4 : 2;
-  if (n > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
-    return fail(SUBM_ERR_INVALID_ARG, "dy, x, mean, rstd or dx is NULL");
-  if (misaligned(dy, elem) || misaligned(x, elem) || misaligned(gamma, elem) || misaligned(dx, elem) ||
-      misaligned(dgamma, elem) || misaligned(dbeta, elem) || misaligned(mean, 4) || misaligned(rstd, 4))
-    return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
-  if (n == 0 && dgamma == nullptr) return SUBM_OK;
-  Backward b{dy, x, gamma, mean, rstd, dx, nullptr};
-  const int blocks = blocks_for(b, n, channels, dtype);
-  if (dgamma != nullptr) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return fail(hip_status(e, "hipGetDevice"));
-    void* scratch = nullptr;
-    st = stream_scratch(dev, stream, std::max<size_t>((size_t)blocks * 2 * channels * sizeof(float), 16), &scratch);
+  return no_throw([&]() -> int {
+    clear_error();
+    Status st = check_layer_norm(n, channels, dtype);
     if (!st.ok()) return fail(st);
-    b.part = static_cast<float*>(scratch);
-  }
-  hipError_t e = hipSuccess;
-  if (n > 0) {
-    e = launch_dtype(b, n, channels, dtype, blocks, stream);
-  }
-  if (e == hipSuccess && dgamma != nullptr) {
-    const int grid = (2 * channels + kSumColumns - 1) / kSumColumns;
-    if (dtype == SUBM_F32)
-      layer_norm_weight_grad_kernel<DT::F32><<<grid, kSumColumns * kSumRows, 0, stream>>>(b.part, blocks, channels, static_cast<float*>(dgamma),
-                                                                       static_cast<float*>(dbeta));
-    else if (dtype == SUBM_F16)
-      layer_norm_weight_grad_kernel<DT::F16><<<grid, kSumColumns * kSumRows, 0, stream>>>(
-          b.part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
-    else
-      layer_norm_weight_grad_kernel<DT::BF16><<<grid, kSumColumns * kSumRows, 0, stream>>>(
-          b.part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
-    e = hipGetLastError();
-  }
-  if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_backward launch"));
-  return SUBM_OK;
+    if ((dgamma == nullptr) != (dbeta == nullptr)) return fail(SUBM_ERR_INVALID_ARG, "dgamma and dbeta go together");
+    const int elem = dtype == SUBM_F32 ? 4 : 2;
+    if (n > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
+      return fail(SUBM_ERR_INVALID_ARG, "dy, x, mean, rstd or dx is NULL");
+    if (misaligned(dy, elem) || misaligned(x, elem) || misaligned(gamma, elem) || misaligned(dx, elem) ||
+        misaligned(dgamma, elem) || misaligned(dbeta, elem) || misaligned(mean, 4) || misaligned(rstd, 4))
+      return fail(SUBM_ERR_INVALID_ARG, "a pointer is not aligned to its element");
+    if (n == 0 && dgamma == nullptr) return SUBM_OK;
+    Backward b{dy, x, gamma, mean, rstd, dx, nullptr};
+    const int blocks = blocks_for(b, n, channels, dtype);
+    std::unique_lock<std::mutex> launches;
+    if (dgamma != nullptr) {
+      int dev = 0;
+      hipError_t e = hipGetDevice(&dev);
+      if (e != hipSuccess) return fail(hip_status(e, "hipGetDevice"));
+      launches = scratch_launch_lock(dev);
+      void* scratch = nullptr;
+      st = stream_scratch(dev, stream, std::max<size_t>((size_t)blocks * 2 * channels * sizeof(float), 16), &scratch);
+      if (!st.ok()) return fail(st);
+      b.part = static_cast<float*>(scratch);
+    }
+    hipError_t e = hipSuccess;
+    if (n > 0) {
+      e = launch_dtype(b, n, channels, dtype, blocks, stream);
+    }
+    if (e == hipSuccess && dgamma != nullptr) {
+      const int grid = (2 * channels + kSumColumns - 1) / kSumColumns;
+      if (dtype == SUBM_F32)
+        layer_norm_weight_grad_kernel<DT::F32><<<grid, kSumColumns * kSumRows, 0, stream>>>(b.part, blocks, channels, static_cast<float*>(dgamma),
+                                                                         static_cast<float*>(dbeta));
+      else if (dtype == SUBM_F16)
+        layer_norm_weight_grad_kernel<DT::F16><<<grid, kSumColumns * kSumRows, 0, stream>>>(
+            b.part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
+      else
+        layer_norm_weight_grad_kernel<DT::BF16><<<grid, kSumColumns * kSumRows, 0, stream>>>(
+            b.part, blocks, channels, static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return fail(hip_status(e, "sparse_layer_norm_backward launch"));
+    return SUBM_OK;
+  });
 }

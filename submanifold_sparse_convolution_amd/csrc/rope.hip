@@ -207,41 +207,47 @@ using namespace submconv;
 
 extern "C" int sparse_rope_frequencies(int count, double base, int scaling, double factor, double trained_length,
                                        float* freq, float* magnitude) {
-  clear_error();
-  if (count < 1) return fail(SUBM_ERR_INVALID_ARG, "count must be at least 1");
-  if (!(base > 1.0) || !std::isfinite(base)) return fail(SUBM_ERR_INVALID_ARG, "base must be above 1 and finite");
-  if (scaling < SUBM_ROPE_PLAIN || scaling > SUBM_ROPE_PARTS) return fail(SUBM_ERR_INVALID_ARG, "unknown scaling");
-  if (!(factor >= 1.0) || !std::isfinite(factor)) return fail(SUBM_ERR_INVALID_ARG, "factor must be at least 1 and finite");
-  if (scaling == SUBM_ROPE_PARTS && (!(trained_length > 0.0) || !std::isfinite(trained_length)))
-    return fail(SUBM_ERR_INVALID_ARG, "trained_length must be positive and finite");
-  if (freq == nullptr) return fail(SUBM_ERR_INVALID_ARG, "freq is NULL");
-  if (scaling == SUBM_ROPE_BASE && count > 1) base *= std::pow(factor, (double)count / (count - 1));
-  for (int i = 0; i < count; ++i) {
-    double f = std::pow(base, -(double)i / count);
-    if (scaling == SUBM_ROPE_LINEAR) f /= factor;
-    if (scaling == SUBM_ROPE_PARTS) {
-      const double turns = trained_length * f / (2.0 * 3.14159265358979323846);
-      const double keep = std::min(1.0, std::max(0.0, (turns - 1.0) / 31.0));
-      f = f * keep + f / factor * (1.0 - keep);
+  return no_throw([&]() -> int {
+    clear_error();
+    if (count < 1) return fail(SUBM_ERR_INVALID_ARG, "count must be at least 1");
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(SUBM_ERR_INVALID_ARG, "base must be above 1 and finite");
+    if (scaling < SUBM_ROPE_PLAIN || scaling > SUBM_ROPE_PARTS) return fail(SUBM_ERR_INVALID_ARG, "unknown scaling");
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return fail(SUBM_ERR_INVALID_ARG, "factor must be at least 1 and finite");
+    if (scaling == SUBM_ROPE_PARTS && (!(trained_length > 0.0) || !std::isfinite(trained_length)))
+      return fail(SUBM_ERR_INVALID_ARG, "trained_length must be positive and finite");
+    if (freq == nullptr) return fail(SUBM_ERR_INVALID_ARG, "freq is NULL");
+    if (scaling == SUBM_ROPE_BASE && count > 1) base *= std::pow(factor, (double)count / (count - 1));
+    for (int i = 0; i < count; ++i) {
+      double f = std::pow(base, -(double)i / count);
+      if (scaling == SUBM_ROPE_LINEAR) f /= factor;
+      if (scaling == SUBM_ROPE_PARTS) {
+        const double turns = trained_length * f / (2.0 * 3.14159265358979323846);
+        const double keep = std::min(1.0, std::max(0.0, (turns - 1.0) / 31.0));
+        f = f * keep + f / factor * (1.0 - keep);
+      }
+      freq[i] = (float)f;
     }
-    freq[i] = (float)f;
-  }
-  if (magnitude != nullptr) *magnitude = scaling == SUBM_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
-  return SUBM_OK;
+    if (magnitude != nullptr) *magnitude = scaling == SUBM_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return SUBM_OK;
+  });
 }
 
 extern "C" int sparse_rope_forward(const subm_heads_t* x, int64_t n, int heads, int head_dim, int dtype,
                                    const int32_t* positions, int64_t position_stride, int axes, const float* freq,
                                    int num_freq, int layout, float magnitude, const subm_heads_t* y,
                                    hipStream_t stream) {
-  return rope(x, n, heads, head_dim, dtype, positions, position_stride, axes, freq, num_freq, layout, magnitude, 1.f,
-              y, stream, "sparse_rope_forward launch");
+  return no_throw([&]() -> int {
+    return rope(x, n, heads, head_dim, dtype, positions, position_stride, axes, freq, num_freq, layout, magnitude, 1.f,
+                y, stream, "sparse_rope_forward launch");
+  });
 }
 
 extern "C" int sparse_rope_backward(const subm_heads_t* dy, int64_t n, int heads, int head_dim, int dtype,
                                     const int32_t* positions, int64_t position_stride, int axes, const float* freq,
                                     int num_freq, int layout, float magnitude, const subm_heads_t* dx,
                                     hipStream_t stream) {
-  return rope(dy, n, heads, head_dim, dtype, positions, position_stride, axes, freq, num_freq, layout, magnitude,
-              -1.f, dx, stream, "sparse_rope_backward launch");
+  return no_throw([&]() -> int {
+    return rope(dy, n, heads, head_dim, dtype, positions, position_stride, axes, freq, num_freq, layout, magnitude,
+                -1.f, dx, stream, "sparse_rope_backward launch");
+  });
 }

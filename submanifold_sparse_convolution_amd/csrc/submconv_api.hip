@@ -305,51 +305,70 @@ void release_map(submconv_map* m) {
 }  // namespace
 
 namespace {
-// Per-(device, stream) scratch buffers (packed weights of the neighbour-pool convolution): at
-// most kScratchStreams per device; the oldest goes back to the pool, in order after the work on
-// its own stream, when a new stream needs one.
+// Per-(device, stream) scratch buffers (packed weights of the neighbour-pool convolution, partial
+// results of the attention and layer norm gradients): at most kScratchStreams per device; the
+// oldest goes back to the pool, in order after the work on its own stream, when a new stream needs
+// one.  A buffer that a later call outgrows is kept (each at least doubles, so all of them are
+// below twice the last): a captured graph may hold its address, and another thread's call may be
+// about to use it.
 struct ScratchEntry {
   hipStream_t stream = nullptr;
   void* ptr = nullptr;
   size_t bytes = 0;
+  std::vector<void*> outgrown;
 };
 struct ScratchCache {
   std::mutex mu;
+  std::mutex launch;  // held from taking a buffer to the last launch that uses it (scratch_launch_lock)
   std::vector<ScratchEntry> entries;
 };
 ScratchCache g_scratch[kMaxDevices];
 constexpr size_t kScratchStreams = 16;
+
+void free_scratch(const ScratchEntry& e) {
+  device_free(e.ptr, e.stream);
+  for (void* p : e.outgrown) device_free(p, e.stream);
+}
 }  // namespace
+
+std::unique_lock<std::mutex> submconv::scratch_launch_lock(int dev) {
+  return std::unique_lock<std::mutex>(g_scratch[dev >= 0 && dev < kMaxDevices ? dev : 0].launch);
+}
 
 Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void** ptr) {
   *ptr = nullptr;
   if (dev < 0 || dev >= kMaxDevices) return make_status(SUBM_ERR_HIP, "device ordinal out of range");
   ScratchCache& c = g_scratch[dev];
   std::lock_guard<std::mutex> lock(c.mu);
-  for (size_t i = 0; i < c.entries.size(); ++i) {
-    ScratchEntry& e = c.entries[i];
-    if (e.stream != stream) continue;
-    if (e.bytes >= bytes) {
-      *ptr = e.ptr;
-      return Status{};
-    }
-    device_free(e.ptr, e.stream);  // in order after this stream's earlier work
-    c.entries.erase(c.entries.begin() + i);
-    break;
+  ScratchEntry* mine = nullptr;
+  for (ScratchEntry& e : c.entries)
+    if (e.stream == stream) mine = &e;
+  if (mine != nullptr && mine->bytes >= bytes) {
+    *ptr = mine->ptr;
+    return Status{};
   }
-  if (c.entries.size() >= kScratchStreams) {
-    device_free(c.entries.front().ptr, c.entries.front().stream);
-    c.entries.erase(c.entries.begin());
-  }
-  const size_t want = round_up(bytes, size_t(1) << 20);
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  SUBM_HIP_TRY(hipStreamIsCapturing(stream, &capture));
+  if (capture != hipStreamCaptureStatusNone)
+    return make_status(SUBM_ERR_UNSUPPORTED,
+                       "the stream's scratch memory cannot grow under graph capture: make the call once on this stream before");
+  const size_t want = round_up(std::max(bytes, mine != nullptr ? 2 * mine->bytes : 0), size_t(1) << 20);
   void* p = nullptr;
   Status s = device_alloc(&p, want, stream);
   if (!s.ok()) return s;
-  ScratchEntry e;
-  e.stream = stream;
-  e.ptr = p;
-  e.bytes = want;
-  c.entries.push_back(e);
+  if (mine == nullptr) {
+    if (c.entries.size() >= kScratchStreams) {
+      free_scratch(c.entries.front());
+      c.entries.erase(c.entries.begin());
+    }
+    c.entries.push_back(ScratchEntry{});
+    mine = &c.entries.back();
+    mine->stream = stream;
+  } else {
+    mine->outgrown.push_back(mine->ptr);
+  }
+  mine->ptr = p;
+  mine->bytes = want;
   *ptr = p;
   return Status{};
 }
@@ -707,6 +726,7 @@ extern "C" int subm_release_cached_memory(void) {
   BlockCache& cache = g_blocks[dev];
   ScratchCache& sc = g_scratch[dev];
   // hold every cache while the device drains, so that nothing new is enqueued on their memory
+  std::lock_guard<std::mutex> l0(sc.launch);
   std::lock_guard<std::mutex> l1(ws.mu);
   std::lock_guard<std::mutex> l2(cache.mu);
   std::lock_guard<std::mutex> l3(sc.mu);
@@ -724,7 +744,7 @@ extern "C" int subm_release_cached_memory(void) {
   }
   for (const CachedBlock& b : cache.blocks) device_free(b.ptr, b.stream);
   cache.blocks.clear();
-  for (const ScratchEntry& x : sc.entries) device_free(x.ptr, x.stream);
+  for (const ScratchEntry& x : sc.entries) free_scratch(x);
   sc.entries.clear();
   e = hipDeviceSynchronize();  // (the stream-ordered frees above)
   if (e != hipSuccess) return fail(hip_status(e, "subm_release_cached_memory"));
@@ -786,6 +806,7 @@ extern "C" int subm_conv3d_forward(submconv_map_t map, int64_t n, int ksize, int
     if (!s.ok()) return fail(s);
     if (state != 3) {
       void* wpk = nullptr;
+      const auto launches = scratch_launch_lock(map->d.device);
       s = stream_scratch(map->d.device, stream, pool_weight_bytes(cin), &wpk);
       if (!s.ok()) return fail(s);
       // state 1: the plan's flags are not known on the host yet, so the conv.hip kernel is launched
@@ -809,6 +830,7 @@ extern "C" int subm_conv3d_forward(submconv_map_t map, int64_t n, int ksize, int
       ++map->d.order_calls == 2) {
     void* blk = nullptr;
     void* scr = nullptr;
+    const auto launches = scratch_launch_lock(map->d.device);
     hipError_t e = hipMallocAsync(&blk, order_block_bytes(n), stream);
     if (e != hipSuccess) return fail(hip_status(e, "row order allocation"));
     s = stream_scratch(map->d.device, stream, order_scratch_bytes(n), &scr);
