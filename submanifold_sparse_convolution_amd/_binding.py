@@ -791,7 +791,7 @@ def sparse_layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None
         y = _vector(out, (n, c), x.dtype, x.device, "out")
     mean = rstd = mean_ptr = rstd_ptr = None
     if stats:
-        mean, rstd = _empty((2, n), torch.float32, x.device, stream)
+        mean, rstd = _empty((n,), torch.float32, x.device, stream), _empty((n,), torch.float32, x.device, stream)
         mean_ptr = mean.data_ptr()
         rstd_ptr = rstd.data_ptr()
     _run("sparse_layer_norm_forward", x.get_device(), stream, x.data_ptr(), n, c, code, g, b, eps, y, mean_ptr, rstd_ptr)
@@ -817,7 +817,7 @@ def sparse_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
         dx = _vector(out, (n, c), x.dtype, x.device, "out")
     dgamma = dbeta = dg_ptr = db_ptr = None
     if weight_grads:
-        dgamma, dbeta = _empty((2, c), x.dtype, x.device, stream)
+        dgamma, dbeta = _empty((c,), x.dtype, x.device, stream), _empty((c,), x.dtype, x.device, stream)
         dg_ptr, db_ptr = dgamma.data_ptr(), dbeta.data_ptr()
     _run("sparse_layer_norm_backward", x.get_device(), stream, dy_ptr, x.data_ptr(), n, c, code, g, m, r, dx, dg_ptr, db_ptr)
     return out, dgamma, dbeta

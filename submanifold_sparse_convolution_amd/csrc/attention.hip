@@ -326,9 +326,9 @@ Status launch(FwdArgs a, hipStream_t stream) {
   }
   // Too few workgroups to fill the compute units: split the keys, as long as a share keeps
   // kShare keys on average (the join costs a launch and a float32 copy of the rows a share).
-  constexpr int kShare = D == DT::F32 ? 96 : 512;
+  constexpr int kShare = D == DT::F32 ? 32 : 512, kPerUnit = D == DT::F32 ? 1 : 2;
   const int64_t blocks = (rows / 128 + a.items) * a.kv_heads;
-  const int64_t want = std::min<int64_t>(2 * kUnits / blocks, a.nk / a.items / kShare);
+  const int64_t want = std::min<int64_t>(kPerUnit * kUnits / blocks, a.nk / a.items / kShare);
   if (want < 2) {
     SUBM_HIP_TRY((launch_tiles<D, DC, 4, false>(a, stream)));
     return Status{};

@@ -470,7 +470,9 @@ Status launch(BwdArgs a, hipStream_t stream) {
   // Measured, forward and backward: 7,813 tokens, 12 / 4 heads of 64, f16: 451 us not split, 368
   // with 4 a unit, 376 with 3 or 6; 3,000 tokens, 12 heads of 128, bf16: 337 us with 2, 345 with 4,
   // 385 with 3; 800 tokens, 8 heads of 64: 41.8 us with shares of 128 rows, 46.8 with 256.
-  constexpr int kPerUnit = DP == 64 ? 4 : 2, kLeast = D == DT::F32 ? 96 : 128;
+  // float32 waves are slow and one a SIMD: one workgroup a unit, whatever is left to each (265
+  // queries, 304 keys in two items, 16 heads of 80).
+  constexpr int kPerUnit = D == DT::F32 ? 1 : DP == 64 ? 4 : 2, kLeast = D == DT::F32 ? 32 : 128;
   if (!wide_q) a.q_splits = splits_for((rows / 128 + a.items) * a.kv_heads, a.nk / a.items, kPerUnit, kLeast);
   if (!wide_k) a.k_splits = splits_for((a.nk / 128 + a.items) * a.kv_heads, rows / a.items, kPerUnit, kLeast);
 
