@@ -87,14 +87,20 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
 // three independent pieces of work, so that the matrix cores run while the exponentials do:
 //   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
 // (Four tiles of each in flight: the same time.)
-template <DT D, int DC, int W, int KEYS, int OCC, bool SPLIT>
-__global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs a) {
+//
+// KG = 2: two groups of W waves hold the same rows and take every other tile of keys, joined through
+// LDS at the end: where a compute unit gets one workgroup, a lone wave a SIMD would wait for each
+// instruction's result in turn.
+template <DT D, int DC, int W, int KG, int KEYS, int OCC, bool SPLIT>
+__global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(FwdArgs a) {
   constexpr int DP = tile_width(DC), KB = KEYS / 32;
   constexpr int kTile = KEYS * kRowBytes<D, DP>;
   constexpr int kRows = 32 * W;
   using Loader = TileLoader<D, DP, KEYS, W>;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[4 * kTile];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(1024))) unsigned char s_kv[KG * 4 * kTile];
+  __shared__ float2 s_join[KG == 1 ? 1 : W * 64];
+  const int lane = threadIdx.x & 63, every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = KG == 1 ? 0 : every / W, wave = KG == 1 ? every : every % W;
   const int group = a.heads / a.kv_heads, head = blockIdx.y;
   int tile;
   const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, blockIdx.x, &tile);
@@ -134,7 +140,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
   lk.lane = lv.lane = lane;
   lk.place(k, a.head_dim, 1, 0, 0);
   lv.place(v, a.head_dim, 1, 0, 0);
-  const uint32_t lds = lds_offset(s_kv);
+  const uint32_t lds = lds_offset(s_kv) + part * 4 * kTile;
   const TileReader<D, DP> rd(lane, lds, lds + 2 * kTile);
   // this workgroup's keys: all, or its share of whole tiles (a share may be empty)
   int tiles = (nk + KEYS - 1) / KEYS, left = nk;
@@ -145,10 +151,14 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
     kp += (int64_t)t0 * KEYS * k.row;
     vp += (int64_t)t0 * KEYS * v.row;
   }
-  // (t and slot apart: inside the loop the slot is a constant)
-  const auto load_k = [&](int t, int slot) { lk.load(kp + (int64_t)t * KEYS * k.row, left - t * KEYS, lds + slot * kTile); };
+  // (t counts this part's tiles; t and slot apart: inside the loop the slot is a constant)
+  const auto load_k = [&](int t, int slot) {
+    const int key = (t * KG + part) * KEYS;
+    lk.load(kp + (int64_t)key * k.row, left - key, lds + slot * kTile);
+  };
   const auto load_v = [&](int t, int slot) {
-    lv.load(vp + (int64_t)t * KEYS * v.row, t < 0 ? 0 : left - t * KEYS, lds + (2 + slot) * kTile);
+    const int key = (t * KG + part) * KEYS;
+    lv.load(vp + (int64_t)key * v.row, t < 0 ? 0 : left - key, lds + (2 + slot) * kTile);
   };
   const auto scores = [&](int slot, f32x16_t (&s)[KB]) {
 #pragma unroll
@@ -190,12 +200,13 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
       barrier_no_fence();
       load_k(t + 2, slot);
       load_v(t, slot);
-      if ((t + 1) * KEYS > left) {  // keys past the end
+      const int key = (t * KG + part) * KEYS;
+      if (key + KEYS > left) {  // keys past the end (perhaps all)
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (t * KEYS + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= left) s[kb][i] = -INFINITY;
+            if (key + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= left) s[kb][i] = -INFINITY;
       }
       scores(slot ^ 1, next);
       float shrink;
@@ -213,18 +224,36 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_forward_kernel(FwdArgs 
           for (int i = 0; i < 16; ++i) acc[db][i] *= shrink;
       }
     };
+    const int steps = (tiles + KG - 1) / KG;
     for (int t = 0;;) {
       step(t, 0, s0, s1);
-      if (++t == tiles) break;
+      if (++t == steps) break;
       step(t, 1, s1, s0);
-      if (++t == tiles) break;
+      if (++t == steps) break;
     }
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
-    product((tiles - 1) % 2, p);
+    product((steps - 1) % 2, p);
   }
-  const float sum = half_sum(state.sum);
+  float sum = half_sum(state.sum);
+  if constexpr (KG == 2) {
+    const uint32_t at = lds_offset(s_kv) + wave * (DC / 32 * 4096);
+    wait_lgkmcnt0();
+    __syncthreads();  // (every part is done with its tiles)
+    if (part == 1) {
+      put_acc<DC>(at, acc, lane);
+      s_join[wave * 64 + lane] = make_float2(state.base, sum);
+    }
+    __syncthreads();
+    if (part == 1) return;
+    const float2 other = s_join[wave * 64 + lane];
+    const float base = fmaxf(state.base, other.x);
+    const float mine = exp2_fast(state.base - base), theirs = exp2_fast(other.x - base);
+    add_acc<DC>(at, acc, mine, theirs, lane);
+    sum = fmaf(other.y, theirs, sum * mine);
+    state.base = base;
+  }
   if (!there) return;
   if constexpr (SPLIT) {
     const int64_t at = ((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row;
@@ -299,13 +328,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   if (a.lse != nullptr && c == 0) a.lse[tok * a.heads + h] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
 }
 
-template <DT D, int DC, int W, bool SPLIT>
+template <DT D, int DC, int W, int KG, bool SPLIT>
 hipError_t launch_tiles(const FwdArgs& a, hipStream_t stream) {
-  constexpr int DP = tile_width(DC);
-  constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DP == 64 ? 3 : 2;
+  constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DC <= 64 && KG == 1 ? 3 : 2;
   const int64_t slots = a.nq * (a.heads / a.kv_heads) / (32 * W) + a.items;
-  attention_forward_kernel<D, DC, W, KEYS, OCC, SPLIT>
-      <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.splits : 1u), W * 64, 0, stream>>>(a);
+  attention_forward_kernel<D, DC, W, KG, KEYS, OCC, SPLIT>
+      <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.splits : 1u), KG * W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -320,17 +348,21 @@ Status launch(FwdArgs a, hipStream_t stream) {
   const int64_t rows = a.nq * (a.heads / a.kv_heads);
   if constexpr (D != DT::F32 && DP == 128) {
     if ((rows / 256 + a.items) * a.kv_heads >= kUnits && rows / a.items >= 256) {
-      SUBM_HIP_TRY((launch_tiles<D, DC, 8, false>(a, stream)));
+      SUBM_HIP_TRY((launch_tiles<D, DC, 8, 1, false>(a, stream)));
       return Status{};
     }
   }
-  // Too few workgroups to fill the compute units: split the keys, as long as a share keeps
-  // kShare keys on average (the join costs a launch and a float32 copy of the rows a share).
-  constexpr int kShare = D == DT::F32 ? 32 : 512, kPerUnit = D == DT::F32 ? 1 : 2;
-  const int64_t blocks = (rows / 128 + a.items) * a.kv_heads;
-  const int64_t want = std::min<int64_t>(kPerUnit * kUnits / blocks, a.nk / a.items / kShare);
-  if (want < 2) {
-    SUBM_HIP_TRY((launch_tiles<D, DC, 4, false>(a, stream)));
+  // Too few workgroups to fill the compute units: two groups of waves on each tile (2,000 tokens, 16
+  // heads of 128: 42 us, 54 in two splits; with fewer than 512 keys the join eats the gain), or,
+  // below half of them, the keys split over workgroups as long as a share keeps kShare keys on
+  // average (the join costs a launch and a float32 copy of the rows a share).  float32 waves need
+  // the registers of two.
+  constexpr int kShare = D == DT::F32 ? 32 : 512, kPerUnit = D == DT::F32 ? 1 : 2, KG = D == DT::F32 ? 1 : 2;
+  const int64_t blocks = (rows / 128 + a.items) * a.kv_heads, keys = a.nk / a.items;
+  const int64_t want = std::min<int64_t>(kPerUnit * kUnits / blocks, keys / kShare);
+  if (want <= KG) {
+    if (blocks <= kUnits && keys >= kShare) SUBM_HIP_TRY((launch_tiles<D, DC, 4, KG, false>(a, stream)));
+    else SUBM_HIP_TRY((launch_tiles<D, DC, 4, 1, false>(a, stream)));
     return Status{};
   }
   a.splits = (int)want;
@@ -343,7 +375,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   if (!st.ok()) return st;
   a.state = static_cast<float2*>(scratch);
   a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + state_bytes);
-  SUBM_HIP_TRY((launch_tiles<D, DC, 4, true>(a, stream)));
+  SUBM_HIP_TRY((launch_tiles<D, DC, 4, 1, true>(a, stream)));
   constexpr int kRowsPer = 256 / (DP / 4);
   const int64_t joins = (rows * a.kv_heads + kRowsPer - 1) / kRowsPer;
   attention_join_kernel<D, DP><<<(unsigned)joins, 256, 0, stream>>>(a);

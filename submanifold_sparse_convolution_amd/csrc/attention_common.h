@@ -308,6 +308,24 @@ __device__ __forceinline__ void store_row(typename Elem<D>::T* row, const f32x16
     }
 }
 
+// Accumulators through LDS between the waves that hold the same own rows: the values of a lane 256
+// bytes apart, so that a wave's accesses are contiguous.  `at`: this wave's area, DC / 32 * 4 KB.
+template <int DC> __device__ __forceinline__ void put_acc(uint32_t at, const f32x16_t (&acc)[DC / 32], int lane) {
+#pragma unroll
+  for (int db = 0; db < DC / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *(lds_float_t*)(uintptr_t)(at + (db * 16 + i) * 256 + lane * 4) = acc[db][i];
+}
+template <int DC> __device__ __forceinline__ void add_acc(uint32_t at, f32x16_t (&acc)[DC / 32], float mine, float theirs, int lane) {
+#pragma unroll
+  for (int db = 0; db < DC / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float v = *(const lds_float_t*)(uintptr_t)(at + (db * 16 + i) * 256 + lane * 4);
+      acc[db][i] = fmaf(v, theirs, acc[db][i] * mine);
+    }
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
