@@ -23,9 +23,9 @@ struct FwdArgs {
   int64_t nq, nk;
   int items, heads, kv_heads, head_dim;
   float scale;
-  // Keys split over `splits` workgroups: each leaves the unnormalised sums of its packed rows,
-  // part [splits, kv_heads, nq * group, DP] and their (base, sum), for the joining kernel.
-  int splits;
+  // Tiles in parts: what a part leaves, [place][rows of a tile][DP] unnormalised sums and their
+  // (base, sum).
+  Cut cut;
   float* part;
   float2* state;
 };
@@ -41,7 +41,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // matrix products that they overlap with.
 template <DT D> __device__ __forceinline__ void pin(Frag<D>& f) {
 #pragma unroll
-  for (int i = 0; i < Elem<D>::kSize / 2; ++i) asm volatile("" : "+v"(f.v[i].x), "+v"(f.v[i].y), "+v"(f.v[i].z), "+v"(f.v[i].w));
+  for (int i = 0; i < Elem<D>::kSize / 2; ++i)
+    asm volatile("" : "+v"(f.v[i].x), "+v"(f.v[i].y), "+v"(f.v[i].z), "+v"(f.v[i].w));
 }
 
 constexpr float kNone = -1.7e38f;  // a running maximum before any score (finite: differences stay numbers)
@@ -91,7 +92,7 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
 // KG = 2: two groups of W waves hold the same rows and take every other tile of keys, joined through
 // LDS at the end: where a compute unit gets one workgroup, a lone wave a SIMD would wait for each
 // instruction's result in turn.
-template <DT D, int DC, int W, int KG, int KEYS, int OCC, bool SPLIT>
+template <DT D, int DC, int W, int KG, int KEYS, int OCC, int CUT>
 __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(FwdArgs a) {
   constexpr int DP = tile_width(DC), KB = KEYS / 32;
   constexpr int kTile = KEYS * kRowBytes<D, DP>;
@@ -101,9 +102,11 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
   __shared__ float2 s_join[KG == 1 ? 1 : W * 64];
   const int lane = threadIdx.x & 63, every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = KG == 1 ? 0 : every / W, wave = KG == 1 ? every : every % W;
-  const int group = a.heads / a.kv_heads, head = blockIdx.y;
+  const int group = a.heads / a.kv_heads;
+  const Share share = share_of<CUT>(a.cut, blockIdx.x);
+  const int head = share.head;
   int tile;
-  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, blockIdx.x, &tile);
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
   int64_t q0, k0;
   int nq, nk;
   item_rows(a.q_offsets, a.nq, item, &q0, &nq);
@@ -144,12 +147,11 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
   const TileReader<D, DP> rd(lane, lds, lds + 2 * kTile);
   // this workgroup's keys: all, or its share of whole tiles (a share may be empty)
   int tiles = (nk + KEYS - 1) / KEYS, left = nk;
-  if constexpr (SPLIT) {
-    const int share = (tiles + a.splits - 1) / a.splits, t0 = min(tiles, share * (int)blockIdx.z);
-    tiles = min(share, tiles - t0);
-    left = min(nk - t0 * KEYS, tiles * KEYS);
-    kp += (int64_t)t0 * KEYS * k.row;
-    vp += (int64_t)t0 * KEYS * v.row;
+  if constexpr (CUT != kNoCut) {
+    const int first = part_steps(a.cut, share.part, &tiles);
+    left = min(nk - first * KEYS, tiles * KEYS);
+    kp += (int64_t)first * KEYS * k.row;
+    vp += (int64_t)first * KEYS * v.row;
   }
   // (t counts this part's tiles; t and slot apart: inside the loop the slot is a constant)
   const auto load_k = [&](int t, int slot) {
@@ -255,8 +257,8 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     state.base = base;
   }
   if (!there) return;
-  if constexpr (SPLIT) {
-    const int64_t at = ((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row;
+  if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0)) {
+    const int64_t at = (int64_t)share.place * kRows + wave * 32 + (lane & 31);
     if (lane < 32) a.state[at] = make_float2(nk > 0 ? state.base : -INFINITY, sum);
     if (tiles == 0) return;
     float* o = a.part + at * DP;
@@ -273,32 +275,43 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     a.lse[qmap.stat(row, a.heads)] = tiles > 0 ? (state.base + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// Joins the splits of a row: DP / 4 threads a row, four channels each.
-template <DT D, int DP>
+// Joins the parts of a tile (blockIdx.x of those in parts), DP / 4 threads a row, blockIdx.y the
+// rows of the tile.
+template <DT D, int DP, int W>
 __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
-  constexpr int kThreads = DP / 4;
-  const int group = a.heads / a.kv_heads;
-  const int64_t rows = a.nq * group, all = rows * a.kv_heads;
-  const int64_t at = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
-  if (at >= all) return;
+  constexpr int kThreads = DP / 4, kRows = 32 * W;
+  const int group = a.heads / a.kv_heads, parts = a.cut.parts;
+  const Share share = tile_share(a.cut, blockIdx.x);
+  int tile;
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
+  int64_t q0;
+  int nq;
+  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+  const int rows = nq * group;
+  const RowMap qmap{q0, share.head * group, group};
+  const Heads<D> out = heads_of<D>(a.out);
   const int c = threadIdx.x % kThreads * 4;
-  // The splits in batches, every load of a batch in flight at once, joined as a running softmax.
+  const int r = blockIdx.y * (256 / kThreads) + threadIdx.x / kThreads;
+  const int64_t row = (int64_t)tile * kRows + r;
+  if (row >= rows) return;
+  const int64_t first = (int64_t)share.place * kRows + r;
+  // The parts in batches, every load of a batch in flight at once, joined as a running softmax.
   constexpr int kBatch = 8;
   float base = -INFINITY, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+  for (int s0 = 0; s0 < parts; s0 += kBatch) {
     float2 st[kBatch];
     float4 p[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int64_t row = min(s0 + i, a.splits - 1) * all + at;
-      st[i] = a.state[row];
-      p[i] = *reinterpret_cast<const float4*>(a.part + row * DP + c);
+      const int64_t at = first + (int64_t)min(s0 + i, parts - 1) * kRows;
+      st[i] = a.state[at];
+      p[i] = *reinterpret_cast<const float4*>(a.part + at * DP + c);
     }
     float top = base;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) top = fmaxf(top, st[i].x);
-    if (top == -INFINITY) continue;  // (no keys: the same in every split)
+    if (top == -INFINITY) continue;  // (no keys: the same in every part)
     const float shrink = exp2_fast(base - top);
     base = top;
     sum *= shrink;
@@ -309,7 +322,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       // a share without keys has a sum of 0 and wrote no part
-      const bool some = s0 + i < a.splits && st[i].y != 0.f;
+      const bool some = s0 + i < parts && st[i].y != 0.f;
       const float w = some ? exp2_fast(st[i].x - base) : 0.f;
       sum = fmaf(w, some ? st[i].y : 0.f, sum);
       o.x = fmaf(w, some ? p[i].x : 0.f, o.x);
@@ -320,66 +333,73 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   }
   const bool none = base == -INFINITY;  // the item has no keys
   const float f = none ? 0.f : 1.f / sum;
-  const int head = (int)(at / rows);
-  const int64_t r = at - head * rows, tok = r / group;
-  const int h = head * group + (int)(r - tok * group);
-  const Heads<D> out = heads_of<D>(a.out);
-  if (c < a.head_dim) store4<D>(out.data + tok * out.row + (int64_t)h * out.head + c, o.x * f, o.y * f, o.z * f, o.w * f);
-  if (a.lse != nullptr && c == 0) a.lse[tok * a.heads + h] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
+  if (c < a.head_dim) store4<D>(qmap.at<D>(out, (int)row) + c, o.x * f, o.y * f, o.z * f, o.w * f);
+  if (a.lse != nullptr && c == 0) a.lse[qmap.stat((int)row, a.heads)] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
 }
 
-template <DT D, int DC, int W, int KG, bool SPLIT>
-hipError_t launch_tiles(const FwdArgs& a, hipStream_t stream) {
-  constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DC <= 64 && KG == 1 ? 3 : 2;
-  const int64_t slots = a.nq * (a.heads / a.kv_heads) / (32 * W) + a.items;
-  attention_forward_kernel<D, DC, W, KG, KEYS, OCC, SPLIT>
-      <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.splits : 1u), KG * W * 64, 0, stream>>>(a);
+template <DT D, int DC, int W, int KG, int CUT> hipError_t launch_tiles(const FwdArgs& a, hipStream_t stream) {
+  constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DC <= 64 && KG == 1 && CUT == kNoCut ? 3 : 2;
+  const dim3 grid = CUT == kNoCut ? dim3((unsigned)a.cut.slots, (unsigned)a.kv_heads) : dim3((unsigned)cut_blocks(a.cut));
+  attention_forward_kernel<D, DC, W, KG, KEYS, OCC, CUT><<<grid, KG * W * 64, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <DT D, int DC, int W, int CUT> Status launch_cut(FwdArgs a, hipStream_t stream) {
+  constexpr int DP = tile_width(DC);
+  int dev = 0;
+  SUBM_HIP_TRY(hipGetDevice(&dev));
+  const auto launches = scratch_launch_lock(dev);
+  const size_t rows = (size_t)cut_places(a.cut) * 32 * W;
+  void* scratch = nullptr;
+  Status st = stream_scratch(dev, stream, rows * (DP * sizeof(float) + sizeof(float2)), &scratch);
+  if (!st.ok()) return st;
+  a.part = static_cast<float*>(scratch);
+  a.state = reinterpret_cast<float2*>(a.part + rows * DP);
+  SUBM_HIP_TRY((launch_tiles<D, DC, W, 1, CUT>(a, stream)));
+  attention_join_kernel<D, DP, W><<<dim3((unsigned)a.cut.cut, 32 * W * (DP / 4) / 256), 256, 0, stream>>>(a);
+  SUBM_HIP_TRY(hipGetLastError());
+  return Status{};
 }
 
 template <DT D, int DC>
 Status launch(FwdArgs a, hipStream_t stream) {
-  constexpr int DP = tile_width(DC);
   // 128 channels: 8 waves on one tile stream halve what each row reads of it (24,576 tokens, 16
   // heads: 2.33 ms, 4 waves 2.80), where they fill the compute units.  64 channels: 4 waves and
   // three workgroups a compute unit, whose exponentials, the bound there, overlap (9,371 rows,
   // 12 heads: 47.9 us, 8 waves 66.7).
   constexpr int kUnits = 256;
-  const int64_t rows = a.nq * (a.heads / a.kv_heads);
-  if constexpr (D != DT::F32 && DP == 128) {
-    if ((rows / 256 + a.items) * a.kv_heads >= kUnits && rows / a.items >= 256) {
-      SUBM_HIP_TRY((launch_tiles<D, DC, 8, 1, false>(a, stream)));
+  constexpr bool kWide = D != DT::F32 && tile_width(DC) == 128;
+  const int64_t rows = a.nq * (a.heads / a.kv_heads), keys = a.nk / a.items, spare = (int64_t)a.items * a.kv_heads;
+  // float32 scores take 8 times as long, so its parts may be short.
+  constexpr int kShare = D == DT::F32 ? 32 : 512;
+  if constexpr (kWide) {
+    const int64_t slots = rows / 256 + a.items;
+    if (slots * a.kv_heads >= kUnits && rows / a.items >= 256) {
+      a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, kUnits, 0);
+      if (a.cut.parts > 1) return launch_cut<D, DC, 8, kCutLast>(a, stream);
+      SUBM_HIP_TRY((launch_tiles<D, DC, 8, 1, kNoCut>(a, stream)));
       return Status{};
     }
   }
-  // Too few workgroups to fill the compute units: two groups of waves on each tile (2,000 tokens, 16
-  // heads of 128: 42 us, 54 in two splits; with fewer than 512 keys the join eats the gain), or,
-  // below half of them, the keys split over workgroups as long as a share keeps kShare keys on
-  // average (the join costs a launch and a float32 copy of the rows a share).  float32 waves need
-  // the registers of two.
-  constexpr int kShare = D == DT::F32 ? 32 : 512, kPerUnit = D == DT::F32 ? 1 : 2, KG = D == DT::F32 ? 1 : 2;
-  const int64_t blocks = (rows / 128 + a.items) * a.kv_heads, keys = a.nk / a.items;
-  const int64_t want = std::min<int64_t>(kPerUnit * kUnits / blocks, keys / kShare);
-  if (want <= KG) {
-    if (blocks <= kUnits && keys >= kShare) SUBM_HIP_TRY((launch_tiles<D, DC, 4, KG, false>(a, stream)));
-    else SUBM_HIP_TRY((launch_tiles<D, DC, 4, 1, false>(a, stream)));
-    return Status{};
+  // Few tiles: parts for two workgroups a unit (float32: one).  Last tiles in parts: not at 64
+  // channels, whose last workgroups speed up as others leave their unit (24,576 tokens, 16 heads: 1.34
+  // ms, 1.39 in parts), nor at the short items that are left here at 128.
+  const int64_t slots = rows / 128 + a.items, tiles = slots * a.kv_heads;
+  constexpr int kFew = kUnits * (D == DT::F32 ? 1 : 2);
+  a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, D == DT::F32 ? kUnits : INT32_MAX, kFew);
+  // Where a compute unit gets one workgroup, two groups of waves on each tile (2,000 tokens, 16 heads
+  // of 128: 42 us, 54 in two parts; with fewer than 512 keys the join eats the gain).  float32 waves
+  // need the registers of two.
+  if constexpr (D != DT::F32) {
+    if (tiles <= kUnits && keys >= 512 && a.cut.parts <= 2) {
+      SUBM_HIP_TRY((launch_tiles<D, DC, 4, 2, kNoCut>(a, stream)));
+      return Status{};
+    }
+  } else {
+    if (a.cut.parts > 1 && a.cut.whole > 0) return launch_cut<D, DC, 4, kCutLast>(a, stream);
   }
-  a.splits = (int)want;
-  int dev = 0;
-  SUBM_HIP_TRY(hipGetDevice(&dev));
-  const auto launches = scratch_launch_lock(dev);
-  const size_t state_bytes = ((size_t)a.splits * rows * a.kv_heads * sizeof(float2) + 255) / 256 * 256;
-  void* scratch = nullptr;
-  Status st = stream_scratch(dev, stream, state_bytes + (size_t)a.splits * rows * a.kv_heads * DP * sizeof(float), &scratch);
-  if (!st.ok()) return st;
-  a.state = static_cast<float2*>(scratch);
-  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + state_bytes);
-  SUBM_HIP_TRY((launch_tiles<D, DC, 4, 1, true>(a, stream)));
-  constexpr int kRowsPer = 256 / (DP / 4);
-  const int64_t joins = (rows * a.kv_heads + kRowsPer - 1) / kRowsPer;
-  attention_join_kernel<D, DP><<<(unsigned)joins, 256, 0, stream>>>(a);
-  SUBM_HIP_TRY(hipGetLastError());
+  if (a.cut.parts > 1) return launch_cut<D, DC, 4, kCutAll>(a, stream);
+  SUBM_HIP_TRY((launch_tiles<D, DC, 4, 1, kNoCut>(a, stream)));
   return Status{};
 }
 
@@ -407,7 +427,8 @@ Status check_attention(const AttentionShape& s) {
   if (s.head_dim % 8 != 0 || s.head_dim > 128)
     return make_status(SUBM_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 up to 128");
   if (!std::isfinite(s.scale)) return make_status(SUBM_ERR_INVALID_ARG, "scale must be finite");
-  if (s.q_offsets == nullptr || s.k_offsets == nullptr) return make_status(SUBM_ERR_INVALID_ARG, "q_offsets or k_offsets is NULL");
+  if (s.q_offsets == nullptr || s.k_offsets == nullptr)
+    return make_status(SUBM_ERR_INVALID_ARG, "q_offsets or k_offsets is NULL");
   if (((reinterpret_cast<uintptr_t>(s.q_offsets) | reinterpret_cast<uintptr_t>(s.k_offsets)) & 7u) != 0)
     return make_status(SUBM_ERR_INVALID_ARG, "an offsets pointer is not 8-byte aligned");
   return Status{};
@@ -453,7 +474,8 @@ extern "C" int sparse_attention_forward(const subm_heads_t* q, const subm_heads_
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
     if (nq == 0) return SUBM_OK;
     if (out->data == k->data || out->data == v->data) return fail(SUBM_ERR_INVALID_ARG, "out must not alias k or v");
-    const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads, head_dim, scale, 1, nullptr, nullptr};
+    const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads,
+                    head_dim, scale, Cut{}, nullptr, nullptr};
     if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
     else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
     else st = launch_dim<DT::BF16>(a, stream);

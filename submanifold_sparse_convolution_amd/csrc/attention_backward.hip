@@ -29,9 +29,9 @@ struct BwdArgs {
   int items, heads, kv_heads, head_dim;
   float scale;
   int q_rows;  // packed rows of a workgroup of the dq kernel
-  // The walked rows split over workgroups: float32 copies of dq [q_splits, kv_heads, nq * group, DP]
-  // and of dk and dv [k_splits, kv_heads, nk, DP], summed by a third kernel.  NULL: not split.
-  int q_splits, k_splits;
+  // Tiles in parts: float32 sums of dq by the first cut, of dk and dv by the second, [place][rows of
+  // a tile][DP], summed by a third kernel.
+  Cut q_cut, k_cut;
   float *dq_part, *dk_part, *dv_part;
 };
 
@@ -49,7 +49,8 @@ template <DT D> __device__ __forceinline__ float absmax_frag(const Frag<D>& f) {
   float m = 0.f;
   const uint32_t w[4] = {f.v[0].x, f.v[0].y, f.v[0].z, f.v[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(to_float<D>((uint16_t)w[i])), fabsf(to_float<D>((uint16_t)(w[i] >> 16)))));
+  for (int i = 0; i < 4; ++i)
+    m = fmaxf(m, fmaxf(fabsf(to_float<D>((uint16_t)w[i])), fabsf(to_float<D>((uint16_t)(w[i] >> 16)))));
   return m;
 }
 
@@ -83,7 +84,7 @@ template <int DC> __device__ __forceinline__ void store_part(float* row, const f
 // d of the own query rows, then dq over the keys, which stream through LDS in tiles of 32.  As in
 // the forward pass a step holds independent pieces of work:
 //   scores and dp of tile t + 1 (k, v),  e of tile t,  product of tile t - 1 (k).
-template <DT D, int DC, int W, int OCC, bool SPLIT>
+template <DT D, int DC, int W, int OCC, int CUT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   constexpr int DP = tile_width(DC), kRows = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
@@ -91,9 +92,11 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   __shared__ __attribute__((aligned(1024))) unsigned char s_kv[6 * kTile];  // four tiles of k, two of v
   __shared__ float s_peak[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = a.heads / a.kv_heads, head = blockIdx.y;
+  const int group = a.heads / a.kv_heads;
+  const Share share = share_of<CUT>(a.q_cut, blockIdx.x);
+  const int head = share.head;
   int tile;
-  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, blockIdx.x, &tile);
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
   int64_t q0, k0;
   int nq, nk;
   item_rows(a.q_offsets, a.nq, item, &q0, &nq);
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     if constexpr (D == DT::F16) peak = fmaxf(peak, absmax_frag<D>(gf[kk]));
   }
   d = half_sum(d);
-  const bool first = !SPLIT || blockIdx.z == 0;  // (every split needs d, one leaves it for dk and dv)
+  const bool first = CUT == kNoCut || share.part <= 0;  // (every part needs d, one leaves it for dk and dv)
   const float base = there ? a.lse[qmap.stat(row, a.heads)] * kLog2e : 0.f;  // log2 of the row's normaliser
   if (first && there && lane < 32) {
     const int64_t at = head * (a.nq * group) + q0 * group + row;
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     if (first && threadIdx.x == 0) {
 #pragma unroll
       for (int w = 0; w < W; ++w) peak = fmaxf(peak, s_peak[w]);
-      a.peak[head * a.q_slots + blockIdx.x] = peak;
+      a.peak[head * a.q_slots + share.slot] = peak;
     }
   }
   const float c = a.scale * kLog2e;
@@ -152,9 +155,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   const uint32_t lds = lds_offset(s_kv);
   const TileReader<D, DP> rd(lane, lds, lds);
   int tiles = (nk + kStep - 1) / kStep, left = nk;
-  if constexpr (SPLIT) {
-    const int share = (tiles + a.q_splits - 1) / a.q_splits, t0 = min(tiles, share * (int)blockIdx.z);
-    tiles = min(share, tiles - t0);
+  if constexpr (CUT != kNoCut) {
+    const int t0 = part_steps(a.q_cut, share.part, &tiles);
     left = min(nk - t0 * kStep, tiles * kStep);
     kp += (int64_t)t0 * kStep * k.row;
     vp += (int64_t)t0 * kStep * v.row;
@@ -162,7 +164,9 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   const auto load_k = [&](int t, int slot) {
     lk.load(kp + (int64_t)t * kStep * k.row, t < 0 ? 0 : left - t * kStep, lds + slot * kTile);
   };
-  const auto load_v = [&](int t, int slot) { lv.load(vp + (int64_t)t * kStep * v.row, left - t * kStep, lds + (4 + slot) * kTile); };
+  const auto load_v = [&](int t, int slot) {
+    lv.load(vp + (int64_t)t * kStep * v.row, left - t * kStep, lds + (4 + slot) * kTile);
+  };
   const auto scores = [&](int slot, f32x16_t& s, f32x16_t& dp) {
     s = zero16();
     dp = zero16();
@@ -230,9 +234,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     product((tiles - 1) % 4, e);
   }
   if (!there) return;
-  if constexpr (SPLIT)
-    store_part<DC>(a.dq_part + (((int64_t)blockIdx.z * a.kv_heads + head) * (a.nq * group) + q0 * group + row) * DP, acc,
-                   a.scale / unit, lane);
+  if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0))
+    store_part<DC>(a.dq_part + ((int64_t)share.place * kRows + wave * 32 + (lane & 31)) * DP, acc, a.scale / unit, lane);
   else
     store_row<D, DC>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
 }
@@ -253,20 +256,23 @@ __device__ __forceinline__ void load_stats(const float* p, int left, uint32_t ld
 // stream through LDS in tiles of 32.  Two waves a SIMD overlap each other's exponentials and
 // products.  At 128 channels in 16 bits the own rows of v stay in LDS: with the two accumulators
 // and k there is no room for them in 256 registers.
-template <DT D, int DC, int W, int OCC, bool SPLIT>
+template <DT D, int DC, int W, int OCC, int CUT>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   constexpr int DP = tile_width(DC), kKeys = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
   constexpr bool kParked = D != DT::F32 && DP == 128;
   using Loader = TileLoader<D, DP, kStep, W>;
   using Parker = TileLoader<D, DP, kKeys, W>;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_qg[4 * kTile + (kParked ? W * kTile : 0)];  // q, q, dout, dout, own v
+  // q, q, dout, dout, own v
+  __shared__ __attribute__((aligned(1024))) unsigned char s_qg[4 * kTile + (kParked ? W * kTile : 0)];
   __shared__ __attribute__((aligned(16))) float s_stat[2 * 2 * 64];  // norm and d of two tiles
   __shared__ float s_peak[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = a.heads / a.kv_heads, head = blockIdx.y;
+  const int group = a.heads / a.kv_heads;
+  const Share share = share_of<CUT>(a.k_cut, blockIdx.x);
+  const int head = share.head;
   int tile;
-  const int item = find_item(a.k_offsets, a.nk, a.items, 1, kKeys, blockIdx.x, &tile);
+  const int item = find_item(a.k_offsets, a.nk, a.items, 1, kKeys, share.slot, &tile);
   int64_t q0, k0;
   int nq, nk;
   item_rows(a.q_offsets, a.nq, item, &q0, &nq);
@@ -323,10 +329,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   const uint32_t stat = __builtin_amdgcn_readfirstlane(lds_offset(s_stat));
   // this workgroup's query rows: all, or its share of whole tiles (a share may be empty)
   int steps = (rows + kStep - 1) / kStep, r0 = 0, end = rows;
-  if constexpr (SPLIT) {
-    const int share = (steps + a.k_splits - 1) / a.k_splits, t0 = min(steps, share * (int)blockIdx.z);
-    steps = min(share, steps - t0);
-    r0 = t0 * kStep;
+  if constexpr (CUT != kNoCut) {
+    r0 = part_steps(a.k_cut, share.part, &steps) * kStep;
     end = min(rows, r0 + steps * kStep);
   }
   int tok = r0 / group, rem = r0 - tok * group;  // of the next tile to load
@@ -399,8 +403,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   }
   wait_vmcnt<0>();  // (the loads past the end)
   if (!there) return;
-  if constexpr (SPLIT) {
-    const int64_t at = (((int64_t)blockIdx.z * a.kv_heads + head) * a.nk + k0 + key) * DP;
+  if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0)) {
+    const int64_t at = ((int64_t)share.place * kKeys + wave * 32 + (lane & 31)) * DP;
     store_part<DC>(a.dk_part + at, dk, a.scale / unit, lane);
     store_part<DC>(a.dv_part + at, dv, p_unit, lane);
   } else {
@@ -409,82 +413,113 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   }
 }
 
-// The sums of split gradients, DP / 4 threads a row: blockIdx.y 0 is dq, 1 dk and 2 dv.
+// The sums of tiles in parts (blockIdx.x of those), DP / 4 threads a row, blockIdx.y the rows of
+// the tile; blockIdx.z 0 is dq, 1 dk and 2 dv.
 template <DT D, int DP>
-__global__ __launch_bounds__(256) void attention_sum_kernel(BwdArgs a) {
+__global__ __launch_bounds__(256) void attention_sum_kernel(BwdArgs a, int q_rows, int k_rows) {
   constexpr int kThreads = DP / 4;
-  const int job = a.dq_part != nullptr ? blockIdx.y : blockIdx.y + 1;
-  const int group = job == 0 ? a.heads / a.kv_heads : 1, splits = job == 0 ? a.q_splits : a.k_splits;
-  const int64_t rows = job == 0 ? a.nq * group : a.nk, all = rows * a.kv_heads;
-  const int64_t at = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+  const int job = a.dq_part != nullptr ? blockIdx.z : blockIdx.z + 1;
+  const Cut cut = job == 0 ? a.q_cut : a.k_cut;
+  const int tile_rows = job == 0 ? q_rows : k_rows, group = job == 0 ? a.heads / a.kv_heads : 1, parts = cut.parts;
+  const int64_t step = (int64_t)tile_rows * DP;
+  if ((int)blockIdx.x >= cut.cut) return;
+  const Share share = tile_share(cut, blockIdx.x);
+  const int64_t* offsets = job == 0 ? a.q_offsets : a.k_offsets;
+  const int64_t total = job == 0 ? a.nq : a.nk;
+  int tile, count;
+  const int item = find_item(offsets, total, a.items, group, tile_rows, share.slot, &tile);
+  int64_t first;
+  item_rows(offsets, total, item, &first, &count);
+  const RowMap map{first, share.head * group, group};
+  const Heads<D> out = heads_of<D>(job == 0 ? a.dq : job == 1 ? a.dk : a.dv);
+  const float* all = job == 0 ? a.dq_part : job == 1 ? a.dk_part : a.dv_part;
   const int c = threadIdx.x % kThreads * 4;
-  if (at >= all || c >= a.head_dim) return;
-  const float* part = (job == 0 ? a.dq_part : job == 1 ? a.dk_part : a.dv_part) + at * DP + c;
+  if (c >= a.head_dim) return;
+  const int r = blockIdx.y * (256 / kThreads) + threadIdx.x / kThreads;
+  const int64_t row = (int64_t)tile * tile_rows + r;
+  if (r >= tile_rows || row >= (int64_t)count * group) return;
+  const float* part = all + ((int64_t)share.place * tile_rows + r) * DP + c;
   float4 o = *reinterpret_cast<const float4*>(part);
 #pragma unroll 8
-  for (int s = 1; s < splits; ++s) {
-    const float4 p = *reinterpret_cast<const float4*>(part + s * all * DP);
+  for (int s = 1; s < parts; ++s) {
+    const float4 p = *reinterpret_cast<const float4*>(part + s * step);
     o.x += p.x;
     o.y += p.y;
     o.z += p.z;
     o.w += p.w;
   }
-  const Heads<D> out = heads_of<D>(job == 0 ? a.dq : job == 1 ? a.dk : a.dv);
-  const int head = (int)(at / rows);
-  const int64_t r = at - head * rows, tok = r / group;
-  const int h = head * group + (int)(r - tok * group);
-  store4<D>(out.data + tok * out.row + (int64_t)h * out.head + c, o.x, o.y, o.z, o.w);
+  store4<D>(map.at<D>(out, (int)row) + c, o.x, o.y, o.z, o.w);
 }
 
-template <DT D, int DC, int W, bool SPLIT> hipError_t launch_dq(BwdArgs& a, hipStream_t stream) {
+template <DT D, int DC, int W, int CUT> hipError_t launch_dq(const BwdArgs& a, hipStream_t stream) {
   constexpr int OCC = D == DT::F32 ? 1 : DC <= 64 ? 3 : 2;
-  a.q_rows = 32 * W;
-  a.q_slots = a.nq * (a.heads / a.kv_heads) / a.q_rows + a.items;
-  attention_dq_kernel<D, DC, W, OCC, SPLIT>
-      <<<dim3((unsigned)a.q_slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.q_splits : 1u), W * 64, 0, stream>>>(a);
+  const dim3 grid =
+      CUT == kNoCut ? dim3((unsigned)a.q_cut.slots, (unsigned)a.kv_heads) : dim3((unsigned)cut_blocks(a.q_cut));
+  attention_dq_kernel<D, DC, W, OCC, CUT><<<grid, W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
-template <DT D, int DC, int W, bool SPLIT> hipError_t launch_dkv(const BwdArgs& a, hipStream_t stream) {
+template <DT D, int DC, int W, int CUT> hipError_t launch_dkv(const BwdArgs& a, hipStream_t stream) {
   constexpr int OCC = D == DT::F32 ? 1 : DC <= 64 ? 3 : 2;
-  const int64_t slots = a.nk / (32 * W) + a.items;
-  attention_dkv_kernel<D, DC, W, OCC, SPLIT>
-      <<<dim3((unsigned)slots, (unsigned)a.kv_heads, SPLIT ? (unsigned)a.k_splits : 1u), W * 64, 0, stream>>>(a);
+  const dim3 grid =
+      CUT == kNoCut ? dim3((unsigned)a.k_cut.slots, (unsigned)a.kv_heads) : dim3((unsigned)cut_blocks(a.k_cut));
+  attention_dkv_kernel<D, DC, W, OCC, CUT><<<grid, W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-// How many workgroups the walked rows are split over, where `blocks` of them leave compute units
-// idle: enough for `per_unit` a compute unit, as long as each keeps `least` walked rows on average.
-int splits_for(int64_t blocks, int64_t walked, int per_unit, int least) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(per_unit * 256 / std::max<int64_t>(blocks, 1), walked / least));
+// The cuts that plan_cut can give: of 8 waves' tiles, which fill the machine, the last; of 4 waves'
+// at 128 channels in 16 bits all (if they filled it, their items would be too short).
+template <DT D, int DC, int W> hipError_t launch_dq(const BwdArgs& a, hipStream_t stream) {
+  constexpr bool kFull = D != DT::F32 && tile_width(DC) == 128;
+  if constexpr (W == 8 || !kFull) {
+    if (a.q_cut.parts > 1 && a.q_cut.whole > 0) return launch_dq<D, DC, W, kCutLast>(a, stream);
+  }
+  if constexpr (W == 4) {
+    if (a.q_cut.parts > 1) return launch_dq<D, DC, W, kCutAll>(a, stream);
+  }
+  return launch_dq<D, DC, W, kNoCut>(a, stream);
+}
+template <DT D, int DC, int W> hipError_t launch_dkv(const BwdArgs& a, hipStream_t stream) {
+  constexpr bool kFull = D != DT::F32 && tile_width(DC) == 128;
+  if constexpr (W == 8 || !kFull) {
+    if (a.k_cut.parts > 1 && a.k_cut.whole > 0) return launch_dkv<D, DC, W, kCutLast>(a, stream);
+  }
+  if constexpr (W == 4) {
+    if (a.k_cut.parts > 1) return launch_dkv<D, DC, W, kCutAll>(a, stream);
+  }
+  return launch_dkv<D, DC, W, kNoCut>(a, stream);
 }
 
 template <DT D, int DC>
 Status launch(BwdArgs a, hipStream_t stream) {
-  constexpr int DP = tile_width(DC);
+  constexpr int DP = tile_width(DC), kUnits = 256;
   const int group = a.heads / a.kv_heads;
-  const int64_t rows = a.nq * group;
+  const int64_t rows = a.nq * group, spare = (int64_t)a.items * a.kv_heads;
   // 128 channels in 16 bits: 8 waves share a tile stream where they fill the compute units.
   constexpr bool kWide = D != DT::F32 && DP == 128;
-  const bool wide_q = kWide && (rows / 256 + a.items) * a.kv_heads >= 256 && rows / a.items >= 256;
-  const bool wide_k = kWide && (a.nk / 256 + a.items) * a.kv_heads >= 256 && a.nk / a.items >= 256;
-  // Measured, forward and backward: 7,813 tokens, 12 / 4 heads of 64, f16: 451 us not split, 368
-  // with 4 a unit, 376 with 3 or 6; 3,000 tokens, 12 heads of 128, bf16: 337 us with 2, 345 with 4,
-  // 385 with 3; 800 tokens, 8 heads of 64: 41.8 us with shares of 128 rows, 46.8 with 256.
+  const bool wide_q = kWide && (rows / 256 + a.items) * a.kv_heads >= kUnits && rows / a.items >= 256;
+  const bool wide_k = kWide && (a.nk / 256 + a.items) * a.kv_heads >= kUnits && a.nk / a.items >= 256;
+  const int q_rows = wide_q ? 256 : 128, k_rows = wide_k ? 256 : 128;
+  // Parts, measured (forward and backward): 7,813 tokens, 12 / 4 heads of 64, f16: 451 us whole, 368
+  // with 4 workgroups a unit, 376 with 3 or 6; 3,000 tokens, 12 heads of 128, bf16: 337 us with 2,
+  // 345 with 4, 385 with 3; 800 tokens, 8 heads of 64: 41.8 us with parts of 128 rows, 46.8 with 256.
   // float32 waves are slow and one a SIMD: one workgroup a unit, whatever is left to each (265
-  // queries, 304 keys in two items, 16 heads of 80).
-  constexpr int kPerUnit = D == DT::F32 ? 1 : DP == 64 ? 4 : 2, kLeast = D == DT::F32 ? 32 : 128;
-  if (!wide_q) a.q_splits = splits_for((rows / 128 + a.items) * a.kv_heads, a.nk / a.items, kPerUnit, kLeast);
-  if (!wide_k) a.k_splits = splits_for((a.nk / 128 + a.items) * a.kv_heads, rows / a.items, kPerUnit, kLeast);
+  // queries, 304 keys in two items, 16 heads of 80: 90 us, 135 with at least 96 rows).
+  constexpr int kFew = kUnits * (D == DT::F32 ? 1 : DP == 64 ? 4 : 2), kLeast = D == DT::F32 ? 32 : 128;
+  constexpr int kResident = kWide ? INT32_MAX : kUnits * (D == DT::F32 ? 1 : 3);  // of 4 waves
+  a.q_rows = q_rows;
+  a.q_slots = rows / q_rows + a.items;
+  a.q_cut = plan_cut(a.q_slots, a.kv_heads, spare, a.nk / a.items, kLeast, wide_q ? kUnits : kResident, kFew);
+  a.k_cut = plan_cut(a.nk / k_rows + a.items, a.kv_heads, spare, rows / a.items, kLeast, wide_k ? kUnits : kResident, kFew);
 
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));
   const auto launches = scratch_launch_lock(dev);
   const auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
-  // norm and d of every query row, a peak for each of the smallest query blocks, and the copies
+  // norm and d of every query row, a peak for each query block, and the parts
   const size_t stat = padded((size_t)rows * a.kv_heads * sizeof(float));
-  const size_t peak = padded((size_t)(rows / 128 + a.items) * a.kv_heads * sizeof(float));
-  const size_t part_q = a.q_splits > 1 ? (size_t)a.q_splits * rows * a.kv_heads * DP * sizeof(float) : 0;
-  const size_t part_k = a.k_splits > 1 ? (size_t)a.k_splits * a.nk * a.kv_heads * DP * sizeof(float) : 0;
+  const size_t peak = padded((size_t)a.q_slots * a.kv_heads * sizeof(float));
+  const size_t part_q = (size_t)cut_places(a.q_cut) * q_rows * DP * sizeof(float);
+  const size_t part_k = (size_t)cut_places(a.k_cut) * k_rows * DP * sizeof(float);
   void* scratch = nullptr;
   Status st = stream_scratch(dev, stream, 2 * stat + peak + part_q + 2 * part_k, &scratch);
   if (!st.ok()) return st;
@@ -500,21 +535,20 @@ Status launch(BwdArgs a, hipStream_t stream) {
   }
   if (a.nq > 0) {
     if constexpr (kWide) {
-      if (wide_q) SUBM_HIP_TRY((launch_dq<D, DC, 8, false>(a, stream)));
+      if (wide_q) SUBM_HIP_TRY((launch_dq<D, DC, 8>(a, stream)));
     }
-    if (!wide_q) SUBM_HIP_TRY((a.q_splits > 1 ? launch_dq<D, DC, 4, true>(a, stream) : launch_dq<D, DC, 4, false>(a, stream)));
+    if (!wide_q) SUBM_HIP_TRY((launch_dq<D, DC, 4>(a, stream)));
   }
   if (a.nk > 0) {
     if constexpr (kWide) {
-      if (wide_k) SUBM_HIP_TRY((launch_dkv<D, DC, 8, false>(a, stream)));
+      if (wide_k) SUBM_HIP_TRY((launch_dkv<D, DC, 8>(a, stream)));
     }
-    if (!wide_k) SUBM_HIP_TRY((a.k_splits > 1 ? launch_dkv<D, DC, 4, true>(a, stream) : launch_dkv<D, DC, 4, false>(a, stream)));
+    if (!wide_k) SUBM_HIP_TRY((launch_dkv<D, DC, 4>(a, stream)));
   }
-  const int jobs = (part_q > 0 ? 1 : 0) + (part_k > 0 ? 2 : 0);
+  const unsigned jobs = (part_q > 0 ? 1 : 0) + (part_k > 0 ? 2 : 0);
   if (jobs > 0) {
-    constexpr int kRowsPer = 256 / (DP / 4);
-    const int64_t most = std::max(part_q > 0 ? rows : 0, part_k > 0 ? a.nk : 0) * a.kv_heads;
-    attention_sum_kernel<D, DP><<<dim3((unsigned)((most + kRowsPer - 1) / kRowsPer), (unsigned)jobs), 256, 0, stream>>>(a);
+    const dim3 grid((unsigned)std::max(a.q_cut.cut, a.k_cut.cut), std::max(q_rows, k_rows) * (DP / 4) / 256, jobs);
+    attention_sum_kernel<D, DP><<<grid, 256, 0, stream>>>(a, q_rows, k_rows);
     SUBM_HIP_TRY(hipGetLastError());
   }
   return Status{};
@@ -557,8 +591,10 @@ extern "C" int sparse_attention_backward(const subm_heads_t* dout, const subm_he
     // (the second kernel reads every input after the first has written dq)
     for (const subm_heads_t* w : {dq, dk, dv})
       for (const subm_heads_t* r : {dout, q, k, v, out})
-        if (w->data != nullptr && w->data == r->data) return fail(SUBM_ERR_INVALID_ARG, "a gradient must not alias an input");
-    if (nq > 0 && nk > 0 && (dq->data == dk->data || dq->data == dv->data)) return fail(SUBM_ERR_INVALID_ARG, "dq, dk and dv must not alias");
+        if (w->data != nullptr && w->data == r->data)
+          return fail(SUBM_ERR_INVALID_ARG, "a gradient must not alias an input");
+    if (nq > 0 && nk > 0 && (dq->data == dk->data || dq->data == dv->data))
+      return fail(SUBM_ERR_INVALID_ARG, "dq, dk and dv must not alias");
     if (nk > 0 && dk->data == dv->data) return fail(SUBM_ERR_INVALID_ARG, "dq, dk and dv must not alias");
     BwdArgs a{};
     a.dout = *dout;
@@ -579,7 +615,6 @@ extern "C" int sparse_attention_backward(const subm_heads_t* dout, const subm_he
     a.kv_heads = kv_heads;
     a.head_dim = head_dim;
     a.scale = scale;
-    a.q_splits = a.k_splits = 1;
     if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);
     else if (dtype == SUBM_F16) st = launch_dim<DT::F16>(a, stream);
     else st = launch_dim<DT::BF16>(a, stream);

@@ -107,8 +107,8 @@ struct RowMap {
 
 // The item of slot `slot` in a tiling by `block` packed rows of `offsets` (each token `group`
 // rows), and the slot's tile in it.
-__device__ __forceinline__ int find_item(const int64_t* offsets, int64_t total, int items, int group, int block, int64_t slot,
-                                         int* tile) {
+__device__ __forceinline__ int find_item(const int64_t* offsets, int64_t total, int items, int group, int block,
+                                         int64_t slot, int* tile) {
   const auto start = [&](int b) {
     const int64_t o = offsets[b];
     return (o < 0 ? 0 : o > total ? total : o) * group / block + b;
@@ -132,6 +132,104 @@ __device__ __forceinline__ void item_rows(const int64_t* offsets, int64_t total,
   *count = (int)(e - s);
 }
 
+// ------------------------------------------------------------------------ parts of tiles
+//
+// Tiles do not fill the compute units evenly: few rows against many leave most of them idle, and a
+// last round of tiles on a full machine takes as long as the others.  The tiles (slots of all
+// heads, head by head) from `whole` on are therefore worked on in `parts` parts of their walked
+// rows by workgroups of their own, which leave float32 sums, [tile - whole][part][rows of a tile], for
+// a second kernel to join in order.  whole = 0: every tile.
+
+struct Cut {
+  int slots, whole, cut, parts;  // cut: tiles in parts
+  // The order of the workgroups.  Tile by tile where each of the 8 XCDs, which take workgroups in
+  // turn, then walks its own part of the rows; else part by part, so that those which walk the same
+  // rows run together.  Tile by tile and part by part: 4 parts (7,813 tokens, 12 / 4 heads of 64,
+  // forward and backward) 360 and 375 us, 16 (8 single tokens, 30,000 keys each, 16 / 4 heads of 128)
+  // 87 and 90; 23 (300 queries, 12,000 keys, 4 heads of 64) 21.0 and 18.0, 6 (800 tokens, 8 heads of
+  // 64, forward and backward) 45.0 and 42.4.
+  bool by_tile;
+};
+
+struct Share {
+  int head, slot;
+  int part;   // -1: the whole tile
+  int place;  // of a part's sums
+};
+
+// Kernels for no tile, every tile and the last tiles in parts: a kernel with one way to its end needs
+// fewer scalar registers.
+constexpr int kNoCut = 0, kCutAll = 1, kCutLast = 2;
+
+// (A division runs on the vector units: without this the addresses that follow from it would stay in
+// vector registers.)
+__device__ __forceinline__ int first_lane(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
+
+template <int CUT> __device__ __forceinline__ Share share_of(const Cut& c, uint32_t block) {
+  if constexpr (CUT == kNoCut) return Share{(int)blockIdx.y, (int)blockIdx.x, -1, 0};
+  const uint32_t whole = CUT == kCutAll ? 0u : (uint32_t)c.whole;
+  uint32_t id = block;
+  Share s{0, 0, -1, 0};
+  if (CUT == kCutAll || block >= whole) {
+    const uint32_t b = block - whole;
+    const uint32_t d = c.by_tile ? c.parts : c.cut, t = first_lane(b / d), u = b - t * d;
+    const uint32_t i = c.by_tile ? t : u;
+    s.part = (int)(c.by_tile ? u : t);
+    s.place = (int)(i * c.parts) + s.part;
+    id = whole + i;
+  }
+  s.head = first_lane(id / (uint32_t)c.slots);
+  s.slot = (int)(id - (uint32_t)s.head * c.slots);
+  return s;
+}
+
+// Of the i-th tile in parts: its head and slot, and the place of its first part.
+__device__ __forceinline__ Share tile_share(const Cut& c, int i) {
+  const int id = c.whole + i, head = id / c.slots;
+  return Share{head, id - head * c.slots, 0, i * c.parts};
+}
+
+// Part `part` of `steps` steps: its first, and how many (perhaps none).
+__device__ __forceinline__ int part_steps(const Cut& c, int part, int* steps) {
+  if (part < 0) return 0;
+  const int share = (*steps + c.parts - 1) / c.parts, first = min(*steps, share * part);
+  *steps = min(share, *steps - first);
+  return first;
+}
+
+// Host.  `slots` * `kv_heads` tiles (`spare` of them perhaps empty) of on average `walked` rows, of which
+// a part keeps at least `least`; `resident` workgroups fill the machine, `few` are wanted when there
+// are less.  parts = 1: nothing to cut.  The last tiles, whole and in parts, bf16: 4,500 tokens, 16 heads
+// of 128, 288 tiles: 240 and 174 us, with the backward pass 1,040 and 738; 24,576 tokens, 1,552 tiles:
+// 2.35 and 2.23 ms; 9,000 tokens, 12 heads of 64, with the backward pass: 1,370 and 1,150 us; float32,
+// 5,000 tokens, 8 heads of 64, with it: 2.95 and 1.91 ms.
+inline Cut plan_cut(int64_t slots, int kv_heads, int64_t spare, int64_t walked, int least, int64_t resident, int64_t few) {
+  const int64_t tiles = slots * kv_heads;
+  Cut c{(int)slots, (int)tiles, 0, 1, false};
+  const int64_t most = walked / least;
+  if (tiles < resident) {
+    const int64_t want = few / tiles < most ? few / tiles : most;
+    if (want >= 2) c = Cut{(int)slots, 0, (int)tiles, (int)want, want % 8 == 0 || 8 % want == 0};
+    return c;
+  }
+  // The tiles past the last full round, in the number of parts whose rounds take least of a tile's
+  // time; not for a gain below a fifth of a tile, nor where empty slots blur where a round ends.
+  const int64_t rest = tiles % resident;
+  if (rest == 0 || spare * 4 > resident || walked < 2048) return c;
+  double best = 0.8;
+  for (int64_t parts = 2; parts <= 16 && parts <= most; ++parts) {
+    const double t = (double)((rest * parts + resident - 1) / resident) / parts + 0.01 * parts;
+    if (t < best) {
+      best = t;
+      c = Cut{(int)slots, (int)(tiles - rest), (int)rest, (int)parts, parts % 8 == 0 || 8 % parts == 0};
+    }
+  }
+  return c;
+}
+
+inline int64_t cut_places(const Cut& c) { return (int64_t)c.cut * c.parts; }
+inline int64_t cut_blocks(const Cut& c) { return c.whole + cut_places(c); }
+
 // ------------------------------------------------------------------------ tiles in LDS
 //
 // A tile is R rows of DP channels, row-major in 16-byte chunks, chunk c of row r at position
@@ -151,7 +249,8 @@ template <DT D, int DP> constexpr int kRowChunks = DP * Elem<D>::kSize / 16;
 template <DT D, int DP> constexpr int kRowBytes = DP * Elem<D>::kSize;
 
 template <DT D, int DP> __device__ __forceinline__ int swizzle(int r) {
-  if constexpr (D == DT::F32) return ((r >> 2) & 1) << 3 | (r & 3) << 1 | ((r >> 3) & 1);  // (row r + 4 on the other 128 bytes)
+  // (float32: row r + 4 on the other 128 bytes)
+  if constexpr (D == DT::F32) return ((r >> 2) & 1) << 3 | (r & 3) << 1 | ((r >> 3) & 1);
   else if constexpr (DP == 128) return (r & 3) << 2 | ((r >> 2) & 3);
   else return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);  // (two rows in 256 bytes)
 }
@@ -316,7 +415,8 @@ template <int DC> __device__ __forceinline__ void put_acc(uint32_t at, const f32
 #pragma unroll
     for (int i = 0; i < 16; ++i) *(lds_float_t*)(uintptr_t)(at + (db * 16 + i) * 256 + lane * 4) = acc[db][i];
 }
-template <int DC> __device__ __forceinline__ void add_acc(uint32_t at, f32x16_t (&acc)[DC / 32], float mine, float theirs, int lane) {
+template <int DC>
+__device__ __forceinline__ void add_acc(uint32_t at, f32x16_t (&acc)[DC / 32], float mine, float theirs, int lane) {
 #pragma unroll
   for (int db = 0; db < DC / 32; ++db)
 #pragma unroll

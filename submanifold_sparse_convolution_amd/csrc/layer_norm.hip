@@ -263,7 +263,8 @@ __global__ __launch_bounds__(kSumColumns * kSumRows) void layer_norm_weight_grad
 }
 
 constexpr int kMaxChannels = 16384;
-constexpr int kGridLimit = 256 * 4;  // workgroups of the forward pass (135,826 x 1024 bf16: 101 us; eight a compute unit 119)
+// workgroups of the forward pass (135,826 x 1024 bf16: 101 us; eight a compute unit 119)
+constexpr int kGridLimit = 256 * 4;
 
 struct Forward {
   const void *x, *gamma, *beta;
@@ -301,8 +302,12 @@ int short_lanes(int chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunk
 // whose gradients and weights stay in registers too, or 3 where a wave then spares a row its
 // barriers (60,000 x 700 float32: 95 us, four waves a row 107); up to 16,384 channels, beyond which
 // float32 rows would not fit.
-int lanes_for(const Forward&, int chunks) { return chunks <= 64 ? short_lanes(chunks) : chunks <= 256 ? 64 : chunks <= 1024 ? 256 : 1024; }
-int lanes_for(const Backward&, int chunks) { return chunks <= 64 ? short_lanes(chunks) : chunks <= 192 ? 64 : chunks <= 512 ? 256 : 1024; }
+int lanes_for(const Forward&, int chunks) {
+  return chunks <= 64 ? short_lanes(chunks) : chunks <= 256 ? 64 : chunks <= 1024 ? 256 : 1024;
+}
+int lanes_for(const Backward&, int chunks) {
+  return chunks <= 64 ? short_lanes(chunks) : chunks <= 192 ? 64 : chunks <= 512 ? 256 : 1024;
+}
 
 int limit_for(const Forward&, int) { return kGridLimit; }
 int limit_for(const Backward&, int chunks) { return parts_limit(chunks); }

@@ -129,6 +129,31 @@ def test_scores_that_grow_and_peak(dtype, d):
     check(q, k, v, g, offsets(ql), offsets(kl), dtype, scale=0.0)
 
 
+@pytest.mark.parametrize("dtype,ql,kl,heads,kv_heads,d", [
+    ("f32", [2100], [2100], 17, 17, 32), ("bf16", [2100], [2100], 29, 29, 128), ("f16", [2100], [2100], 46, 46, 64),
+    ("bf16", [900, 300], [2500, 2200], 64, 16, 96), ("f16", [2300], [2060], 30, 30, 120)])
+def test_a_few_tiles_past_a_full_machine(dtype, ql, kl, heads, kv_heads, d):
+    # the last tiles, those of the last heads, are worked on in parts: the first, a middle and the last
+    # key head and their query heads against the oracle
+    print(dtype, ql, kl, heads, kv_heads, d, flush=True)
+    q, k, v, g = make(ql, kl, heads, kv_heads, d, dtype, 16)
+    qo, ko = offsets(ql), offsets(kl)
+    qd, kd = on_device(qo), on_device(ko)
+    out, lse = sc.sparse_attention_forward(q, k, v, qd, kd)
+    grads = sc.sparse_attention_backward(g, q, k, v, out, lse, qd, kd)
+    torch.cuda.synchronize()
+    group, u_p = heads // kv_heads, 0.0 if dtype == "f32" else U[dtype]
+    for h in (0, kv_heads // 2, kv_heads - 1):
+        qh, kh = slice(h * group, (h + 1) * group), slice(h, h + 1)
+        a = [f64(t) for t in (q[:, qh], k[:, kh], v[:, kh])]
+        gh = f64(g[:, qh])
+        want = (*ref.attention(*a, qo, ko, d ** -0.5), *ref.attention_grad(gh, *a, qo, ko, d ** -0.5))
+        bounds = ref.attention_error_bounds(*a, qo, ko, d ** -0.5, U[dtype], TINY[dtype], u_p, gh)
+        got = (out[:, qh], lse[:, qh], grads[0][:, qh], grads[1][:, kh], grads[2][:, kh])
+        for name, x, w, b in zip(("out", "lse", "dq", "dk", "dv"), got, want, bounds):
+            within(x, w, b + (0.0 if name == "lse" else TINY[dtype]), name)
+
+
 @pytest.mark.parametrize("g_scale", [1e-6, 1.0, 100.0])
 def test_float16_gradients_of_any_size(g_scale):
     # (gradients below the subnormals of float16 cannot come out: dq, dk, dv carry 1e-6 * ... as far
