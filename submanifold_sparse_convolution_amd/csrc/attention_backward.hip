@@ -11,6 +11,11 @@
 // would fall among or under the subnormals.  p is scaled by 2^15 (p <= 1), and e by the power of
 // two that takes the largest |dout| of its row (for dq) or of its item and head (for dk) to
 // [1, 2); the results are scaled back in float32.  bfloat16 has float32's range and needs neither.
+//
+// Bound by the matrix cores and, at 64 channels, by the exponentials.  Measured: items of 9,000 and
+// 7,384 tokens, 16 heads of 128, bf16: dq 1.43 ms (3 products, 1.16 PFLOP/s, matrix cores busy 65 %),
+// dk and dv 2.1 ms (4 products, 1.06 PFLOP/s, 54 %); five items of up to 2,971 tokens, 12 / 4 heads of
+// 64, f16: dq 115 us (0.69 PFLOP/s), dk and dv 168 us (0.63).
 #include <algorithm>
 #include <cmath>
 

