@@ -14,8 +14,8 @@
  * No call synchronises.  Every result is bitwise reproducible from run to run: no sum goes
  * through atomics.
  *
- * sparse_layer_norm_backward (with weight gradients), sparse_attention_forward (few query rows)
- * and sparse_attention_backward keep partial results in scratch memory of the stream, which grows
+ * sparse_layer_norm_backward (with weight gradients), sparse_attention_forward and
+ * sparse_attention_backward may keep partial results in scratch memory of the stream, which grows
  * to the largest call so far and is given back by subm_release_cached_memory.  It cannot grow
  * under graph capture (SUBM_ERR_UNSUPPORTED): make the call once on the capturing stream before.
  * A captured call stays valid until subm_release_cached_memory; its replays run on that stream.
@@ -159,8 +159,9 @@ int sparse_rope_backward(const subm_heads_t* dy, int64_t n, int heads, int head_
  *   out          may be q (same strides); it must not overlap k or v.
  * Scores, the running maximum and sum, and out accumulate in float32.  With 16-bit storage the
  * probabilities are rounded to it for the product with v.  Rows of one item never meet values of
- * another, whatever they hold.  When there are few query rows the keys are split over workgroups
- * and joined by a second kernel, with float32 partial results in the stream's scratch memory.
+ * another, whatever they hold.  Where query rows do not fill the compute units evenly, keys are split
+ * over workgroups and joined by a second kernel, with float32 partial results in the stream's scratch
+ * memory.
  * Errors: SUBM_ERR_INVALID_ARG, SUBM_ERR_UNSUPPORTED, SUBM_ERR_OUT_OF_MEMORY, SUBM_ERR_HIP.
  */
 int sparse_attention_forward(const subm_heads_t* q, const subm_heads_t* k, const subm_heads_t* v, int64_t nq,
