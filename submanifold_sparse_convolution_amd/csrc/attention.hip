@@ -381,7 +381,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   if constexpr (kWide) {
     const int64_t slots = rows / 256 + a.items;
     if (slots * a.kv_heads >= kUnits && rows / a.items >= 256) {
-      a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, kUnits, 0);
+      a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, kUnits, 0, kGainAt128);
       if (a.cut.parts > 1) return launch_cut<D, DC, 8, kCutLast>(a, stream);
       SUBM_HIP_TRY((launch_tiles<D, DC, 8, 1, kNoCut>(a, stream)));
       return Status{};
@@ -392,7 +392,7 @@ Status launch(FwdArgs a, hipStream_t stream) {
   // ms, 1.39 in parts), nor at the short items that are left here at 128.
   const int64_t slots = rows / 128 + a.items, tiles = slots * a.kv_heads;
   constexpr int kFew = kUnits * (D == DT::F32 ? 1 : 2);
-  a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, D == DT::F32 ? kUnits : INT32_MAX, kFew);
+  a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, D == DT::F32 ? kUnits : INT32_MAX, kFew, kGain);
   // Where a compute unit gets one workgroup, two groups of waves on each tile (2,000 tokens, 16 heads
   // of 128: 42 us, 54 in two parts; with fewer than 512 keys the join eats the gain).  float32 waves
   // need the registers of two.

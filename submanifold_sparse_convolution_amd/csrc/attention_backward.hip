@@ -513,8 +513,11 @@ Status launch(BwdArgs a, hipStream_t stream) {
   constexpr int kResident = kWide ? INT32_MAX : kUnits * (D == DT::F32 ? 1 : 3);  // of 4 waves
   a.q_rows = q_rows;
   a.q_slots = rows / q_rows + a.items;
-  a.q_cut = plan_cut(a.q_slots, a.kv_heads, spare, a.nk / a.items, kLeast, wide_q ? kUnits : kResident, kFew);
-  a.k_cut = plan_cut(a.nk / k_rows + a.items, a.kv_heads, spare, rows / a.items, kLeast, wide_k ? kUnits : kResident, kFew);
+  constexpr double kLess = kWide ? kGainAt128 : kGain;
+  const int64_t k_slots = a.nk / k_rows + a.items;
+  const int64_t q_full = wide_q ? kUnits : kResident, k_full = wide_k ? kUnits : kResident;
+  a.q_cut = plan_cut(a.q_slots, a.kv_heads, spare, a.nk / a.items, kLeast, q_full, kFew, kLess);
+  a.k_cut = plan_cut(k_slots, a.kv_heads, spare, rows / a.items, kLeast, k_full, kFew, kLess);
 
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));

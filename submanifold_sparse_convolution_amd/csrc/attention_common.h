@@ -151,6 +151,12 @@ struct Cut {
   bool by_tile;
 };
 
+// At 128 channels in 16 bits a half-empty last round runs at a higher clock, and parts must gain more
+// than elsewhere.  16 heads of 128, bf16: 6,100 tokens, 128 of 384 tiles in 2 parts: 329 -> 304 us, 7,000
+// tokens, 192 of 448 in 4: 395 -> 413; as large last rounds elsewhere, forward and backward: float32,
+// 3,500 tokens, 16 heads of 64: 2.09 -> 1.91 ms, bf16, 10,500 tokens, 16 heads of 64: 2.28 -> 2.18 ms.
+constexpr double kGain = 0.8, kGainAt128 = 0.65;
+
 struct Share {
   int head, slot;
   int part;   // -1: the whole tile
@@ -203,7 +209,8 @@ __device__ __forceinline__ int part_steps(const Cut& c, int part, int* steps) {
 // of 128, 288 tiles: 240 and 174 us, with the backward pass 1,040 and 738; 24,576 tokens, 1,552 tiles:
 // 2.35 and 2.23 ms; 9,000 tokens, 12 heads of 64, with the backward pass: 1,370 and 1,150 us; float32,
 // 5,000 tokens, 8 heads of 64, with it: 2.95 and 1.91 ms.
-inline Cut plan_cut(int64_t slots, int kv_heads, int64_t spare, int64_t walked, int least, int64_t resident, int64_t few) {
+inline Cut plan_cut(int64_t slots, int kv_heads, int64_t spare, int64_t walked, int least, int64_t resident, int64_t few,
+                    double gain) {
   const int64_t tiles = slots * kv_heads;
   Cut c{(int)slots, (int)tiles, 0, 1, false};
   const int64_t most = walked / least;
@@ -213,10 +220,10 @@ inline Cut plan_cut(int64_t slots, int kv_heads, int64_t spare, int64_t walked, 
     return c;
   }
   // The tiles past the last full round, in the number of parts whose rounds take least of a tile's
-  // time; not for a gain below a fifth of a tile, nor where empty slots blur where a round ends.
+  // time, if that is less than `gain` of it and empty slots do not blur where a round ends.
   const int64_t rest = tiles % resident;
   if (rest == 0 || spare * 4 > resident || walked < 2048) return c;
-  double best = 0.8;
+  double best = gain;
   for (int64_t parts = 2; parts <= 16 && parts <= most; ++parts) {
     const double t = (double)((rest * parts + resident - 1) / resident) / parts + 0.01 * parts;
     if (t < best) {
