@@ -370,9 +370,9 @@ template <DT D, int DC, int W, int CUT> Status launch_cut(FwdArgs a, hipStream_t
 template <DT D, int DC>
 Status launch(FwdArgs a, hipStream_t stream) {
   // 128 channels: 8 waves on one tile stream halve what each row reads of it (24,576 tokens, 16
-  // heads: 2.33 ms, 4 waves 2.80), where they fill the compute units.  64 channels: 4 waves and
-  // three workgroups a compute unit, whose exponentials, the bound there, overlap (9,371 rows,
-  // 12 heads: 47.9 us, 8 waves 66.7).
+  // heads, whole tiles: 2.33 ms, 4 waves 2.80), where they fill the compute units.  64 channels: 4
+  // waves and three workgroups a compute unit, whose exponentials, the bound there, overlap (9,371
+  // rows, 12 heads: 47.9 us, 8 waves 66.7).
   constexpr int kUnits = 256;
   constexpr bool kWide = D != DT::F32 && tile_width(DC) == 128;
   const int64_t rows = a.nq * (a.heads / a.kv_heads), keys = a.nk / a.items, spare = (int64_t)a.items * a.kv_heads;
