@@ -306,11 +306,12 @@ void release_map(submconv_map* m) {
 
 namespace {
 // Per-(device, stream) scratch buffers (packed weights of the neighbour-pool convolution, partial
-// results of the attention and layer norm gradients): at most kScratchStreams per device; the
-// oldest goes back to the pool, in order after the work on its own stream, when a new stream needs
-// one.  A buffer that a later call outgrows is kept (each at least doubles, so all of them are
-// below twice the last): a captured graph may hold its address, and another thread's call may be
-// about to use it.
+// results of the attention and layer norm gradients), one for each stream that has needed one, kept
+// until subm_release_cached_memory.  None is taken back for another stream: a captured graph may
+// hold its address, and the free would be enqueued on a stream that another thread may be
+// capturing or may have destroyed.  A buffer that a later call outgrows is kept (each at least
+// doubles, so all of them are below twice the last): a captured graph may hold its address, and
+// another thread's call may be about to use it.
 struct ScratchEntry {
   hipStream_t stream = nullptr;
   void* ptr = nullptr;
@@ -323,11 +324,11 @@ struct ScratchCache {
   std::vector<ScratchEntry> entries;
 };
 ScratchCache g_scratch[kMaxDevices];
-constexpr size_t kScratchStreams = 16;
 
+// (after the device has been waited for, so on the null stream: the entry's own may be gone)
 void free_scratch(const ScratchEntry& e) {
-  device_free(e.ptr, e.stream);
-  for (void* p : e.outgrown) device_free(p, e.stream);
+  device_free(e.ptr, nullptr);
+  for (void* p : e.outgrown) device_free(p, nullptr);
 }
 }  // namespace
 
@@ -357,10 +358,6 @@ Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void*
   Status s = device_alloc(&p, want, stream);
   if (!s.ok()) return s;
   if (mine == nullptr) {
-    if (c.entries.size() >= kScratchStreams) {
-      free_scratch(c.entries.front());
-      c.entries.erase(c.entries.begin());
-    }
     c.entries.push_back(ScratchEntry{});
     mine = &c.entries.back();
     mine->stream = stream;
@@ -742,7 +739,7 @@ extern "C" int subm_release_cached_memory(void) {
     ws.tag = 0;
     if (e != hipSuccess) return fail(hip_status(e, "subm_release_cached_memory workspace"));
   }
-  for (const CachedBlock& b : cache.blocks) device_free(b.ptr, b.stream);
+  for (const CachedBlock& b : cache.blocks) device_free(b.ptr, nullptr);  // (its own stream may be gone)
   cache.blocks.clear();
   for (const ScratchEntry& x : sc.entries) free_scratch(x);
   sc.entries.clear();
