@@ -18,7 +18,10 @@
  * sparse_attention_backward may keep partial results in scratch memory of the stream, which grows
  * to the largest call so far and is given back by subm_release_cached_memory.  It cannot grow
  * under graph capture (SUBM_ERR_UNSUPPORTED): make the call once on the capturing stream before.
- * A captured call stays valid until subm_release_cached_memory; its replays run on that stream.
+ * The scratch memory of captured calls is kept apart from that of other calls: a captured call stays
+ * valid until subm_release_cached_memory, and its graph may be replayed on any stream.  Calls that
+ * were captured on one stream share their scratch memory, so replays of different graphs from one
+ * stream must not overlap.
  */
 #ifndef SPARSE_TRANSFORMER_H
 #define SPARSE_TRANSFORMER_H

@@ -299,12 +299,15 @@ hipError_t launch_pool_conv(const PoolTiling& t, const void* plan, const uint32_
                             const void* feats, const void* weight, const void* bias, void* out, void* wpk,
                             hipStream_t stream);
 
+// Whether work enqueued on the stream is being captured into a graph.
+bool stream_captures(hipStream_t stream);
+
 // Per-(device, stream) scratch of at least `bytes`, reused by every call on that stream (work on
 // one stream is ordered, so a later call cannot overwrite it while an earlier one still reads
-// it); grows by a stream-ordered allocation and keeps what it outgrows; SUBM_ERR_UNSUPPORTED when
-// it would have to grow under graph capture (submconv_api.hip).  The caller holds
-// scratch_launch_lock from before the call until its last launch that uses the memory: launches of
-// two threads on one stream must not interleave on it.
+// it); captured calls have scratch apart from it, which is the graphs'.  Grows by a stream-ordered
+// allocation and keeps what it outgrows; SUBM_ERR_UNSUPPORTED when it would have to grow under graph
+// capture (submconv_api.hip).  The caller holds scratch_launch_lock from before the call until its
+// last launch that uses the memory: launches of two threads on one stream must not interleave on it.
 std::unique_lock<std::mutex> scratch_launch_lock(int dev);
 Status stream_scratch(int dev, hipStream_t stream, size_t bytes, void** ptr);
 

@@ -309,13 +309,16 @@ namespace {
 // results of the attention and layer norm gradients), one for each stream that has needed one, kept
 // until subm_release_cached_memory.  None is taken back for another stream: a captured graph may
 // hold its address, and the free would be enqueued on a stream that another thread may be
-// capturing or may have destroyed.  A buffer that a later call outgrows is kept (each at least
-// doubles, so all of them are below twice the last): a captured graph may hold its address, and
-// another thread's call may be about to use it.
+// capturing or may have destroyed.  The memory of a captured call is the graphs' from then on (the
+// next eager call on the stream gets its own), so a replay on another stream does not meet the
+// stream's eager work.  A buffer that a later call outgrows is kept (each at least doubles, so all
+// of them are below twice the last): a captured graph may hold its address.
 struct ScratchEntry {
   hipStream_t stream = nullptr;
   void* ptr = nullptr;
   size_t bytes = 0;
+  void* graph_ptr = nullptr;
+  size_t graph_bytes = 0;
   std::vector<void*> outgrown;
 };
 struct ScratchCache {
@@ -328,9 +331,18 @@ ScratchCache g_scratch[kMaxDevices];
 // (after the device has been waited for, so on the null stream: the entry's own may be gone)
 void free_scratch(const ScratchEntry& e) {
   device_free(e.ptr, nullptr);
+  device_free(e.graph_ptr, nullptr);
   for (void* p : e.outgrown) device_free(p, nullptr);
 }
 }  // namespace
+
+// (An error, as for the null stream while another stream captures, is left to the launch to report.)
+bool submconv::stream_captures(hipStream_t stream) {
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &capture) == hipSuccess) return capture != hipStreamCaptureStatusNone;
+  (void)hipGetLastError();
+  return false;
+}
 
 std::unique_lock<std::mutex> submconv::scratch_launch_lock(int dev) {
   return std::unique_lock<std::mutex>(g_scratch[dev >= 0 && dev < kMaxDevices ? dev : 0].launch);
@@ -344,15 +356,24 @@ Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void*
   ScratchEntry* mine = nullptr;
   for (ScratchEntry& e : c.entries)
     if (e.stream == stream) mine = &e;
+  if (stream_captures(stream)) {
+    if (mine != nullptr && mine->graph_bytes < bytes && mine->bytes >= bytes) {
+      if (mine->graph_ptr != nullptr) mine->outgrown.push_back(mine->graph_ptr);
+      mine->graph_ptr = mine->ptr;
+      mine->graph_bytes = mine->bytes;
+      mine->ptr = nullptr;
+      mine->bytes = 0;
+    }
+    if (mine == nullptr || mine->graph_bytes < bytes)
+      return make_status(SUBM_ERR_UNSUPPORTED,
+                         "the stream's scratch memory cannot grow under graph capture: make the call once on this stream before");
+    *ptr = mine->graph_ptr;
+    return Status{};
+  }
   if (mine != nullptr && mine->bytes >= bytes) {
     *ptr = mine->ptr;
     return Status{};
   }
-  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
-  SUBM_HIP_TRY(hipStreamIsCapturing(stream, &capture));
-  if (capture != hipStreamCaptureStatusNone)
-    return make_status(SUBM_ERR_UNSUPPORTED,
-                       "the stream's scratch memory cannot grow under graph capture: make the call once on this stream before");
   const size_t want = round_up(std::max(bytes, mine != nullptr ? 2 * mine->bytes : 0), size_t(1) << 20);
   void* p = nullptr;
   Status s = device_alloc(&p, want, stream);
@@ -361,7 +382,7 @@ Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void*
     c.entries.push_back(ScratchEntry{});
     mine = &c.entries.back();
     mine->stream = stream;
-  } else {
+  } else if (mine->ptr != nullptr) {
     mine->outgrown.push_back(mine->ptr);
   }
   mine->ptr = p;

@@ -68,3 +68,29 @@ def test_a_graph_outlives_the_scratch_of_many_streams():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(captured, eager)), round_
+
+
+def test_a_graph_replays_beside_its_stream():
+    # the graph's scratch memory is not that of eager calls on the stream it was captured on: both may run at once
+    inputs, step = training_step(1500, 4, 64, 2)
+    home, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(home):
+        want = [e.clone() for e in step()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=home):
+            captured = step()
+    rows, eager_step = training_step(1400, 4, 64, 3)
+    eager_want = [e.clone() for e in eager_step()]
+    torch.cuda.synchronize()
+    for round_ in range(10):
+        with torch.cuda.stream(home):
+            eager = [eager_step() for _ in range(3)]
+        with torch.cuda.stream(other):
+            for _ in range(3):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, want)), round_
+        for run in eager:
+            assert all(torch.equal(a, b) for a, b in zip(run, eager_want)), round_
