@@ -185,10 +185,10 @@ int sparse_indice_map_offset_counts(submconv_map_t map, int64_t* counts);
  *     cells per row and 2 GiB), both sized for the largest build so far, rounded up to 64 MiB;
  *   - the rulebook blocks of freed maps kept for reuse on their stream (at most 8 and at most
  *     1 GiB; a block is 112 bytes per row);
- *   - one scratch buffer for each stream that needed one: the packed weights of the neighbour-pool
- *     kernel (27 x 128 x cin x 2 bytes, rounded up to 1 MiB) and the partial results of the operators of
- *     sparse_transformer.h, grown to the largest call so far; outgrown buffers are kept too (all
- *     together below twice the last).
+ *   - one scratch buffer for each stream that needed one, the size of its largest call so far
+ *     (rounded up to 1 MiB): the packed weights of the neighbour-pool kernel (27 x 128 x cin x 2
+ *     bytes) and the partial results of the operators of sparse_transformer.h; and what calls
+ *     captured into graphs have been given.
  * Live maps keep their own memory (rulebook, plan), freed with them; the static array of
  * subm_conv3d_forward_noalloc (1,769,472 bytes) stays for the life of the process.  The call
  * waits for all work on the device (hipDeviceSynchronize) while it holds the library's locks, so

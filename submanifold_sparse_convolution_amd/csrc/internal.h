@@ -305,8 +305,8 @@ bool stream_captures(hipStream_t stream);
 // Per-(device, stream) scratch of at least `bytes`, reused by every call on that stream (work on
 // one stream is ordered, so a later call cannot overwrite it while an earlier one still reads
 // it); captured calls have scratch apart from it, which is the graphs'.  Grows by a stream-ordered
-// allocation and keeps what it outgrows; SUBM_ERR_UNSUPPORTED when it would have to grow under graph
-// capture (submconv_api.hip).  The caller holds scratch_launch_lock from before the call until its
+// free and allocation; SUBM_ERR_UNSUPPORTED when it would have to grow under graph capture
+// (submconv_api.hip).  The caller holds scratch_launch_lock from before the call until its
 // last launch that uses the memory: launches of two threads on one stream must not interleave on it.
 std::unique_lock<std::mutex> scratch_launch_lock(int dev);
 Status stream_scratch(int dev, hipStream_t stream, size_t bytes, void** ptr);

@@ -311,15 +311,15 @@ namespace {
 // hold its address, and the free would be enqueued on a stream that another thread may be
 // capturing or may have destroyed.  The memory of a captured call is the graphs' from then on (the
 // next eager call on the stream gets its own), so a replay on another stream does not meet the
-// stream's eager work.  A buffer that a later call outgrows is kept (each at least doubles, so all
-// of them are below twice the last): a captured graph may hold its address.
+// stream's eager work.  An eager buffer that a later call outgrows goes back to the pool in order
+// after the work on its stream; the graphs' are kept.
 struct ScratchEntry {
   hipStream_t stream = nullptr;
   void* ptr = nullptr;
   size_t bytes = 0;
   void* graph_ptr = nullptr;
   size_t graph_bytes = 0;
-  std::vector<void*> outgrown;
+  std::vector<void*> graph_outgrown;
 };
 struct ScratchCache {
   std::mutex mu;
@@ -332,7 +332,7 @@ ScratchCache g_scratch[kMaxDevices];
 void free_scratch(const ScratchEntry& e) {
   device_free(e.ptr, nullptr);
   device_free(e.graph_ptr, nullptr);
-  for (void* p : e.outgrown) device_free(p, nullptr);
+  for (void* p : e.graph_outgrown) device_free(p, nullptr);
 }
 }  // namespace
 
@@ -358,7 +358,7 @@ Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void*
     if (e.stream == stream) mine = &e;
   if (stream_captures(stream)) {
     if (mine != nullptr && mine->graph_bytes < bytes && mine->bytes >= bytes) {
-      if (mine->graph_ptr != nullptr) mine->outgrown.push_back(mine->graph_ptr);
+      if (mine->graph_ptr != nullptr) mine->graph_outgrown.push_back(mine->graph_ptr);
       mine->graph_ptr = mine->ptr;
       mine->graph_bytes = mine->bytes;
       mine->ptr = nullptr;
@@ -374,17 +374,18 @@ Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void*
     *ptr = mine->ptr;
     return Status{};
   }
-  const size_t want = round_up(std::max(bytes, mine != nullptr ? 2 * mine->bytes : 0), size_t(1) << 20);
-  void* p = nullptr;
-  Status s = device_alloc(&p, want, stream);
-  if (!s.ok()) return s;
   if (mine == nullptr) {
     c.entries.push_back(ScratchEntry{});
     mine = &c.entries.back();
     mine->stream = stream;
-  } else if (mine->ptr != nullptr) {
-    mine->outgrown.push_back(mine->ptr);
   }
+  device_free(mine->ptr, stream);
+  mine->ptr = nullptr;
+  mine->bytes = 0;
+  const size_t want = round_up(bytes, size_t(1) << 20);
+  void* p = nullptr;
+  Status s = device_alloc(&p, want, stream);
+  if (!s.ok()) return s;
   mine->ptr = p;
   mine->bytes = want;
   *ptr = p;

@@ -1,5 +1,7 @@
 """The scratch memory of the transformer-block operators: many streams, captured graphs, streams that
 share a handle."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -94,3 +96,29 @@ def test_a_graph_replays_beside_its_stream():
         assert all(torch.equal(a, b) for a, b in zip(captured, want)), round_
         for run in eager:
             assert all(torch.equal(a, b) for a, b in zip(run, eager_want)), round_
+
+
+def pool_used():
+    """Bytes of the device's memory pool in use (the library's stream-ordered allocations)."""
+    hip = sc.load_library()  # (its dependencies resolve through it)
+    pool, used = ctypes.c_void_p(), ctypes.c_uint64()
+    assert hip.hipDeviceGetDefaultMemPool(ctypes.byref(pool), ctypes.c_int(0)) == 0
+    assert hip.hipMemPoolGetAttribute(pool, ctypes.c_int(0x7), ctypes.byref(used)) == 0  # hipMemPoolAttrUsedMemCurrent
+    return used.value
+
+
+def test_scratch_memory_is_that_of_the_largest_call():
+    sc.subm_release_cached_memory()
+    base, sizes = pool_used(), (1000, 1700, 2500, 4000, 6000, 9000)
+    for n in sizes:  # the backward pass keeps two floats a query row and head, 64 heads of 8: 512 n bytes, whole tiles
+        inputs, step = training_step(n, 64, 8, 4)
+        step()
+        torch.cuda.synchronize()
+    held = pool_used() - base
+    sc.subm_release_cached_memory()
+    alone = training_step(sizes[-1], 64, 8, 4)[1]
+    before = pool_used()
+    alone()
+    torch.cuda.synchronize()
+    print(f"  after {sizes} queries {held} bytes, after the last alone {pool_used() - before}", flush=True)
+    assert held == pool_used() - before
