@@ -28,7 +28,8 @@
  *     16-byte-multiple row sizes take the vectorised kernels; anything else takes a slower
  *     element-wise path with identical results.
  *   - Scalars and out-parameters named in the signatures as host values are HOST pointers.
- *   - All device work is enqueued on `stream` (0 = the null stream).  Nothing throws across the
+ *   - All device work is enqueued on `stream` (0 = the null stream; hipStreamPerThread is the calling
+ *     thread's own, and a map built on it is freed by that thread).  Nothing throws across the
  *     ABI: every call returns an int status (subm_status_t); on error out-parameters are left
  *     as documented and subm_last_error() gives a thread-local message.
  *   - The library keeps a device memory pool per GPU (stream-ordered allocations whose release

@@ -354,10 +354,10 @@ template <DT D, int DC, int W, int CUT> Status launch_cut(FwdArgs a, hipStream_t
   constexpr int DP = tile_width(DC);
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));
-  const auto launches = scratch_launch_lock(dev);
+  ScratchLease lease;
   const size_t rows = (size_t)cut_places(a.cut) * 32 * W;
   void* scratch = nullptr;
-  Status st = stream_scratch(dev, stream, rows * (DP * sizeof(float) + sizeof(float2)), &scratch);
+  Status st = lease.take(dev, stream, rows * (DP * sizeof(float) + sizeof(float2)), &scratch);
   if (!st.ok()) return st;
   a.part = static_cast<float*>(scratch);
   a.state = reinterpret_cast<float2*>(a.part + rows * DP);

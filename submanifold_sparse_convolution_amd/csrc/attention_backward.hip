@@ -521,7 +521,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
 
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));
-  const auto launches = scratch_launch_lock(dev);
+  ScratchLease lease;
   const auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
   // norm and d of every query row, a peak for each query block, and the parts
   const size_t stat = padded((size_t)rows * a.kv_heads * sizeof(float));
@@ -529,7 +529,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
   const size_t part_q = (size_t)cut_places(a.q_cut) * q_rows * DP * sizeof(float);
   const size_t part_k = (size_t)cut_places(a.k_cut) * k_rows * DP * sizeof(float);
   void* scratch = nullptr;
-  Status st = stream_scratch(dev, stream, 2 * stat + peak + part_q + 2 * part_k, &scratch);
+  Status st = lease.take(dev, stream, 2 * stat + peak + part_q + 2 * part_k, &scratch);
   if (!st.ok()) return st;
   unsigned char* p = static_cast<unsigned char*>(scratch);
   a.norm = reinterpret_cast<float*>(p);

@@ -1675,7 +1675,7 @@ hipError_t launch_subm_conv(const MapData* map, int64_t n, int ksize, int cin, i
   a.weight_bytes = wb < kOffsetLimit ? (uint32_t)wb : 0u;
   a.gate = gate;
   a.gate_n = gate_n;
-  if (ksize == 3 && map->order_block != nullptr && stream == map->order_stream) {
+  if (ksize == 3 && map->order_block != nullptr && same_stream(stream, map->order_stream)) {
     const OrderView v = order_view(map->order_block, map->n);
     a.order_gate = v.gate;
     a.order_rows = v.rows;

@@ -302,14 +302,25 @@ hipError_t launch_pool_conv(const PoolTiling& t, const void* plan, const uint32_
 // Whether work enqueued on the stream is being captured into a graph.
 bool stream_captures(hipStream_t stream);
 
-// Per-(device, stream) scratch of at least `bytes`, reused by every call on that stream (work on
-// one stream is ordered, so a later call cannot overwrite it while an earlier one still reads
-// it); captured calls have scratch apart from it, which is the graphs'.  Grows by a stream-ordered
-// free and allocation; SUBM_ERR_UNSUPPORTED when it would have to grow under graph capture
-// (submconv_api.hip).  The caller holds scratch_launch_lock from before the call until its
-// last launch that uses the memory: launches of two threads on one stream must not interleave on it.
-std::unique_lock<std::mutex> scratch_launch_lock(int dev);
-Status stream_scratch(int dev, hipStream_t stream, size_t bytes, void** ptr);
+// Scratch memory of one call: per-(device, stream) memory of at least `bytes`, reused by every call
+// on that stream (work on one stream is ordered, so a later call cannot overwrite it while an earlier
+// one still reads it); captured calls have scratch apart from it, which is the graphs'.  Grows by a
+// stream-ordered free and allocation; SUBM_ERR_UNSUPPORTED when it would have to grow under graph
+// capture (submconv_api.hip).  The call holds the lease until its last launch that uses the memory:
+// launches of two threads on one stream must not interleave on it.  On hipStreamPerThread the memory
+// is the lease's alone, allocated and freed in stream order.
+class ScratchLease {
+ public:
+  ScratchLease() = default;
+  ScratchLease(const ScratchLease&) = delete;
+  ScratchLease& operator=(const ScratchLease&) = delete;
+  ~ScratchLease();
+  Status take(int dev, hipStream_t stream, size_t bytes, void** ptr);
+
+ private:
+  std::unique_lock<std::mutex> launches_;
+  void* own_ = nullptr;
+};
 
 }  // namespace submconv
 
@@ -344,13 +355,16 @@ Status map_check(submconv_map* map);
 // Makes map->d.pairs / per_tap valid (waits for the build's last kernel on first use); fails with
 // the build's coordinate status.
 Status map_counts(submconv_map* map);
+// Whether two handles name one stream whose work is ordered.  hipStreamPerThread is one handle for a
+// stream of its own in every thread.
+inline bool same_stream(hipStream_t a, hipStream_t b) { return a == b && a != hipStreamPerThread; }
 // Records that work reading the map's memory is enqueued on `stream` (every entry point that
 // reads a map calls it before enqueuing); a map used only on the stream of its build gives its
 // memory back to the per-device block cache when freed (map_memory_give).
 // Work enqueued on another stream than the build's is also ordered after the build: the stream
 // waits for the build's last kernel unless it has already completed.
 inline void map_note_use(submconv_map* map, hipStream_t stream) {
-  if (map != nullptr && stream != map->d.home) {
+  if (map != nullptr && !same_stream(stream, map->d.home)) {
     map->other_streams.store(true, std::memory_order_relaxed);
     if (map->d.ready != nullptr && hipEventQuery(map->d.ready) != hipSuccess)
       (void)hipStreamWaitEvent(stream, map->d.ready, 0);

@@ -423,14 +423,13 @@ extern "C" int sparse_layer_norm_backward(const void* dy, const void* x, int64_t
     if (n == 0 && dgamma == nullptr) return SUBM_OK;
     Backward b{dy, x, gamma, mean, rstd, dx, nullptr};
     const int blocks = blocks_for(b, n, channels, dtype);
-    std::unique_lock<std::mutex> launches;
+    ScratchLease lease;
     if (dgamma != nullptr) {
       int dev = 0;
       hipError_t e = hipGetDevice(&dev);
       if (e != hipSuccess) return fail(hip_status(e, "hipGetDevice"));
-      launches = scratch_launch_lock(dev);
       void* scratch = nullptr;
-      st = stream_scratch(dev, stream, std::max<size_t>((size_t)blocks * 2 * channels * sizeof(float), 16), &scratch);
+      st = lease.take(dev, stream, std::max<size_t>((size_t)blocks * 2 * channels * sizeof(float), 16), &scratch);
       if (!st.ok()) return fail(st);
       b.part = static_cast<float*>(scratch);
     }

@@ -297,7 +297,7 @@ void release_map(submconv_map* m) {
   device_free(m->d.pair_out, m->d.home);  // (work on other streams has completed: the free rules)
   // the plan block goes to the cache when the plan and every use of the map ran on the map's stream
   map_memory_give(m->d.device, m->d.pool_plan, m->d.pool_plan_bytes, m->d.home,
-                  !m->other_streams.load(std::memory_order_relaxed) && m->d.pool_stream == m->d.home);
+                  !m->other_streams.load(std::memory_order_relaxed) && same_stream(m->d.pool_stream, m->d.home));
   device_free(m->d.order_block, m->d.order_stream);  // (in order after the calls that used it)
   delete m;
 }
@@ -323,7 +323,7 @@ struct ScratchEntry {
 };
 struct ScratchCache {
   std::mutex mu;
-  std::mutex launch;  // held from taking a buffer to the last launch that uses it (scratch_launch_lock)
+  std::mutex launch;  // held from taking a buffer to the last launch that uses it (ScratchLease)
   std::vector<ScratchEntry> entries;
 };
 ScratchCache g_scratch[kMaxDevices];
@@ -344,13 +344,19 @@ bool submconv::stream_captures(hipStream_t stream) {
   return false;
 }
 
-std::unique_lock<std::mutex> submconv::scratch_launch_lock(int dev) {
-  return std::unique_lock<std::mutex>(g_scratch[dev >= 0 && dev < kMaxDevices ? dev : 0].launch);
-}
+submconv::ScratchLease::~ScratchLease() { device_free(own_, hipStreamPerThread); }
 
-Status submconv::stream_scratch(int dev, hipStream_t stream, size_t bytes, void** ptr) {
+Status submconv::ScratchLease::take(int dev, hipStream_t stream, size_t bytes, void** ptr) {
   *ptr = nullptr;
   if (dev < 0 || dev >= kMaxDevices) return make_status(SUBM_ERR_HIP, "device ordinal out of range");
+  if (stream == hipStreamPerThread) {
+    if (stream_captures(stream))
+      return make_status(SUBM_ERR_UNSUPPORTED, "no scratch memory under graph capture on hipStreamPerThread");
+    Status s = device_alloc(&own_, bytes, stream);
+    *ptr = own_;
+    return s;
+  }
+  launches_ = std::unique_lock<std::mutex>(g_scratch[dev].launch);
   ScratchCache& c = g_scratch[dev];
   std::lock_guard<std::mutex> lock(c.mu);
   ScratchEntry* mine = nullptr;
@@ -402,7 +408,7 @@ Status submconv::map_memory_take(int dev, size_t bytes, hipStream_t stream, void
     for (size_t i = 0; i < cache.blocks.size(); ++i) {
       const CachedBlock& b = cache.blocks[i];
       // (at most twice the size asked for, so a small map does not hold a large block)
-      if (b.stream == stream && b.bytes >= bytes && b.bytes / 2 <= bytes &&
+      if (same_stream(b.stream, stream) && b.bytes >= bytes && b.bytes / 2 <= bytes &&
           (best < 0 || b.bytes < cache.blocks[best].bytes))
         best = (int)i;
     }
@@ -420,7 +426,7 @@ Status submconv::map_memory_take(int dev, size_t bytes, hipStream_t stream, void
 
 void submconv::map_memory_give(int dev, void* ptr, size_t bytes, hipStream_t stream, bool reusable) {
   if (ptr == nullptr) return;
-  if (reusable && dev >= 0 && dev < kMaxDevices) {
+  if (reusable && stream != hipStreamPerThread && dev >= 0 && dev < kMaxDevices) {
     BlockCache& cache = g_blocks[dev];
     std::lock_guard<std::mutex> lock(cache.mu);
     size_t held = 0;
@@ -729,7 +735,7 @@ Status pool_prepare(submconv_map* map, hipStream_t stream, int* state) {
   if (d.pool_state == 1 && hipEventQuery(d.pool_slot.ready) == hipSuccess)
     d.pool_state = reinterpret_cast<volatile MapHostFlags*>(d.pool_slot.host)->flags != 0u ? 3 : 2;
   // work on another stream than the plan's waits for the plan kernel
-  if (d.pool_state == 1 && stream != d.pool_stream) SUBM_HIP_TRY(hipStreamWaitEvent(stream, d.pool_slot.ready, 0));
+  if (d.pool_state == 1 && !same_stream(stream, d.pool_stream)) SUBM_HIP_TRY(hipStreamWaitEvent(stream, d.pool_slot.ready, 0));
   *state = d.pool_state;
   return Status{};
 }
@@ -825,8 +831,8 @@ extern "C" int subm_conv3d_forward(submconv_map_t map, int64_t n, int ksize, int
     if (!s.ok()) return fail(s);
     if (state != 3) {
       void* wpk = nullptr;
-      const auto launches = scratch_launch_lock(map->d.device);
-      s = stream_scratch(map->d.device, stream, pool_weight_bytes(cin), &wpk);
+      ScratchLease lease;
+      s = lease.take(map->d.device, stream, pool_weight_bytes(cin), &wpk);
       if (!s.ok()) return fail(s);
       // state 1: the plan's flags are not known on the host yet, so the conv.hip kernel is launched
       // behind the pool kernel and each of the two runs only if the tile flags say it should
@@ -845,14 +851,14 @@ extern "C" int subm_conv3d_forward(submconv_map_t map, int64_t n, int ksize, int
   std::unique_lock<std::mutex> order_lock;
   if (map != nullptr) order_lock = std::unique_lock<std::mutex>(map->mu);
   if (ksize == 3 && n >= kOrderMinRows && dtype != SUBM_F32 && cout > 32 && map->d.order_block == nullptr &&
-      stream == map->d.home && !map->other_streams.load(std::memory_order_relaxed) && row_order_enabled() &&
+      same_stream(stream, map->d.home) && !map->other_streams.load(std::memory_order_relaxed) && row_order_enabled() &&
       ++map->d.order_calls == 2) {
     void* blk = nullptr;
     void* scr = nullptr;
-    const auto launches = scratch_launch_lock(map->d.device);
+    ScratchLease lease;
     hipError_t e = hipMallocAsync(&blk, order_block_bytes(n), stream);
     if (e != hipSuccess) return fail(hip_status(e, "row order allocation"));
-    s = stream_scratch(map->d.device, stream, order_scratch_bytes(n), &scr);
+    s = lease.take(map->d.device, stream, order_scratch_bytes(n), &scr);
     if (!s.ok()) {
       device_free(blk, stream);
       return fail(s);
@@ -909,7 +915,7 @@ extern "C" int subm_conv3d_forward_noalloc(submconv_map_t map, int64_t n, int ks
       MapData& d = map->d;
       if (d.pool_state == 1 && hipEventQuery(d.pool_slot.ready) == hipSuccess)
         d.pool_state = reinterpret_cast<volatile MapHostFlags*>(d.pool_slot.host)->flags != 0u ? 3 : 2;
-      if (d.pool_state == 1 && stream != d.pool_stream) {
+      if (d.pool_state == 1 && !same_stream(stream, d.pool_stream)) {
         const hipError_t we = hipStreamWaitEvent(stream, d.pool_slot.ready, 0);
         if (we != hipSuccess) return fail(hip_status(we, "subm_conv3d_forward_noalloc stream wait"));
       }

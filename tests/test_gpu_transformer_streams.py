@@ -1,6 +1,7 @@
 """The scratch memory of the transformer-block operators: many streams, captured graphs, streams that
 share a handle."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -122,3 +123,75 @@ def test_scratch_memory_is_that_of_the_largest_call():
     torch.cuda.synchronize()
     print(f"  after {sizes} queries {held} bytes, after the last alone {pool_used() - before}", flush=True)
     assert held == pool_used() - before
+
+
+PER_THREAD = 2  # hipStreamPerThread: one handle, a stream of its own in every thread
+
+
+def in_threads(*work):
+    """Runs each function in a thread of its own, all at once; raises what one of them raised."""
+    errors, start = [], threading.Barrier(len(work))
+
+    def run(f):
+        try:
+            start.wait(30)
+            f()
+            assert sc.load_library().hipStreamSynchronize(ctypes.c_void_p(PER_THREAD)) == 0
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(f,)) for f in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if errors:
+        raise errors[0]
+
+
+def test_threads_on_their_own_streams():
+    # scratch memory under the handle that all threads share is not shared
+    sets = {}
+    for n in (900, 1500):
+        (q, k, v, g), step = training_step(n, 4, 64, n)
+        x = torch.randn(n, 256, device=DEV)
+        _, mean, rstd = sc.sparse_layer_norm_forward(x, stats=True)
+        want = [*step(), *sc.sparse_layer_norm_backward(x, x, mean, rstd)[:1]]
+        runs = [[torch.empty_like(t) for t in want] for _ in range(12)]
+        sets[n] = (q, k, v, g, on_device([n // 3, n - n // 3]), x, mean, rstd, want, runs)
+    torch.cuda.synchronize()
+
+    def work(n):
+        q, k, v, g, o, x, mean, rstd, want, runs = sets[n]
+        for out, lse, dq, dk, dv, dx in runs:
+            sc.sparse_attention_forward(q, k, v, o, out=out, lse=lse, stream=PER_THREAD)
+            sc.sparse_attention_backward(g, q, k, v, out, lse, o, dq=dq, dk=dk, dv=dv, stream=PER_THREAD)
+            sc.sparse_layer_norm_backward(x, x, mean, rstd, weight_grads=False, out=dx, stream=PER_THREAD)
+
+    in_threads(lambda: work(900), lambda: work(1500))
+    for *_, want, runs in sets.values():
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(run, want))
+
+
+def test_maps_of_threads_on_their_own_streams():
+    # nor are the memory blocks of freed maps
+    sets = []
+    for key, step in (("2a", 1), ("2a", 2)):
+        coords = torch.from_numpy(np.ascontiguousarray(synth.coords_for(key)[::step])).to(DEV)
+        feats = torch.randn(coords.shape[0], 64, device=DEV).to(torch.bfloat16)
+        weight = (torch.randn(64, 3, 3, 3, 64, device=DEV) / 40).to(torch.bfloat16)
+        with sc.sparse_indice_map_build(coords) as m:
+            want = sc.subm_conv3d_forward(m, feats, weight)
+        sets.append((coords, feats, weight, want, [torch.empty_like(want) for _ in range(12)]))
+    torch.cuda.synchronize()
+
+    def work(coords, feats, weight, want, runs):
+        for out in runs:
+            with sc.sparse_indice_map_build(coords, stream=PER_THREAD) as m:
+                sc.subm_conv3d_forward(m, feats, weight, out=out, stream=PER_THREAD)
+
+    in_threads(*(lambda s=s: work(*s) for s in sets))
+    for *_, want, runs in sets:
+        assert all(torch.equal(run, want) for run in runs)
