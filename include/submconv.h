@@ -267,6 +267,12 @@ int sparse_indice_map_copy_nbr(submconv_map_t map, int32_t* nbr, hipStream_t str
  * the device say it should; sparse_indice_map_plan_state reports the plan's state.  Every other
  * call takes the general kernels.  Both families compute the same sums (results differ by
  * summation order only, within the storage rounding).
+ * Graph capture.  A captured call allocates and builds nothing: where the plan or the buffer of the
+ * packed weights is missing (no such call ran on the map and the stream before) it takes the general
+ * kernels, and the sparse-row order (sparse_indice_map_row_order_state) is left to a later call.
+ * Captured calls have a packed-weight buffer apart from other calls', kept until
+ * subm_release_cached_memory; those captured on one stream share it, so replays of different graphs
+ * from one stream must not overlap.  The map must outlive the graph.
  * Tuning and tests: the environment variable SUBMCONV_POOL=0 keeps the general kernels,
  * SUBMCONV_TILE=<name> forces one of their tile configurations (and the general kernels), and
  * SUBMCONV_PERSISTENT=0 launches one workgroup per row tile instead of one per compute unit

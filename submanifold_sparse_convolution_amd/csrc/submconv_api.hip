@@ -85,8 +85,11 @@ Status device_alloc(void** ptr, size_t bytes, hipStream_t stream) {
   Status s = ensure_pool(dev);
   if (!s.ok()) return s;
   *ptr = nullptr;
-  SUBM_HIP_TRY(hipMallocAsync(ptr, bytes, stream));
-  return Status{};
+  const hipError_t e = hipMallocAsync(ptr, bytes, stream);
+  if (e == hipSuccess) return Status{};
+  (void)hipGetLastError();  // (else the next launch's check would report it)
+  *ptr = nullptr;
+  return hip_status(e, "hipMallocAsync");
 }
 
 void device_free(void* ptr, hipStream_t stream) {
@@ -709,11 +712,14 @@ bool pool_eligible(const submconv_map* map, int64_t n, int ksize, int cin, int c
 
 // Builds the map's plan on first use (enqueued on `stream`; the overflow flag arrives in the
 // plan's pinned word) and reads the flag once the plan kernel has completed.  Returns the
-// map's pool_state (1: built, flag not read yet; 2: usable; 3: overflowed).
+// map's pool_state (1: built, flag not read yet; 2: usable; 3: overflowed); under graph capture 3
+// also where the plan would have to be built or waited for.
 Status pool_prepare(submconv_map* map, hipStream_t stream, int* state) {
   std::lock_guard<std::mutex> lock(map->mu);
   MapData& d = map->d;
+  *state = 3;
   if (d.pool_state == 0) {
+    if (stream_captures(stream)) return Status{};
     PoolTiling t;
     if (!pool_tiling(d.n, &t)) return make_status(SUBM_ERR_HIP, "internal error: no neighbour-pool tiling");
     Status s = take_flag_slot(d.device, &d.pool_slot);
@@ -735,7 +741,10 @@ Status pool_prepare(submconv_map* map, hipStream_t stream, int* state) {
   if (d.pool_state == 1 && hipEventQuery(d.pool_slot.ready) == hipSuccess)
     d.pool_state = reinterpret_cast<volatile MapHostFlags*>(d.pool_slot.host)->flags != 0u ? 3 : 2;
   // work on another stream than the plan's waits for the plan kernel
-  if (d.pool_state == 1 && !same_stream(stream, d.pool_stream)) SUBM_HIP_TRY(hipStreamWaitEvent(stream, d.pool_slot.ready, 0));
+  if (d.pool_state == 1 && !same_stream(stream, d.pool_stream)) {
+    if (stream_captures(stream)) return Status{};
+    SUBM_HIP_TRY(hipStreamWaitEvent(stream, d.pool_slot.ready, 0));
+  }
   *state = d.pool_state;
   return Status{};
 }
@@ -829,11 +838,14 @@ extern "C" int subm_conv3d_forward(submconv_map_t map, int64_t n, int ksize, int
     int state = 0;
     s = pool_prepare(map, stream, &state);
     if (!s.ok()) return fail(s);
+    void* wpk = nullptr;
+    ScratchLease lease;
     if (state != 3) {
-      void* wpk = nullptr;
-      ScratchLease lease;
       s = lease.take(map->d.device, stream, pool_weight_bytes(cin), &wpk);
-      if (!s.ok()) return fail(s);
+      if (s.code == SUBM_ERR_UNSUPPORTED) state = 3;  // (under graph capture, before any call on the stream)
+      else if (!s.ok()) return fail(s);
+    }
+    if (state != 3) {
       // state 1: the plan's flags are not known on the host yet, so the conv.hip kernel is launched
       // behind the pool kernel and each of the two runs only if the tile flags say it should
       const uint32_t* gate = state == 1 ? pool_tile_flags(map->d.pool_tiling, map->d.pool_plan) : nullptr;
@@ -847,29 +859,29 @@ extern "C" int subm_conv3d_forward(submconv_map_t map, int64_t n, int ksize, int
     }
   }
   // A large map's second convolution on the matrix-core walk enqueues its sparse-row order (built
-  // only where rows have few neighbours, decided on the device; row_order.hip).
+  // only where rows have few neighbours, decided on the device; row_order.hip).  Calls under graph
+  // capture do not count, and where its memory is not to be had the map keeps its input order.
   std::unique_lock<std::mutex> order_lock;
   if (map != nullptr) order_lock = std::unique_lock<std::mutex>(map->mu);
-  if (ksize == 3 && n >= kOrderMinRows && dtype != SUBM_F32 && cout > 32 && map->d.order_block == nullptr &&
+  if (ksize == 3 && n >= kOrderMinRows && dtype != SUBM_F32 && cout > 32 && map->d.order_calls < 2 &&
       same_stream(stream, map->d.home) && !map->other_streams.load(std::memory_order_relaxed) && row_order_enabled() &&
-      ++map->d.order_calls == 2) {
+      !stream_captures(stream) && ++map->d.order_calls == 2) {
     void* blk = nullptr;
     void* scr = nullptr;
     ScratchLease lease;
-    hipError_t e = hipMallocAsync(&blk, order_block_bytes(n), stream);
-    if (e != hipSuccess) return fail(hip_status(e, "row order allocation"));
-    s = lease.take(map->d.device, stream, order_scratch_bytes(n), &scr);
-    if (!s.ok()) {
+    s = device_alloc(&blk, order_block_bytes(n), stream);
+    if (s.ok()) s = lease.take(map->d.device, stream, order_scratch_bytes(n), &scr);
+    if (s.ok()) {
+      const hipError_t e = launch_row_order(&map->d, blk, scr, stream);
+      if (e != hipSuccess) {
+        device_free(blk, stream);
+        return fail(hip_status(e, "row order launch"));
+      }
+      map->d.order_block = blk;
+      map->d.order_stream = stream;
+    } else {
       device_free(blk, stream);
-      return fail(s);
     }
-    e = launch_row_order(&map->d, blk, scr, stream);
-    if (e != hipSuccess) {
-      device_free(blk, stream);
-      return fail(hip_status(e, "row order launch"));
-    }
-    map->d.order_block = blk;
-    map->d.order_stream = stream;
   }
   hipError_t e = launch_subm_conv(map == nullptr ? nullptr : &map->d, n, ksize, cin, cout, dtype, feats, weight, bias, out, stream);
   if (e != hipSuccess) return fail(hip_status(e, "subm_conv3d_forward launch"));

@@ -195,3 +195,65 @@ def test_maps_of_threads_on_their_own_streams():
     in_threads(*(lambda s=s: work(*s) for s in sets))
     for *_, want, runs in sets:
         assert all(torch.equal(run, want) for run in runs)
+
+
+def conv_case(cout):
+    """A set of at least 131,072 rows, 64 input channels: 128 output channels take the neighbour-pool
+    kernel, 64 the walk that a second call reorders."""
+    gen = torch.Generator(device="cpu").manual_seed(cout)
+    coords = torch.from_numpy(synth.coords_for("3a")).to(DEV)
+    feats = torch.randn(coords.shape[0], 64, generator=gen).to(torch.bfloat16).to(DEV)
+    weight = (torch.randn(cout, 3, 3, 3, 64, generator=gen) / 40).to(torch.bfloat16).to(DEV)
+    return coords, feats, weight
+
+
+def capture(m, feats, weight, stream):
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = sc.subm_conv3d_forward(m, feats, weight)
+    return graph, out
+
+
+def test_a_convolution_is_captured_without_any_call_before(monkeypatch):
+    monkeypatch.delenv("SUBMCONV_POOL", raising=False)
+    coords, feats, weight = conv_case(128)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s), sc.sparse_indice_map_build(coords) as m:
+        graph, captured = capture(m, feats, weight, s)  # neither plan nor packed weights yet
+        assert sc.sparse_indice_map_plan_state(m) == sc.SUBM_PLAN_NONE
+        monkeypatch.setenv("SUBMCONV_POOL", "0")
+        general = sc.subm_conv3d_forward(m, feats, weight)
+        monkeypatch.delenv("SUBMCONV_POOL")
+        pool = sc.subm_conv3d_forward(m, feats, weight)
+        torch.cuda.synchronize()
+        assert sc.sparse_indice_map_plan_state(m) == sc.SUBM_PLAN_READY
+        warm, captured_pool = capture(m, feats, weight, s)
+        for _ in range(3):
+            captured.zero_()
+            captured_pool.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            warm.replay()
+            again = sc.subm_conv3d_forward(m, feats, weight)
+            torch.cuda.synchronize()
+            assert torch.equal(captured, general) and torch.equal(captured_pool, pool) and torch.equal(again, pool)
+
+
+def test_a_second_call_on_a_map_is_captured():
+    coords, feats, weight = conv_case(64)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s), sc.sparse_indice_map_build(coords) as m:
+        want = sc.subm_conv3d_forward(m, feats, weight)
+        graph, captured = capture(m, feats, weight, s)
+        assert sc.sparse_indice_map_row_order_state(m) == sc.SUBM_ORDER_NONE  # left to a later call
+        ordered = sc.subm_conv3d_forward(m, feats, weight)
+        assert sc.sparse_indice_map_row_order_state(m) != sc.SUBM_ORDER_NONE
+        for _ in range(3):
+            captured.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(captured, want) and torch.equal(ordered, want)
