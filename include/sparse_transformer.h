@@ -182,8 +182,9 @@ int sparse_attention_forward(const subm_heads_t* q, const subm_heads_t* k, const
  *   lse            the forward pass's, required.
  * A query without keys gets dq = 0, a key without queries dk = dv = 0.  With 16-bit storage p and
  * ds are rounded to it for their products; with SUBM_F16 both are scaled by powers of two first
- * (ds by the largest |dout| of its row for dq, of its item and head for dk), so that small
- * gradients keep their digits.  Other arguments and errors as in the forward pass.
+ * (ds by the largest |dout| of its row for dq, of its item and head for dk, or by what the item's
+ * longest row of v leaves room for), so that small gradients keep their digits and none overflows
+ * before the products.  Other arguments and errors as in the forward pass.
  */
 int sparse_attention_backward(const subm_heads_t* dout, const subm_heads_t* q, const subm_heads_t* k,
                               const subm_heads_t* v, const subm_heads_t* out, const float* lse, int64_t nq,

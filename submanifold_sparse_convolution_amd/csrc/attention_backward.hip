@@ -10,7 +10,11 @@
 // float16 storage: p spans 2^-24 and below for long items, e is as small as the gradient; both
 // would fall among or under the subnormals.  p is scaled by 2^15 (p <= 1), and e by the power of
 // two that takes the largest |dout| of its row (for dq) or of its item and head (for dk) to
-// [1, 2); the results are scaled back in float32.  bfloat16 has float32's range and needs neither.
+// [1, 2), or by the smaller one that keeps 2 |dout|_2 max_j |v_j|_2, which no |dp - d| exceeds (d is
+// a mean of dp), below 2^15; the results are scaled back in float32.  A kernel before the others
+// leaves the norms of v (7,813 tokens, 4 key heads of 64: 4 us on the device, the whole training call
+// 371 -> 376 us; 800 tokens, 8 heads of 64: 42 -> 46).  bfloat16 has float32's range and needs none of
+// this.
 //
 // Bound by the matrix cores and, at 64 channels, by the exponentials.  Measured: items of 9,000 and
 // 7,384 tokens, 16 heads of 128, bf16: dq 1.43 ms (3 products, 1.16 PFLOP/s, matrix cores busy 65 %),
@@ -28,9 +32,12 @@ struct BwdArgs {
   subm_heads_t dout, q, k, v, out, dq, dk, dv;
   const float* lse;
   float *norm, *delta;  // [kv_heads, nq * group]: log2 of each packed row's normaliser (less kF16Shift), and d
-  float* peak;      // [kv_heads, slots]: the largest |dout| of each query block (float16 only)
+  // float16 only: [kv_heads, q_slots] the largest |dout| and bound of |dp - d| of each query block,
+  // and [kv_heads, v_slots] a bound of |v|_2 over each block of kNormKeys keys
+  float2* peak;
+  float* v_norm;
   const int64_t *q_offsets, *k_offsets;
-  int64_t nq, nk, q_slots;
+  int64_t nq, nk, q_slots, v_slots;
   int items, heads, kv_heads, head_dim;
   float scale;
   int q_rows;  // packed rows of a workgroup of the dq kernel
@@ -42,12 +49,40 @@ struct BwdArgs {
 
 constexpr int kStep = 32;  // rows of the walked tile
 
+constexpr int kNormKeys = 256;  // keys of a workgroup of the kernel that leaves v's norms
+
 constexpr float kF16Shift = 15.f;  // p is scaled by 2^15 in float16 products
 
 // 2^-floor(log2 x): the power of two that takes x to [1, 2); 1 for 0, subnormal and non-finite x.
 __device__ __forceinline__ float unit_scale(float x) {
   const int e = (int)(__float_as_uint(x) >> 23) & 255;
   return e == 0 || e >= 254 ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
+}
+
+// The power of two for e (see the top): from the largest |dout| and a bound of |dp - d|.
+__device__ __forceinline__ float e_scale(float peak, float bound) {
+  return fminf(unit_scale(peak), unit_scale(bound) * 16384.f);
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int mk = 32; mk >= 1; mk >>= 1) v = fmaxf(v, __shfl_xor(v, mk, 64));
+  return v;
+}
+
+// A bound of |v|_2 over the item's keys, from their blocks: the same in every thread of the
+// workgroup, all of which call it (`slots`: a float a wave).
+template <int W> __device__ __forceinline__ float item_norm(const BwdArgs& a, int head, int item, int64_t k0, int nk, float* slots) {
+  const float* norms = a.v_norm + head * a.v_slots + k0 / kNormKeys + item;
+  const int blocks = (int)(((int64_t)nk + kNormKeys - 1) / kNormKeys);
+  float v = 0.f;
+  for (int t = threadIdx.x; t < blocks; t += W * 64) v = fmaxf(v, norms[t]);
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) v = fmaxf(v, slots[w]);
+  return v;
 }
 
 template <DT D> __device__ __forceinline__ float absmax_frag(const Frag<D>& f) {
@@ -86,6 +121,42 @@ template <int DC> __device__ __forceinline__ void store_part(float* row, const f
           make_float4(acc[db][4 * i] * f, acc[db][4 * i + 1] * f, acc[db][4 * i + 2] * f, acc[db][4 * i + 3] * f);
 }
 
+// A bound of |v|_2 over each block of keys (blockIdx.x of those, blockIdx.y the key head): 16 lanes a
+// row, each with the largest square sum of its 8 channels, added up (one sum a block and not one a
+// row; the longest row's norm is between a quarter of the bound and all of it).
+template <DT D> __global__ __launch_bounds__(256) void attention_norm_kernel(BwdArgs a) {
+  __shared__ float s_top[64];
+  const int head = blockIdx.y, c = threadIdx.x % 16 * 8;
+  int tile;
+  const int item = find_item(a.k_offsets, a.nk, a.items, 1, kNormKeys, blockIdx.x, &tile);
+  int64_t k0;
+  int nk;
+  item_rows(a.k_offsets, a.nk, item, &k0, &nk);
+  const int64_t first = (int64_t)tile * kNormKeys;
+  if (first >= nk) return;
+  const int rows = (int)(nk - first < kNormKeys ? nk - first : kNormKeys);
+  const Heads<D> v = heads_of<D>(a.v);
+  const typename Elem<D>::T* p = v.data + (k0 + first) * v.row + (int64_t)head * v.head + c;
+  Frag<D> f[kNormKeys / 16];
+#pragma unroll
+  for (int i = 0; i < kNormKeys / 16; ++i) {
+    const int r = i * 16 + threadIdx.x / 16;
+    f[i].v[0] = r < rows && c < a.head_dim ? *reinterpret_cast<const uint4*>(p + (int64_t)r * v.row) : make_uint4(0, 0, 0, 0);
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kNormKeys / 16; ++i) top = fmaxf(top, dot_frag<D>(f[i], f[i], 0.f));
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  if ((threadIdx.x & 63) < 16) s_top[threadIdx.x / 64 * 16 + threadIdx.x % 64] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sq += fmaxf(fmaxf(s_top[i], s_top[16 + i]), fmaxf(s_top[32 + i], s_top[48 + i]));
+  a.v_norm[head * a.v_slots + blockIdx.x] = sqrtf(sq);
+}
+
 // d of the own query rows, then dq over the keys, which stream through LDS in tiles of 32.  As in
 // the forward pass a step holds independent pieces of work:
 //   scores and dp of tile t + 1 (k, v),  e of tile t,  product of tile t - 1 (k).
@@ -95,7 +166,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   constexpr int kTile = kStep * kRowBytes<D, DP>;
   using Loader = TileLoader<D, DP, kStep, W>;
   __shared__ __attribute__((aligned(1024))) unsigned char s_kv[6 * kTile];  // four tiles of k, two of v
-  __shared__ float s_peak[W];
+  __shared__ float2 s_peak[W];
+  __shared__ float s_norm[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads;
   const Share share = share_of<CUT>(a.q_cut, blockIdx.x);
@@ -120,13 +192,16 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   const typename Elem<D>::T* qrow = qmap.at<D>(heads_of<D>(a.q), safe);
   const typename Elem<D>::T* grow = qmap.at<D>(heads_of<D>(a.dout), safe);
   const typename Elem<D>::T* orow = qmap.at<D>(heads_of<D>(a.out), safe);
-  float d = 0.f, peak = 0.f;
+  float d = 0.f, peak = 0.f, sq = 0.f;
 #pragma unroll
   for (int kk = 0; kk < DC / 16; ++kk) {
     qf[kk] = own_frag<D>(qrow, there, kk, a.head_dim, lane);
     gf[kk] = own_frag<D>(grow, there, kk, a.head_dim, lane);
     d = dot_frag<D>(gf[kk], own_frag<D>(orow, there, kk, a.head_dim, lane), d);
-    if constexpr (D == DT::F16) peak = fmaxf(peak, absmax_frag<D>(gf[kk]));
+    if constexpr (D == DT::F16) {
+      peak = fmaxf(peak, absmax_frag<D>(gf[kk]));
+      sq = dot_frag<D>(gf[kk], gf[kk], sq);
+    }
   }
   d = half_sum(d);
   const bool first = CUT == kNoCut || share.part <= 0;  // (every part needs d, one leaves it for dk and dv)
@@ -139,15 +214,16 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   float unit = 1.f;
   if constexpr (D == DT::F16) {
     peak = half_max(peak);
-    unit = unit_scale(peak);
-#pragma unroll
-    for (int mk = 16; mk >= 1; mk >>= 1) peak = fmaxf(peak, __shfl_xor(peak, mk, 64));
-    if (lane == 0) s_peak[wave] = peak;
+    const float bound = 2.f * sqrtf(half_sum(sq)) * item_norm<W>(a, head, item, k0, nk, s_norm);
+    unit = e_scale(peak, bound);
+    const float2 top = make_float2(wave_max(peak), wave_max(bound));
+    if (lane == 0) s_peak[wave] = top;
     __syncthreads();
     if (first && threadIdx.x == 0) {
+      float2 all = top;
 #pragma unroll
-      for (int w = 0; w < W; ++w) peak = fmaxf(peak, s_peak[w]);
-      a.peak[head * a.q_slots + share.slot] = peak;
+      for (int w = 0; w < W; ++w) all = make_float2(fmaxf(all.x, s_peak[w].x), fmaxf(all.y, s_peak[w].y));
+      a.peak[head * a.q_slots + share.slot] = all;
     }
   }
   const float c = a.scale * kLog2e;
@@ -271,7 +347,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   // q, q, dout, dout, own v
   __shared__ __attribute__((aligned(1024))) unsigned char s_qg[4 * kTile + (kParked ? W * kTile : 0)];
   __shared__ __attribute__((aligned(16))) float s_stat[2 * 2 * 64];  // norm and d of two tiles
-  __shared__ float s_peak[W];
+  __shared__ float2 s_peak[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads;
   const Share share = share_of<CUT>(a.k_cut, blockIdx.x);
@@ -292,18 +368,19 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   const float* delta = a.delta + head * (a.nq * group) + q0 * group;
 
   float unit = 1.f;
-  if constexpr (D == DT::F16) {  // the largest |dout| of the item and head, from its query blocks
+  if constexpr (D == DT::F16) {  // the largest |dout| and bound of the item and head, from its query blocks
     const int64_t first = q0 * group / a.q_rows + item;
-    float peak = 0.f;
-    for (int t = threadIdx.x; t < (rows + a.q_rows - 1) / a.q_rows; t += W * 64)
-      peak = fmaxf(peak, a.peak[head * a.q_slots + first + t]);
-#pragma unroll
-    for (int mk = 32; mk >= 1; mk >>= 1) peak = fmaxf(peak, __shfl_xor(peak, mk, 64));
-    if (lane == 0) s_peak[wave] = peak;
+    float2 top = make_float2(0.f, 0.f);
+    for (int t = threadIdx.x; t < (rows + a.q_rows - 1) / a.q_rows; t += W * 64) {
+      const float2 b = a.peak[head * a.q_slots + first + t];
+      top = make_float2(fmaxf(top.x, b.x), fmaxf(top.y, b.y));
+    }
+    top = make_float2(wave_max(top.x), wave_max(top.y));
+    if (lane == 0) s_peak[wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < W; ++w) peak = fmaxf(peak, s_peak[w]);
-    unit = unit_scale(peak);
+    for (int w = 0; w < W; ++w) top = make_float2(fmaxf(top.x, s_peak[w].x), fmaxf(top.y, s_peak[w].y));
+    unit = e_scale(top.x, top.y);
   }
   const float p_unit = D == DT::F16 ? 1.f / 32768.f : 1.f;
 
@@ -523,23 +600,32 @@ Status launch(BwdArgs a, hipStream_t stream) {
   SUBM_HIP_TRY(hipGetDevice(&dev));
   ScratchLease lease;
   const auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
-  // norm and d of every query row, a peak for each query block, and the parts
+  // norm and d of every query row, peaks of query and key blocks, and the parts
   const size_t stat = padded((size_t)rows * a.kv_heads * sizeof(float));
-  const size_t peak = padded((size_t)a.q_slots * a.kv_heads * sizeof(float));
+  a.v_slots = a.nk / kNormKeys + a.items;
+  const size_t peak = D == DT::F16 ? padded((size_t)a.q_slots * a.kv_heads * sizeof(float2)) : 0;
+  const size_t norm = D == DT::F16 ? padded((size_t)a.v_slots * a.kv_heads * sizeof(float)) : 0;
   const size_t part_q = (size_t)cut_places(a.q_cut) * q_rows * DP * sizeof(float);
   const size_t part_k = (size_t)cut_places(a.k_cut) * k_rows * DP * sizeof(float);
   void* scratch = nullptr;
-  Status st = lease.take(dev, stream, 2 * stat + peak + part_q + 2 * part_k, &scratch);
+  Status st = lease.take(dev, stream, 2 * stat + peak + norm + part_q + 2 * part_k, &scratch);
   if (!st.ok()) return st;
   unsigned char* p = static_cast<unsigned char*>(scratch);
   a.norm = reinterpret_cast<float*>(p);
   a.delta = reinterpret_cast<float*>(p + stat);
-  a.peak = reinterpret_cast<float*>(p + 2 * stat);
-  p += 2 * stat + peak;
+  a.peak = reinterpret_cast<float2*>(p + 2 * stat);
+  a.v_norm = reinterpret_cast<float*>(p + 2 * stat + peak);
+  p += 2 * stat + peak + norm;
   if (part_q > 0) a.dq_part = reinterpret_cast<float*>(p);
   if (part_k > 0) {
     a.dk_part = reinterpret_cast<float*>(p + part_q);
     a.dv_part = reinterpret_cast<float*>(p + part_q + part_k);
+  }
+  if constexpr (D == DT::F16) {
+    if (a.nk > 0) {
+      attention_norm_kernel<D><<<dim3((unsigned)a.v_slots, (unsigned)a.kv_heads), 256, 0, stream>>>(a);
+      SUBM_HIP_TRY(hipGetLastError());
+    }
   }
   if (a.nq > 0) {
     if constexpr (kWide) {

@@ -278,3 +278,39 @@ def test_refusals():
         sc.sparse_attention_forward(q, q, q, o, out=torch.empty((1, 4, 64), dtype=q.dtype, device=DEV).expand(8, 4, 64))
     with pytest.raises(ValueError):
         sc.sparse_attention_backward(q, q, q, q, q, None, o)
+
+
+def check_large_values(q, k, v, g, ql, kl):
+    """float16 gradients whose score gradients pass its range: the bounds of check, with the roundoff of
+    e where its power of two is that of a bound B of 2 |dout|_2 |v|_2, up to 4 times it, with B unit >= 2^14:
+    at most 2^-25 / unit <= 2^-39 B <= 2^-36 |dout|_2 |v|_2, |dout|_2 <= sqrt(D) max |dout|."""
+    qo, ko, scale = offsets(ql), offsets(kl), q.shape[2] ** -0.5
+    qd, kd = on_device(qo), on_device(ko)
+    out, lse = sc.sparse_attention_forward(q, k, v, qd, kd, scale)
+    grads = sc.sparse_attention_backward(g, q, k, v, out, lse, qd, kd, scale)
+    torch.cuda.synchronize()
+    a = [f64(t) for t in (q, k, v)]
+    tiny = max(TINY["f16"], 2.0 ** -36 * q.shape[2] ** 0.5 * np.linalg.norm(a[2], axis=2).max())
+    bounds = ref.attention_error_bounds(*a, qo, ko, scale, U["f16"], tiny, U["f16"], f64(g))[2:]
+    for name, got, w, b in zip(("dq", "dk", "dv"), grads, ref.attention_grad(f64(g), *a, qo, ko, scale), bounds):
+        assert np.abs(w).max() < 65504, name  # (float16 holds the gradient)
+        within(got, w, b + TINY["f16"], name)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_float16_gradients_against_large_values(sign):
+    # two keys with equal scores and opposite values of 3,000: e is 94, 2^10 times that passes 65,504
+    full = lambda *rows: torch.tensor(rows, device=DEV).half()[:, None, None].expand(-1, 1, 64).contiguous()  # noqa: E731
+    q, k, v, g = full(0.0, 0.0), full(0.5, 0.5 * sign), full(3000.0, -3000.0), full(2.0 ** -10, 2.0 ** -10)
+    check_large_values(q, k, v, g, [2], [2])
+
+
+@pytest.mark.parametrize("heads,kv_heads,d", [(2, 2, 64), (6, 2, 128), (4, 1, 40)])
+def test_float16_gradients_of_long_value_rows(heads, kv_heads, d):
+    # some rows of v a thousand times the others, items of their own, gradients of any size
+    ql, kl = [200, 0, 70, 300], [150, 40, 0, 1100]
+    q, k, v, g = make(ql, kl, heads, kv_heads, d, "f16", 17, q_scale=2.0, g_scale=1e-3)
+    v[::37] *= 3000
+    v[1::74] *= 400
+    check_large_values(q, k, v, g, ql, kl)
+    check_large_values(q, k, v, g * 2.0 ** -10, ql, kl)
