@@ -152,7 +152,7 @@ int sparse_rope_backward(const subm_heads_t* dy, int64_t n, int heads, int head_
  *                other values give unspecified results, but every access stays inside the tensors.
  *   items        1 .. 65535.  Items without queries or without keys are allowed: a query without
  *                keys gets out = 0 and lse = -infinity.
- *   nq, nk       0 .. 2^31 - 1, and nq * heads <= 2^31 - 1.
+ *   nq, nk       0 .. 2^31 - 2^24, and nq * heads <= 2^31 - 2^24.
  *   heads        at most 128 a key head.
  *   head_dim     a multiple of 8, 8 .. 128.  data 16-byte aligned, strides multiples of 16 bytes
  *                (else SUBM_ERR_UNSUPPORTED); row strides of at most 2^22 bytes, head strides of at

@@ -421,14 +421,17 @@ template <DT D> Status launch_dim(const FwdArgs& a, hipStream_t stream) {
 Status check_attention(const AttentionShape& s) {
   if (s.dtype != SUBM_F32 && s.dtype != SUBM_F16 && s.dtype != SUBM_BF16)
     return make_status(SUBM_ERR_UNSUPPORTED, "dtype must be SUBM_F32, SUBM_F16 or SUBM_BF16");
-  if (s.nq < 0 || s.nk < 0 || s.nq > INT32_MAX || s.nk > INT32_MAX)
-    return make_status(SUBM_ERR_INVALID_ARG, "nq and nk must be 0 .. 2^31 - 1");
+  // Rows are counted in 32 bits, up to a few tiles past the last, and a launch of 256 threads for each
+  // 128 of them (and one more an item) has at most 2^32 - 1.
+  constexpr int64_t kMost = (int64_t(1) << 31) - (int64_t(1) << 24);
+  if (s.nq < 0 || s.nk < 0 || s.nq > kMost || s.nk > kMost)
+    return make_status(SUBM_ERR_INVALID_ARG, "nq and nk must be 0 .. 2^31 - 2^24");
   if (s.items < 1 || s.items > 65535) return make_status(SUBM_ERR_INVALID_ARG, "items must be 1 .. 65535");
   if (s.heads < 1 || s.kv_heads < 1 || s.heads % s.kv_heads != 0)
     return make_status(SUBM_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
   if (s.kv_heads > 65535) return make_status(SUBM_ERR_INVALID_ARG, "kv_heads exceeds 65535");
   if (s.heads / s.kv_heads > 128) return make_status(SUBM_ERR_UNSUPPORTED, "more than 128 query heads a key head");
-  if (s.nq * s.heads > INT32_MAX) return make_status(SUBM_ERR_INVALID_ARG, "nq * heads exceeds 2^31 - 1");
+  if (s.nq * s.heads > kMost) return make_status(SUBM_ERR_INVALID_ARG, "nq * heads exceeds 2^31 - 2^24");
   if (s.head_dim < 1) return make_status(SUBM_ERR_INVALID_ARG, "head_dim must be at least 1");
   if (s.head_dim % 8 != 0 || s.head_dim > 128)
     return make_status(SUBM_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 up to 128");

@@ -173,6 +173,19 @@ def test_attention_rejects_bad_arguments(lib):
     assert bw(nq=0, nk=0, lse=None) == OK
 
 
+def test_attention_rows_stay_within_32_bits(lib):
+    # (no queries: what passes the checks launches nothing)
+    most = 2 ** 31 - 2 ** 24
+
+    def fw(nq, nk, h=1):
+        return lib.sparse_attention_forward(heads(), heads(4096, 0, 16), heads(4096, 0, 16), nq, nk, 256, 512, 1, h, 1, 16, 2, 0.25,
+                                            heads(8192), None, None)
+
+    assert fw(0, most) == OK
+    assert fw(0, most + 1) == INVALID and fw(0, 2 ** 31 - 1) == INVALID
+    assert fw(most + 1, 1) == INVALID and fw(most // 64 + 1, 1, 64) == INVALID
+
+
 def test_binding_checks_before_calling():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError):
