@@ -161,7 +161,8 @@ int sparse_rope_backward(const subm_heads_t* dy, int64_t n, int heads, int head_
  *   lse          device float32 [nq, heads], or NULL.
  *   out          may be q (same strides); it must not overlap k or v.
  * Scores, the running maximum and sum, and out accumulate in float32.  With 16-bit storage the
- * probabilities are rounded to it for the product with v.  Rows of one item never meet values of
+ * probabilities are rounded to it for the product with v (SUBM_F16: from 2^11 for the largest score
+ * down, so that many small ones beside it keep their weight).  Rows of one item never meet values of
  * another, whatever they hold.  Where query rows do not fill the compute units evenly, keys are split
  * over workgroups and joined by a second kernel, with float32 partial results in the stream's scratch
  * memory.

@@ -52,12 +52,15 @@ template <DT D> __device__ __forceinline__ void pin(Frag<D>& f) {
 }
 
 constexpr float kNone = -1.7e38f;  // a running maximum before any score (finite: differences stay numbers)
-constexpr float kSlack = 8.f;      // a new maximum up to 2^8 above the base leaves the base
 
 // The running softmax of one own row (held by the lanes l and l + 32, half its scores each):
-// scores are kept as c * s - base in powers of two; base is a maximum that may lag behind the
-// true one by kSlack, so that most tiles do not rescale the accumulator (p stays below 2^8, which
-// every storage type holds).
+// scores are kept as c * s - base in powers of two; base is a maximum, less kLift, that may lag behind
+// the true one by kSlack, so that most tiles do not rescale the accumulator.  p stays below
+// 2^(kLift + kSlack), which the storage type holds.  float16 rounds what is below 2^-25 to zero, and
+// thousands of such keys beside one large score are not nothing (60,000 at 2^-25.5 of it are a
+// thousandth): there p starts from 2^11, and what vanishes is below 2^-36 of the largest.
+template <DT D> constexpr float kLift = D == DT::F16 ? 11.f : 0.f;
+template <DT D> constexpr float kSlack = D == DT::F16 ? 4.f : 8.f;
 struct RowState {
   float base = kNone;
   float sum = 0.f;  // of this lane's half
@@ -65,15 +68,16 @@ struct RowState {
 
 // Scores (raw) -> probabilities in place; returns the factor that earlier sums shrink by, and
 // whether any row of the wave does shrink.
-template <int KB>
+template <DT D, int KB>
 __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowState& st, float* shrink) {
   float top = s[0][0];
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
     for (int i = 0; i < 16; i += 2) top = max3(top, s[kb][i], s[kb][i + 1]);
-  top = half_max(top) * c;
-  const bool moves = __builtin_amdgcn_ballot_w64(top > st.base + kSlack) != 0;
+  top = half_max(top);
+  top = kLift<D> == 0.f ? top * c : fmaf(top, c, -kLift<D>);
+  const bool moves = __builtin_amdgcn_ballot_w64(top > st.base + kSlack<D>) != 0;
   // (a scalar gate instead of a branch, which would part the matrix products from the exponentials)
   const float base = fmaxf(st.base, top + (moves ? 0.f : -INFINITY));
   *shrink = exp2_fast(st.base - base);
@@ -218,7 +222,7 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
       }
       scores(slot ^ 1, next);
       float shrink;
-      const bool moves = softmax_tile<KB>(s, c, state, &shrink);
+      const bool moves = softmax_tile<D, KB>(s, c, state, &shrink);
       product(slot ^ 1, p);
 #pragma unroll
       for (int st = 0; st < 2 * KB; ++st) {

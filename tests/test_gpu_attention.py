@@ -314,3 +314,28 @@ def test_float16_gradients_of_long_value_rows(heads, kv_heads, d):
     v[1::74] *= 400
     check_large_values(q, k, v, g, ql, kl)
     check_large_values(q, k, v, g * 2.0 ** -10, ql, kl)
+
+
+@pytest.mark.parametrize("ql,kl,heads,d", [([1], [60001], 2, 64), ([300], [9000], 2, 64), ([2, 700], [30000, 5000], 3, 128), ([1500], [5000], 16, 128)])
+def test_float16_keys_far_below_the_largest(ql, kl, heads, d):
+    # one key per item scores 2^25.5 times the others, whose values alone are not zero: their
+    # probabilities are scaled by 2^11 at least before float16 rounds them (2^-25 / 2^11 = 2^-36)
+    rng = np.random.default_rng(18)
+    q, k, v, _ = make(ql, kl, heads, heads, d, "f16", 18)
+    v = v.abs()
+    q[..., 0], q[..., 1:] = 16.0, 0.0
+    k[..., 0], k[..., 1:] = -0.84, 0.0
+    qo, ko, scale = offsets(ql), offsets(kl), 0.125
+    for b in range(len(kl)):
+        top = ko[b] + rng.integers(kl[b])
+        k[top, :, 0] = 8.0
+        v[top] = 0.0
+    out, lse = sc.sparse_attention_forward(q, k, v, on_device(qo), on_device(ko), scale)
+    torch.cuda.synchronize()
+    few = slice(0, min(q.shape[0], 310))  # (every row is alike)
+    a = [f64(q[few]), f64(k), f64(v)]
+    qo = np.minimum(qo, few.stop)
+    want, wlse = ref.attention(*a, qo, ko, scale)
+    bounds = ref.attention_error_bounds(*a, qo, ko, scale, U["f16"], 2.0 ** -36, U["f16"])
+    within(out[few], want, bounds[0] + TINY["f16"], "out")
+    within(lse[few], wlse, bounds[1], "lse")
