@@ -12,8 +12,9 @@ from . import _binding as _b
 
 
 def _plain(t: torch.Tensor) -> torch.Tensor:
-    """A gradient as the library takes it: autograd may hand over expanded or permuted ones."""
-    return t if t.is_contiguous() else t.contiguous()
+    """A gradient as the library takes it: autograd may hand over expanded or permuted ones, and parts
+    of larger ones (of a concatenation) that start anywhere."""
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 class _LayerNorm(torch.autograd.Function):

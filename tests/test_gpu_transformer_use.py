@@ -76,6 +76,28 @@ def test_plain_norm_and_partial_gradients():
     assert torch.equal(beta.grad, torch.full_like(beta, 20.0)) and x.grad is None
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_that_start_anywhere(dtype):
+    # the gradient of a part of a concatenation is a view of the whole one, at an odd element
+    rng = np.random.default_rng(4)
+    n, heads, d = 40, 2, 16
+    off = torch.tensor([0, 15, 40], device=DEV)
+    pos = torch.arange(n, device=DEV, dtype=torch.int32)[:, None]
+    freq = sc.sparse_rope_frequencies(4)[0].to(DEV)
+    x, gamma = (leaf(rng, *shape).detach().to(dtype).requires_grad_() for shape in ((n, heads * d), (heads * d,)))
+    w = leaf(rng, 1 + n * heads * d).detach().to(dtype)
+    grads = []
+    for front in (1, 0):
+        for f in (lambda: sa.layer_norm(x, gamma), lambda: sa.rope(x.view(n, heads, d), pos, freq, sc.SUBM_ROPE_HALF),
+                  lambda: sa.attention(*[x.view(n, heads, d)] * 3, off)):
+            x.grad = None
+            y = f().reshape(-1)
+            y = torch.cat([y[:1].detach(), y]) if front else y
+            (y * w[1 - front:]).sum().backward()
+            grads.append(x.grad)
+    assert all(torch.equal(a, b) for a, b in zip(grads[:3], grads[3:]))
+
+
 def test_captured_in_a_graph():
     rng = np.random.default_rng(2)
     n, heads, d = 600, 4, 64
