@@ -487,6 +487,8 @@ extern "C" int sparse_attention_forward(const subm_heads_t* q, const subm_heads_
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return fail(SUBM_ERR_INVALID_ARG, "lse is not 4-byte aligned");
     if (nq == 0) return SUBM_OK;
     if (out->data == k->data || out->data == v->data) return fail(SUBM_ERR_INVALID_ARG, "out must not alias k or v");
+    if (out->data == q->data && ((nq > 1 && out->row_stride != q->row_stride) || (heads > 1 && out->head_stride != q->head_stride)))
+      return fail(SUBM_ERR_INVALID_ARG, "out over q needs the same strides");
     const FwdArgs a{*q, *k, *v, *out, lse, q_offsets, k_offsets, nq, nk, items, heads, kv_heads,
                     head_dim, scale, Cut{}, nullptr, nullptr};
     if (dtype == SUBM_F32) st = launch_dim<DT::F32>(a, stream);

@@ -186,6 +186,17 @@ def test_attention_rows_stay_within_32_bits(lib):
     assert fw(most + 1, 1) == INVALID and fw(most // 64 + 1, 1, 64) == INVALID
 
 
+def test_attention_over_the_queries_needs_their_strides(lib):
+    def fw(out, nq=4, h=4):  # (no device: what passes the checks fails to launch)
+        return lib.sparse_attention_forward(heads(), heads(8192), heads(12288), nq, 4, 256, 512, 1, h, h, 16, 2, 0.25, out, None, None)
+
+    assert fw(heads(4096, 128, 16)) == INVALID and fw(heads(4096, 64, 32)) == INVALID
+    assert b"strides" in lib.subm_last_error()
+    if not torch.cuda.is_available():
+        for same in (fw(heads()), fw(heads(4096, 128, 16), nq=1), fw(heads(4096, 64, 32), h=1)):
+            assert same not in (OK, INVALID)
+
+
 def test_binding_checks_before_calling():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError):
