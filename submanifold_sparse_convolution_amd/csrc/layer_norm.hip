@@ -70,9 +70,10 @@ int parts_limit(int chunks) { return chunks > 128 && chunks <= 192 ? 256 * 2 : k
 
 constexpr int threads_for(int tpr) { return tpr > 256 ? tpr : 256; }
 
+// (x may be y: neither is declared free of aliases.)
 template <DT D, int TPR, int ITEMS, bool TAIL>
 __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_forward_kernel(
-    const typename Elem<D>::T* __restrict__ x, int64_t n, int channels, const typename Elem<D>::T* __restrict__ gamma,
+    const typename Elem<D>::T* x, int64_t n, int channels, const typename Elem<D>::T* __restrict__ gamma,
     const typename Elem<D>::T* __restrict__ beta, float eps, typename Elem<D>::T* y, float* __restrict__ mean,
     float* __restrict__ rstd) {
   constexpr int V = kChunk<D>;
