@@ -339,3 +339,32 @@ def test_float16_keys_far_below_the_largest(ql, kl, heads, d):
     bounds = ref.attention_error_bounds(*a, qo, ko, scale, U["f16"], 2.0 ** -36, U["f16"])
     within(out[few], want, bounds[0] + TINY["f16"], "out")
     within(lse[few], wlse, bounds[1], "lse")
+
+
+# Kernels that the shapes above do not reach, on some heads as in test_a_few_tiles_past_a_full_machine.
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("ql,kl,heads,kv_heads,d", [
+    ([1100], [1090], 60, 60, 128), ([700, 500], [1000, 800], 64, 32, 96), ([1100], [1090], 60, 60, 88)])
+def test_eight_waves_on_whole_tiles(dtype, ql, kl, heads, kv_heads, d):
+    # 96 and 128 channels, at least 256 tiles of 256 rows and of 256 keys, too short to cut the last of them
+    test_a_few_tiles_past_a_full_machine(dtype, ql, kl, heads, kv_heads, d)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("ql,kl,heads,kv_heads", [([600], [610], 45, 45), ([300, 0, 130], [700, 40, 1300], 40, 20)])
+def test_two_groups_of_waves_on_a_tile(dtype, d, ql, kl, heads, kv_heads):
+    # up to 256 tiles of 128 rows, at least 512 keys an item, an odd and an even number of tiles of keys
+    test_a_few_tiles_past_a_full_machine(dtype, ql, kl, heads, kv_heads, d)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 96])
+@pytest.mark.parametrize("ql,kl", [([1, 1, 1], [4000, 17, 9001]), ([40], [6000])])
+def test_keys_in_parts_of_narrow_heads(dtype, d, ql, kl):
+    check(*make(ql, kl, 8, 2, d, dtype, 19), offsets(ql), offsets(kl), dtype, backward=False)
+
+
+@pytest.mark.parametrize("dtype,heads,d", [("f32", 17, 64), ("f32", 17, 80), ("f32", 17, 128), ("f16", 46, 32), ("bf16", 46, 64)])
+def test_last_tiles_in_parts(dtype, heads, d):
+    test_a_few_tiles_past_a_full_machine(dtype, [2100], [2100], heads, heads, d)

@@ -91,6 +91,12 @@ def test_shapes(dtype, n, c):
     check(*inputs(n, c, dtype, n * 7 + c), dtype, f"{dtype} n={n} C={c}")
 
 
+@pytest.mark.parametrize("dtype,n,c", [("f32", 1500, 1100), ("f16", 2100, 2056), ("bf16", 1030, 4100), ("f16", 1300, 8200), ("f32", 1100, 8193)])
+def test_rows_over_several_waves_in_turn(dtype, n, c):
+    # more rows than workgroups: each sums several through the same LDS slots
+    check(*inputs(n, c, dtype, n + c), dtype, f"{dtype} n={n} C={c}")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_rows_and_a_mean_far_from_zero(dtype):
     check(*inputs(22406, 96, dtype, 5, shift=50.0), dtype, f"{dtype} 22406 rows, mean 50")

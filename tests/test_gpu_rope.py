@@ -70,6 +70,18 @@ def test_shapes(dtype, interleaved, case):
     check(y, pos, freq, interleaved, 1.25, dtype, back=True)
 
 
+MANY = [  # several rows a workgroup (from 2,048 rows), the last one short; 40,001: as many as its sines leave; groups of heads
+    (2049, 2, 64, 3, 10), (5003, 3, 40, 1, 20), (70001, 1, 16, 1, 5), (40001, 1, 256, 1, 128), (2, 20, 4096, 1, 100),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("case", MANY)
+def test_many_rows_and_heads(dtype, interleaved, case):
+    test_shapes(dtype, interleaved, case)
+
+
 @pytest.mark.parametrize("interleaved", [True, False])
 def test_positions_beyond_the_digits_of_float32(interleaved):
     x, _ = make(6, 2, 32, "f32", 3)
