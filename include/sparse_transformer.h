@@ -157,7 +157,7 @@ int sparse_rope_backward(const subm_heads_t* dy, int64_t n, int heads, int head_
  *   head_dim     a multiple of 8, 8 .. 128.  data 16-byte aligned, strides multiples of 16 bytes
  *                (else SUBM_ERR_UNSUPPORTED); row strides of at most 2^22 bytes, head strides of at
  *                most 2^22 bytes.
- *   scale        finite.
+ *   scale        finite; the forward pass takes magnitudes below 7e-31 as that.
  *   lse          device float32 [nq, heads], or NULL.
  *   out          may be q (same strides); it must not overlap k or v.
  * Scores, the running maximum and sum, and out accumulate in float32.  With 16-bit storage the

@@ -10,10 +10,11 @@
 // a few rows against long caches, which read k and v once at HBM speed.
 //
 // Measured: items of 13,001 and 11,575 tokens, 16 heads of 128, bf16: 2.23 ms, 1.11 PFLOP/s (matrix
-// cores busy 58 % of the cycles, at a clock that the power limit holds near 1.8 GHz); four items of
-// 450 to 4,001 queries and up to 1,374 keys, 12 heads of 64, f16: 48 us, 0.53 PFLOP/s (each product of
-// 64 channels waits for as many exponentials); 8 single tokens, up to 32,768 keys each, 16 / 4 heads
-// of 128, bf16: 87 us, 4.9 TB/s.
+// cores busy 58 % of the cycles, at a clock that the power limit holds near 1.8 GHz; in a trace of 30
+// calls 2.20 to 2.29 ms); four items of 450 to 4,001 queries and up to 1,374 keys, 12 heads of 64, f16:
+// 48 us, 0.53 PFLOP/s (636 workgroups of unequal length at once, each product of 64 channels beside as
+// many exponentials); 8 single tokens, up to 32,768 keys each, 16 / 4 heads of 128, bf16: 87 us, 4.9
+// TB/s.
 #include <algorithm>
 #include <cmath>
 

@@ -17,9 +17,9 @@
 // this.
 //
 // Bound by the matrix cores and, at 64 channels, by the exponentials.  Measured: items of 9,000 and
-// 7,384 tokens, 16 heads of 128, bf16: dq 1.43 ms (3 products, 1.16 PFLOP/s, matrix cores busy 65 %),
-// dk and dv 2.1 ms (4 products, 1.06 PFLOP/s, 54 %); five items of up to 2,971 tokens, 12 / 4 heads of
-// 64, f16: dq 115 us (0.69 PFLOP/s), dk and dv 168 us (0.63).
+// 7,384 tokens, 16 heads of 128, bf16: dq 1.40 ms (3 products, 1.19 PFLOP/s, matrix cores busy 65 %),
+// dk and dv 2.07 ms (4 products, 1.07 PFLOP/s, 54 %); five items of up to 2,971 tokens, 12 / 4 heads of
+// 64, f16: dq 117 us (0.67 PFLOP/s), dk and dv 175 us (0.60).
 #include <algorithm>
 #include <cmath>
 

@@ -9,8 +9,8 @@
 // Rows of any length and alignment take the same path; the last chunk of a row goes element by
 // element when C is not a multiple of the chunk.
 //
-// Measured: 135,826 x 1,024 bf16: forward 101 us (5.5 TB/s), backward 160 us (5.2 TB/s); 4,099 x 675
-// float32, backward: 14.6 us, two launches; 450 x 768 f16, forward: 3.6 us on the device, 5.7 a call.
+// Measured: 135,826 x 1,024 bf16: forward 102 us (5.5 TB/s), backward 160 us (5.2 TB/s); 4,099 x 675
+// float32, backward: 15 us, two launches; 450 x 768 f16, forward: 3.4 us on the device, 6.2 a call.
 #include <algorithm>
 #include <cmath>
 
@@ -150,8 +150,8 @@ __global__ __launch_bounds__(threads_for(TPR)) void layer_norm_backward_kernel(
       db[i][j] = 0.f;
     }
   }
-  // (Waves of other rows hide a row's memory latency: prefetching the next row into registers
-  // takes one of three resident workgroups away and measured 186 us for 155.)
+  // (Waves of other rows hide a row's memory latency: prefetching the next row into registers takes
+  // a resident workgroup away; when there were three of them it measured 186 us for 155.)
   for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; row < n; row += (int64_t)gridDim.x * kRows) {
     Chunk<typename Elem<D>::T, V> cx[ITEMS], cdy[ITEMS];  // (every load before the first use)
 #pragma unroll
