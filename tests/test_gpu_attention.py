@@ -368,3 +368,31 @@ def test_keys_in_parts_of_narrow_heads(dtype, d, ql, kl):
 @pytest.mark.parametrize("dtype,heads,d", [("f32", 17, 64), ("f32", 17, 80), ("f32", 17, 128), ("f16", 46, 32), ("bf16", 46, 64)])
 def test_last_tiles_in_parts(dtype, heads, d):
     test_a_few_tiles_past_a_full_machine(dtype, [2100], [2100], heads, heads, d)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_items_never_meet_in_other_types(dtype):
+    # (float16: an item's power of two comes from its own gradients and values)
+    ql, kl = [40, 50, 60], [70, 33, 90]
+    q, k, v, g = make(ql, kl, 4, 2, 64, dtype, 20)
+    qo, ko = offsets(ql), offsets(kl)
+    clean = check(q, k, v, g, qo, ko, dtype)
+    for t, (a, b) in ((q, (40, 90)), (k, (70, 103)), (v, (70, 103)), (g, (40, 90))):
+        t[a:b:2] = float("nan")
+        t[a + 1:b:2] = float("inf")
+    qd, kd = on_device(qo), on_device(ko)
+    out, lse = sc.sparse_attention_forward(q, k, v, qd, kd)
+    grads = sc.sparse_attention_backward(g, q, k, v, out, lse, qd, kd)
+    for got, want, o in zip((out, lse, *grads), clean, (qo, qo, qo, ko, ko)):
+        keep = [*range(o[0], o[1]), *range(o[2], o[3])]
+        assert torch.equal(got[keep], want[keep])
+
+
+def test_offsets_that_are_wrong_stay_inside_in_float16():
+    # (the clamps hold for the norms of v and the peaks of dout, too)
+    q, k, v, g = make([700], [700], 2, 2, 64, "f16", 21)
+    for bad in ([0, 9000, 700], [-50, 300, 700], [600, 10, 40], [0, 700, 700]):
+        o = on_device(bad)
+        out, lse = sc.sparse_attention_forward(q, k, v, o)
+        sc.sparse_attention_backward(g, q, k, v, out, lse, o)
+    torch.cuda.synchronize()
