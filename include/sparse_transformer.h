@@ -1,5 +1,5 @@
 /*
- * sparse_transformer.h -- C ABI of the operators of a sparse transformer block: layer norm,
+ * sparse_transformer.h -- C ABI of the operators of a sparse transformer block: norms, embeddings,
  * rotary positions and attention over the items of a sparse tensor, each with its backward pass.
  * Part of libsubmconv.so; status codes, dtypes, pointer and stream conventions are those of
  * submconv.h.
@@ -14,8 +14,8 @@
  * No call synchronises.  Every result is bitwise reproducible from run to run: no sum goes
  * through atomics.
  *
- * sparse_layer_norm_backward (with weight gradients), sparse_attention_forward and
- * sparse_attention_backward may keep partial results in scratch memory of the stream, which grows
+ * The backward passes of the norms (with weight gradients) and of the embedding, and attention forward
+ * and backward may keep partial results in scratch memory of the stream, which grows
  * to the largest call so far and is given back by subm_release_cached_memory.  It cannot grow
  * under graph capture (SUBM_ERR_UNSUPPORTED): make the call once on the capturing stream before.
  * The scratch memory of captured calls is kept apart from that of other calls: a captured call stays
@@ -82,6 +82,85 @@ int sparse_layer_norm_forward(const void* x, int64_t n, int channels, int dtype,
 int sparse_layer_norm_backward(const void* dy, const void* x, int64_t n, int channels, int dtype,
                                const void* gamma, const float* mean, const float* rstd, void* dx, void* dgamma,
                                void* dbeta, hipStream_t stream);
+
+/* ------------------------------------------------------------------ root-mean-square norm */
+
+/*
+ * sparse_rms_norm_forward -- with t = x + residual,
+ *   y = t * rstd * gamma,   rstd = 1 / sqrt(mean_c(t^2) + eps),   total = t,
+ * the step between two layers of a block: the layer's output x joins the residual stream, which is
+ * normalised for the next layer.  t and its square sum are float32; y is of t before total rounds it.
+ *   x, residual  device [n, channels] in `dtype`, aligned to their element; residual may be NULL (t = x).
+ *   n            0 <= n <= 2^31 - 1; n == 0 returns SUBM_OK with no launch.
+ *   channels     1 .. 16384, any value.
+ *   gamma        device [channels] in `dtype`, may be NULL for 1.
+ *   eps          > 0 and finite.
+ *   y            device [n, channels] in `dtype`; may be x or residual (in place).
+ *   total        device [n, channels] in `dtype`, required with a residual, else it may be NULL; may be x or
+ *                residual (in place) but not y.  Any other overlap is undefined.
+ *   rstd         device float32 [n], or NULL: what the backward pass needs beside total.
+ * Errors: SUBM_ERR_INVALID_ARG, SUBM_ERR_UNSUPPORTED, SUBM_ERR_HIP.
+ */
+int sparse_rms_norm_forward(const void* x, const void* residual, int64_t n, int channels, int dtype, const void* gamma,
+                            float eps, void* y, void* total, float* rstd, hipStream_t stream);
+
+/*
+ * sparse_rms_norm_quantize_forward -- sparse_rms_norm_forward with y in 8 bits, for a linear layer in 8
+ * bits: y = q * scale with one scale for `group` consecutive channels of a row,
+ *   scale = max(max |y| / 448, 2^-126),   q = y / scale rounded to nearest even (e4m3, largest 448).
+ *   group   32, 64 or 128 channels (the last group of a row may be shorter), or 0 for the whole row.
+ *   q       device [n, channels] bytes, e4m3 without infinities; it must not overlap another argument.
+ *   scales  device float32 [n, ceil(channels / group)] ([n] for group 0).
+ * The maximum is of the values that are numbers: NaN comes out as NaN, and leaves its group's scale alone;
+ * an infinite value makes the scale infinite, the value NaN and the rest of its group 0.
+ * The other arguments and errors are those of sparse_rms_norm_forward.  y has no gradient of its own: the
+ * backward pass takes that of the 16- or 32-bit y (q / scale taken as y).
+ */
+int sparse_rms_norm_quantize_forward(const void* x, const void* residual, int64_t n, int channels, int dtype,
+                                     const void* gamma, float eps, int group, void* q, float* scales, void* total,
+                                     float* rstd, hipStream_t stream);
+
+/*
+ * sparse_rms_norm_backward -- gradients of sparse_rms_norm_forward.  With h = total * rstd and a = dy gamma:
+ *   dx = rstd (a - h mean_c(a h)) + dtotal,   dgamma = sum_r dy h;
+ * dx is the gradient of x and of residual alike.
+ *   dy, total  device [n, channels] in `dtype`; total is the forward pass's (x without a residual).
+ *   dtotal     the gradient of total, [n, channels], or NULL for none.
+ *   gamma, rstd  as in the forward pass.
+ *   dx         device [n, channels] in `dtype`; may be dy or dtotal (in place).
+ *   dgamma     device [channels] in `dtype`, overwritten, or NULL (no weight gradient).  n == 0 writes zeros.
+ * The row sums of dgamma are float32, per workgroup and then over workgroups in a fixed order, rounded
+ * once.  Errors: as the forward pass, and SUBM_ERR_OUT_OF_MEMORY.
+ */
+int sparse_rms_norm_backward(const void* dy, const void* total, const void* dtotal, int64_t n, int channels, int dtype,
+                             const void* gamma, const float* rstd, void* dx, void* dgamma, hipStream_t stream);
+
+/* -------------------------------------------------------------------------------- embedding */
+
+/*
+ * sparse_embedding_forward -- out_i = scale * table[tokens_i], rounded once: rows of a learned table for
+ * tokens that name them (codebook entries of voxels, words of a prompt).
+ *   table        device [rows, channels] in `dtype`, aligned to its element.
+ *   rows         1 .. 2^21.
+ *   channels     1 .. 16384, any value.
+ *   tokens       device [n], integers of token_bytes (4 or 8) bytes.  A token outside 0 .. rows - 1 (padding,
+ *                -1) gives a row of zeros.
+ *   n            0 <= n <= 2^31 - 1; n == 0 returns SUBM_OK with no launch.
+ *   scale        finite.
+ *   out          device [n, channels] in `dtype`; it must not overlap the table.
+ * Errors: SUBM_ERR_INVALID_ARG, SUBM_ERR_UNSUPPORTED, SUBM_ERR_HIP.
+ */
+int sparse_embedding_forward(const void* table, int rows, int channels, int dtype, const void* tokens, int token_bytes,
+                             int64_t n, float scale, void* out, hipStream_t stream);
+
+/*
+ * sparse_embedding_backward -- dtable_t = scale * sum of dout_i over the tokens_i that are t, every row of
+ * dtable [rows, channels] overwritten (zeros where no token names it).  The tokens are sorted by row and
+ * position, so each float32 sum has one order; it is rounded once.  dtable must not overlap dout.  Other
+ * arguments as in the forward pass.  Errors: as the forward pass, and SUBM_ERR_OUT_OF_MEMORY.
+ */
+int sparse_embedding_backward(const void* dout, int rows, int channels, int dtype, const void* tokens, int token_bytes,
+                              int64_t n, float scale, void* dtable, hipStream_t stream);
 
 /* ------------------------------------------------------------------------- rotary positions */
 

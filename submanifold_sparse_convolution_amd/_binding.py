@@ -62,6 +62,11 @@ C_FUNCTIONS = (
     "subm_conv3d_forward_group_norm_act",
     "sparse_layer_norm_forward",
     "sparse_layer_norm_backward",
+    "sparse_rms_norm_forward",
+    "sparse_rms_norm_quantize_forward",
+    "sparse_rms_norm_backward",
+    "sparse_embedding_forward",
+    "sparse_embedding_backward",
     "sparse_rope_frequencies",
     "sparse_rope_forward",
     "sparse_rope_backward",
@@ -140,6 +145,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         cf, cd, hp = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_HeadsArg)
         lib.sparse_layer_norm_forward.argtypes = [vp, i64, ci, ci, vp, vp, cf, vp, vp, vp, vp]
         lib.sparse_layer_norm_backward.argtypes = [vp, vp, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp]
+        lib.sparse_rms_norm_forward.argtypes = [vp, vp, i64, ci, ci, vp, cf, vp, vp, vp, vp]
+        lib.sparse_rms_norm_quantize_forward.argtypes = [vp, vp, i64, ci, ci, vp, cf, ci, vp, vp, vp, vp, vp]
+        lib.sparse_rms_norm_backward.argtypes = [vp, vp, vp, i64, ci, ci, vp, vp, vp, vp, vp]
+        lib.sparse_embedding_forward.argtypes = [vp, ci, ci, ci, vp, ci, i64, cf, vp, vp]
+        lib.sparse_embedding_backward.argtypes = [vp, ci, ci, ci, vp, ci, i64, cf, vp, vp]
         lib.sparse_rope_frequencies.argtypes = [ci, cd, ci, cd, cd, ctypes.POINTER(cf), ctypes.POINTER(cf)]
         for rope in (lib.sparse_rope_forward, lib.sparse_rope_backward):
             rope.argtypes = [hp, i64, ci, ci, ci, vp, i64, ci, vp, ci, ci, cf, hp, vp]
@@ -821,6 +831,118 @@ def sparse_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
         dg_ptr, db_ptr = dgamma.data_ptr(), dbeta.data_ptr()
     _run("sparse_layer_norm_backward", x.get_device(), stream, dy_ptr, x.data_ptr(), n, c, code, g, m, r, dx, dg_ptr, db_ptr)
     return out, dgamma, dbeta
+
+
+def _rms_norm_args(x, gamma, residual, total, stats, stream):
+    """(rows, channels, dtype code, pointers of gamma and residual, total and its pointer, rstd and its)."""
+    n, c, code = _matrix(x, "x")
+    g = None if gamma is None else _vector(gamma, (c,), x.dtype, x.device, "gamma")
+    if residual is None:
+        r = None
+        t = None if total is None else _vector(total, (n, c), x.dtype, x.device, "total")
+    else:
+        r = _vector(residual, (n, c), x.dtype, x.device, "residual")
+        if total is None:
+            total = _empty_like(x, stream)
+            t = total.data_ptr()
+        else:
+            t = _vector(total, (n, c), x.dtype, x.device, "total")
+    rstd = _empty((n,), torch.float32, x.device, stream) if stats else None
+    return n, c, code, g, r, total, t, rstd, None if rstd is None else rstd.data_ptr()
+
+
+def sparse_rms_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                            eps: float = 1e-6, stats: bool = False, out: torch.Tensor | None = None,
+                            total: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of the rows of x + residual [N, C]: (y, total, rstd).  total is x + residual (None
+    without a residual), rstd float32 [N] only with stats=True; the backward pass needs both.  out and total
+    may be x or residual (in place)."""
+    n, c, code, g, r, total, t, rstd, rstd_ptr = _rms_norm_args(x, gamma, residual, total, stats, stream)
+    if out is None:
+        out = _empty_like(x, stream)
+        y = out.data_ptr()
+    else:
+        y = _vector(out, (n, c), x.dtype, x.device, "out")
+    _run("sparse_rms_norm_forward", x.get_device(), stream, x.data_ptr(), r, n, c, code, g, eps, y, t, rstd_ptr)
+    return out, total, rstd
+
+
+def sparse_rms_norm_quantize_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                                     eps: float = 1e-6, group: int = 128, stats: bool = False,
+                                     total: torch.Tensor | None = None, stream=None):
+    """sparse_rms_norm_forward with y in 8 bits: (q float8_e4m3fn [N, C], scales float32 [N, groups], total, rstd),
+    y = q * scale with a scale each `group` channels (32, 64, 128; 0: a row)."""
+    n, c, code, g, r, total, t, rstd, rstd_ptr = _rms_norm_args(x, gamma, residual, total, stats, stream)
+    q = _empty((n, c), torch.float8_e4m3fn, x.device, stream)
+    scales = _empty((n, -(-c // group) if group > 0 else 1), torch.float32, x.device, stream)
+    _run("sparse_rms_norm_quantize_forward", x.get_device(), stream, x.data_ptr(), r, n, c, code, g, eps, group, q.data_ptr(),
+         scales.data_ptr(), t, rstd_ptr)
+    return q, scales, total, rstd
+
+
+def sparse_rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor | None = None,
+                             dtotal: torch.Tensor | None = None, weight_grads: bool = True,
+                             out: torch.Tensor | None = None, stream=None):
+    """Gradients of sparse_rms_norm_forward: (dx, dgamma), dx that of x and of residual alike, dgamma None with
+    weight_grads=False.  total, rstd: the forward pass's (total is x without a residual); dtotal: the gradient
+    of total.  out may be dy or dtotal (in place)."""
+    n, c, code = _matrix(total, "total")
+    if dy is None or rstd is None:
+        raise ValueError("dy and rstd are required")
+    dy_ptr = _vector(dy, (n, c), total.dtype, total.device, "dy")
+    r = _vector(rstd, (n,), torch.float32, total.device, "rstd")
+    g = None if gamma is None else _vector(gamma, (c,), total.dtype, total.device, "gamma")
+    dt = None if dtotal is None else _vector(dtotal, (n, c), total.dtype, total.device, "dtotal")
+    if out is None:
+        out = _empty_like(total, stream)
+        dx = out.data_ptr()
+    else:
+        dx = _vector(out, (n, c), total.dtype, total.device, "out")
+    dgamma = _empty((c,), total.dtype, total.device, stream) if weight_grads else None
+    _run("sparse_rms_norm_backward", total.get_device(), stream, dy_ptr, total.data_ptr(), dt, n, c, code, g, r, dx,
+         None if dgamma is None else dgamma.data_ptr())
+    return out, dgamma
+
+
+def _tokens_arg(tokens, device):
+    """(data_ptr, bytes of a token, count)."""
+    if not isinstance(tokens, torch.Tensor) or not tokens.is_cuda or not tokens.is_contiguous():
+        _device_tensor(tokens, "tokens")
+    if tokens.dim() != 1 or tokens.dtype not in (torch.int32, torch.int64) or tokens.get_device() != device:
+        raise ValueError("tokens must be int32 or int64 [N] on the same device")
+    return tokens.data_ptr(), tokens.element_size(), tokens.shape[0]
+
+
+def sparse_embedding_forward(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
+                             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """scale * table[tokens]: table [rows, C], tokens int32 / int64 [N]; zeros for a token outside the table."""
+    rows, c, code = _matrix(table, "table")
+    t, size, n = _tokens_arg(tokens, table.get_device())
+    if out is None:
+        out = _empty((n, c), table.dtype, table.device, stream)
+        y = out.data_ptr()
+    else:
+        y = _vector(out, (n, c), table.dtype, table.device, "out")
+    _run("sparse_embedding_forward", table.get_device(), stream, table.data_ptr(), rows, c, code, t, size, n, scale, y)
+    return out
+
+
+def sparse_embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, rows: int, scale: float = 1.0,
+                              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of sparse_embedding_forward's table: [rows, C], every row written."""
+    n, c, code = _matrix(dout, "dout")
+    t, size, count = _tokens_arg(tokens, dout.get_device())
+    if count != n:
+        raise ValueError("dout and tokens must have the same rows")
+    if not 0 < rows < 2 ** 31:
+        raise ValueError("rows must be 1 .. 2^31 - 1")
+    if out is None:
+        out = _empty((rows, c), dout.dtype, dout.device, stream)
+        d = out.data_ptr()
+    else:
+        d = _vector(out, (rows, c), dout.dtype, dout.device, "out")
+    _run("sparse_embedding_backward", dout.get_device(), stream, dout.data_ptr(), rows, c, code, t, size, n, scale, d)
+    return out
 
 
 def _heads_arg(t, what, like=None):

@@ -39,6 +39,51 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     return _LayerNorm.apply(x, gamma, beta, eps)
 
 
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        y, total, rstd = _b.sparse_rms_norm_forward(x, gamma, residual, eps, stats=True)
+        ctx.save_for_backward(x if residual is None else total, gamma, rstd)
+        ctx.set_materialize_grads(False)
+        return y if residual is None else (y, total)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dtotal=None):
+        total, gamma, rstd = ctx.saved_tensors
+        want_x, want_residual, want_gamma, _ = ctx.needs_input_grad
+        if dy is None:  # only the sum was used
+            dx, dgamma = dtotal, None
+        else:
+            dx, dgamma = _b.sparse_rms_norm_backward(_plain(dy), total, rstd, gamma, None if dtotal is None else _plain(dtotal),
+                                                     weight_grads=want_gamma)
+        return dx if want_x else None, dx if want_residual else None, dgamma, None
+
+
+def rms_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None, eps: float = 1e-6):
+    """Root-mean-square norm of the rows of x [N, C]; with a residual (norm of x + residual, x + residual).  See
+    sparse_rms_norm_forward."""
+    return _RmsNorm.apply(x, residual, gamma, eps)
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, tokens, scale):
+        ctx.save_for_backward(tokens)
+        ctx.rows, ctx.scale = table.shape[0], scale
+        return _b.sparse_embedding_forward(table, tokens, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        return _b.sparse_embedding_backward(_plain(dout), ctx.saved_tensors[0], ctx.rows, ctx.scale), None, None
+
+
+def embedding(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """scale * table[tokens], tokens [N]; see sparse_embedding_forward."""
+    return _Embedding.apply(table, tokens, scale)
+
+
 class _Rope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, positions, freq, layout, magnitude):

@@ -17,58 +17,17 @@
 #include "chunk.h"
 #include "device_common.h"
 #include "internal.h"
+#include "row_lanes.h"
 #include "sparse_transformer.h"
 
 namespace submconv {
 namespace {
-
-// TPR lanes (a part of a wave, a wave, or a workgroup of TPR threads) hold one row, ITEMS chunks of V
-// values each.
-
-template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
-  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
-}
-
-// Sum over aligned groups of LANES lanes, the same in every lane, in VALU instructions alone (an LDS
-// permutation a step would cost a row some 12 LDS round trips in the backward pass).
-template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
-  static_assert(LANES == 8 || LANES == 16 || LANES == 32 || LANES == 64, "lanes of a row");
-  v = dpp_add<0xB1>(v);   // quads: lanes 1 0 3 2
-  v = dpp_add<0x4E>(v);   // quads: lanes 2 3 0 1
-  v = dpp_add<0x141>(v);  // half rows mirrored
-  if constexpr (LANES == 8) return v;
-  v = dpp_add<0x140>(v);  // rows of 16 mirrored
-  if constexpr (LANES == 16) return v;
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  if constexpr (LANES == 32) return v;
-  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
-}
-
-// Sum over the TPR lanes of a row, the same in all of them.  For TPR > 64 every thread of the
-// workgroup must call it (it synchronises), with a slot array of its own per call site.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* slots) {
-  v = lanes_sum<TPR < 64 ? TPR : 64>(v);
-  if constexpr (TPR > 64) {
-    __syncthreads();  // the slots' readers of the previous row are done
-    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int w = 0; w < TPR / 64; ++w) v += slots[w];
-  }
-  return v;
-}
 
 // Workgroups of the backward pass, each a partial weight gradient: the four a compute unit that are
 // resident (1,024 16-bit channels, 135,826 rows: 160 us; two 238, three 180, eight 170), two with
 // three chunks a lane (60,000 x 700 float32: 95 us, four 103).
 constexpr int kPartsLimit = 256 * 4;
 int parts_limit(int chunks) { return chunks > 128 && chunks <= 192 ? 256 * 2 : kPartsLimit; }
-
-constexpr int threads_for(int tpr) { return tpr > 256 ? tpr : 256; }
 
 // (x may be y: neither is declared free of aliases.)
 template <DT D, int TPR, int ITEMS, bool TAIL>
@@ -301,8 +260,6 @@ void launch(const Backward& b, int64_t n, int channels, int blocks, hipStream_t 
       b.rstd, static_cast<T*>(b.dx), b.part);
 }
 
-// Lanes of a row: short rows share a wave (179,096 x 48 bf16, forward: 8.1 us, 45 with a wave a row).
-int short_lanes(int chunks) { return chunks <= 8 ? 8 : chunks <= 16 ? 16 : chunks <= 32 ? 32 : 64; }
 // A lane holds up to 4 chunks in the forward pass and 2 in the backward pass,
 // whose gradients and weights stay in registers too, or 3 where a wave then spares a row its
 // barriers (60,000 x 700 float32: 95 us, four waves a row 107); up to 16,384 channels, beyond which
