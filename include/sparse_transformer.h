@@ -272,6 +272,43 @@ int sparse_attention_backward(const subm_heads_t* dout, const subm_heads_t* q, c
                               int kv_heads, int head_dim, int dtype, float scale, const subm_heads_t* dq,
                               const subm_heads_t* dk, const subm_heads_t* dv, hipStream_t stream);
 
+/* ------------------------------------------------------------ attention in a sliding window */
+
+/*
+ * sparse_window_attention_forward -- sparse_attention_forward where a query sees a part of its item's keys:
+ * those next to its own position, and the first `sinks`.  Query i of an item with nq queries and nk keys stands
+ * at key position p = i + nk - nq (the queries are the last tokens of a sequence whose keys are all its
+ * tokens: a whole prompt, a chunk of one after a cache, or one new token) and sees key j if
+ *   j <= p + right  and  (j >= p - left  or  j < sinks).
+ *   left, right  >= 0; 2^31 or more leaves that end open (left open and right 0 is causal attention).
+ *   sinks        0 .. 128 (else SUBM_ERR_UNSUPPORTED).  They are not seen before p + right reaches them.
+ *   k_lengths    device int64 [items], or NULL: how many of an item's key rows are there (a cache with room
+ *                behind its tokens); values outside 0 .. its rows are taken as the nearest.  Rows past it are not read.
+ * A query that sees no key (p + right < 0, or an item without keys) gets out = 0 and lse = -infinity.  A key or
+ * value that a query does not see, NaN and infinities included, does not change the query's result (a tile in
+ * which such a value meets other rows is computed again row by row, which is slow).  Only the tiles of keys
+ * that some row of a block sees are read.  All other arguments, limits and errors are those of
+ * sparse_attention_forward, and SUBM_ERR_INVALID_ARG for a negative left, right or sinks.
+ */
+int sparse_window_attention_forward(const subm_heads_t* q, const subm_heads_t* k, const subm_heads_t* v, int64_t nq,
+                                    int64_t nk, const int64_t* q_offsets, const int64_t* k_offsets,
+                                    const int64_t* k_lengths, int items, int heads, int kv_heads, int head_dim,
+                                    int dtype, float scale, int64_t left, int64_t right, int sinks,
+                                    const subm_heads_t* out, float* lse, hipStream_t stream);
+
+/*
+ * sparse_window_attention_backward -- gradients of sparse_window_attention_forward without k_lengths: those of
+ * sparse_attention_backward, each sum over the keys that a query sees or the queries that see a key.  A key
+ * that no query sees gets dk = dv = 0.  The sinks' sums go through float32 partial results, one a chunk
+ * of query rows.
+ */
+int sparse_window_attention_backward(const subm_heads_t* dout, const subm_heads_t* q, const subm_heads_t* k,
+                                     const subm_heads_t* v, const subm_heads_t* out, const float* lse, int64_t nq,
+                                     int64_t nk, const int64_t* q_offsets, const int64_t* k_offsets, int items,
+                                     int heads, int kv_heads, int head_dim, int dtype, float scale, int64_t left,
+                                     int64_t right, int sinks, const subm_heads_t* dq, const subm_heads_t* dk,
+                                     const subm_heads_t* dv, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

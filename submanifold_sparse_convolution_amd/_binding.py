@@ -72,6 +72,8 @@ C_FUNCTIONS = (
     "sparse_rope_backward",
     "sparse_attention_forward",
     "sparse_attention_backward",
+    "sparse_window_attention_forward",
+    "sparse_window_attention_backward",
     "subm_status_string",
     "subm_last_error",
 )
@@ -156,6 +158,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.sparse_attention_forward.argtypes = [hp, hp, hp, i64, i64, vp, vp, ci, ci, ci, ci, ci, cf, hp, vp, vp]
         lib.sparse_attention_backward.argtypes = [hp, hp, hp, hp, hp, vp, i64, i64, vp, vp, ci, ci, ci, ci, ci, cf, hp,
                                                   hp, hp, vp]
+        lib.sparse_window_attention_forward.argtypes = [hp, hp, hp, i64, i64, vp, vp, vp, ci, ci, ci, ci, ci, cf, i64, i64,
+                                                        ci, hp, vp, vp]
+        lib.sparse_window_attention_backward.argtypes = [hp, hp, hp, hp, hp, vp, i64, i64, vp, vp, ci, ci, ci, ci, ci, cf,
+                                                         i64, i64, ci, hp, hp, hp, vp]
         for name in C_FUNCTIONS[:-2]:
             getattr(lib, name).restype = ci
         lib.subm_status_string.argtypes = [ci]
@@ -1036,15 +1042,8 @@ def _attention_args(q, k, v, q_offsets, k_offsets, scale):
     return qa, ka, va, k_offsets, scale
 
 
-def sparse_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
-                             k_offsets: torch.Tensor | None = None, scale: float | None = None,
-                             out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
-    """Attention within items: (out [Nq, heads, head_dim], lse float32 [Nq, heads]).
-
-    q [Nq, heads, head_dim], k and v [Nk, kv_heads, head_dim] with any row and head strides;
-    q_offsets, k_offsets int64 [items + 1] on the device (k_offsets None: self attention); scale
-    defaults to head_dim ** -0.5.  A query whose item has no keys gets out 0, lse -infinity."""
-    qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
+def _attention_out(q, out, lse, stream):
+    """(out, its argument, lse, its data_ptr), new ones where not given."""
     nq, heads, dim = q.shape
     if out is None:
         out = _empty((nq, heads, dim), q.dtype, q.device, stream)
@@ -1058,9 +1057,38 @@ def sparse_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         lse_ptr = lse.data_ptr()
     else:
         lse_ptr = _vector(lse, (nq, heads), torch.float32, q.device, "lse")
+    return out, oa, lse, lse_ptr
+
+
+def sparse_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                             k_offsets: torch.Tensor | None = None, scale: float | None = None,
+                             out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Attention within items: (out [Nq, heads, head_dim], lse float32 [Nq, heads]).
+
+    q [Nq, heads, head_dim], k and v [Nk, kv_heads, head_dim] with any row and head strides;
+    q_offsets, k_offsets int64 [items + 1] on the device (k_offsets None: self attention); scale
+    defaults to head_dim ** -0.5.  A query whose item has no keys gets out 0, lse -infinity."""
+    qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
+    nq, heads, dim = q.shape
+    out, oa, lse, lse_ptr = _attention_out(q, out, lse, stream)
     _run("sparse_attention_forward", q.get_device(), stream, qa, ka, va, nq, k.shape[0], q_offsets.data_ptr(),
          k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype], scale, oa, lse_ptr)
     return out, lse
+
+
+def _attention_grads(dout, q, k, out, lse, dq, dk, dv, stream):
+    """(arguments of dout and out, lse's data_ptr, dq, dk, dv and their arguments), new gradients where not given."""
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(k.shape, q.dtype, q.device, stream) if dv is None else dv
+    ga, oa = _heads_arg(dout, "dout", q), _heads_arg(out, "out", q)
+    dqa, dka, dva = _heads_arg(dq, "dq", q), _heads_arg(dk, "dk", q), _heads_arg(dv, "dv", q)
+    if not (dout.shape == out.shape == dq.shape == q.shape) or not (dk.shape == dv.shape == k.shape):
+        raise ValueError("dout, out and dq must have q's shape, dk and dv k's")
+    if lse is None:
+        raise ValueError("lse is required")
+    lse_ptr = _vector(lse, tuple(q.shape[:2]), torch.float32, q.device, "lse")
+    return ga, oa, lse_ptr, dq, dk, dv, dqa, dka, dva
 
 
 def sparse_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1072,17 +1100,59 @@ def sparse_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     dk and dv may be given as views of a packed buffer."""
     qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
     nq, heads, dim = q.shape
-    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _empty(k.shape, q.dtype, q.device, stream) if dk is None else dk
-    dv = _empty(k.shape, q.dtype, q.device, stream) if dv is None else dv
-    ga, oa = _heads_arg(dout, "dout", q), _heads_arg(out, "out", q)
-    dqa, dka, dva = _heads_arg(dq, "dq", q), _heads_arg(dk, "dk", q), _heads_arg(dv, "dv", q)
-    if not (dout.shape == out.shape == dq.shape == q.shape) or not (dk.shape == dv.shape == k.shape):
-        raise ValueError("dout, out and dq must have q's shape, dk and dv k's")
-    if lse is None:
-        raise ValueError("lse is required")
-    lse_ptr = _vector(lse, (nq, heads), torch.float32, q.device, "lse")
+    ga, oa, lse_ptr, dq, dk, dv, *da = _attention_grads(dout, q, k, out, lse, dq, dk, dv, stream)
     _run("sparse_attention_backward", q.get_device(), stream, ga, qa, ka, va, oa, lse_ptr, nq, k.shape[0],
          q_offsets.data_ptr(), k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype],
-         scale, dqa, dka, dva)
+         scale, *da)
+    return dq, dk, dv
+
+
+def _window_args(left, right, sinks):
+    """left, right (None: open) and sinks as the library takes them."""
+    ends = []
+    for end, what in ((left, "left"), (right, "right")):
+        if end is not None and end < 0:
+            raise ValueError(f"{what} must not be negative (None leaves it open)")
+        ends.append(2 ** 31 if end is None else min(int(end), 2 ** 31))
+    if not 0 <= sinks < 2 ** 31:
+        raise ValueError("sinks must not be negative")
+    return (*ends, int(sinks))
+
+
+def sparse_window_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                                    k_offsets: torch.Tensor | None = None, left: int | None = None,
+                                    right: int | None = None, sinks: int = 0, k_lengths: torch.Tensor | None = None,
+                                    scale: float | None = None, out: torch.Tensor | None = None,
+                                    lse: torch.Tensor | None = None, stream=None):
+    """sparse_attention_forward within a sliding window: (out, lse).  Query i of an item with nq queries and nk
+    keys stands at p = i + nk - nq and sees key j if j <= p + right and (j >= p - left or j < sinks); None
+    leaves that end open (right=0: causal).  k_lengths int64 [items]: how many of an item's key rows are
+    there (a cache with room behind its tokens)."""
+    qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
+    left, right, sinks = _window_args(left, right, sinks)
+    nq, heads, dim = q.shape
+    items = q_offsets.shape[0] - 1
+    lengths = None if k_lengths is None else _vector(k_lengths, (items,), torch.int64, q.device, "k_lengths")
+    out, oa, lse, lse_ptr = _attention_out(q, out, lse, stream)
+    _run("sparse_window_attention_forward", q.get_device(), stream, qa, ka, va, nq, k.shape[0], q_offsets.data_ptr(),
+         k_offsets.data_ptr(), lengths, items, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype], scale, left, right, sinks, oa,
+         lse_ptr)
+    return out, lse
+
+
+def sparse_window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                     out: torch.Tensor, lse: torch.Tensor, q_offsets: torch.Tensor,
+                                     k_offsets: torch.Tensor | None = None, left: int | None = None,
+                                     right: int | None = None, sinks: int = 0, scale: float | None = None,
+                                     dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                                     dv: torch.Tensor | None = None, stream=None):
+    """(dq, dk, dv) of sparse_window_attention_forward (without k_lengths) from dout and the forward pass's out
+    and lse.  dq, dk and dv may be given as views of a packed buffer."""
+    qa, ka, va, k_offsets, scale = _attention_args(q, k, v, q_offsets, k_offsets, scale)
+    left, right, sinks = _window_args(left, right, sinks)
+    nq, heads, dim = q.shape
+    ga, oa, lse_ptr, dq, dk, dv, *da = _attention_grads(dout, q, k, out, lse, dq, dk, dv, stream)
+    _run("sparse_window_attention_backward", q.get_device(), stream, ga, qa, ka, va, oa, lse_ptr, nq, k.shape[0],
+         q_offsets.data_ptr(), k_offsets.data_ptr(), q_offsets.shape[0] - 1, heads, k.shape[1], dim, _DTYPE_CODES[q.dtype],
+         scale, left, right, sinks, *da)
     return dq, dk, dv

@@ -124,3 +124,27 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torc
               k_offsets: torch.Tensor | None = None, scale: float | None = None) -> torch.Tensor:
     """Attention within items; see sparse_attention_forward."""
     return _Attention.apply(q, k, v, q_offsets, k_offsets, scale)
+
+
+class _WindowAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, q_offsets, k_offsets, window, scale):
+        out, lse = _b.sparse_window_attention_forward(q, k, v, q_offsets, k_offsets, *window, scale=scale)
+        ctx.save_for_backward(q, k, v, out, lse, q_offsets, k_offsets)
+        ctx.window, ctx.scale = window, scale
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, q_offsets, k_offsets = ctx.saved_tensors
+        dq, dk, dv = _b.sparse_window_attention_backward(_plain(dout), q, k, v, out, lse, q_offsets, k_offsets, *ctx.window,
+                                                         scale=ctx.scale)
+        return dq, dk, dv, None, None, None, None
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                     k_offsets: torch.Tensor | None = None, left: int | None = None, right: int | None = None,
+                     sinks: int = 0, scale: float | None = None) -> torch.Tensor:
+    """Attention within a sliding window of each item; see sparse_window_attention_forward."""
+    return _WindowAttention.apply(q, k, v, q_offsets, k_offsets, (left, right, sinks), scale)

@@ -22,7 +22,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsubmconv.so")
 SOURCES = ["submconv_api.hip", "indice_map.hip", "conv.hip", "conv_pool.hip", "conv_offsets.hip", "structure.hip",
            "norm.hip", "sort_scan.hip", "row_order.hip", "peak.hip", "layer_norm.hip", "rms_norm.hip", "embedding.hip",
-           "rope.hip", "attention.hip", "attention_backward.hip"]
+           "rope.hip", "attention.hip", "attention_backward.hip", "window_attention.hip", "window_attention_backward.hip"]
 
 ARCH = "gfx950"
 COMMON = [

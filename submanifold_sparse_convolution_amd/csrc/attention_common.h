@@ -447,5 +447,11 @@ struct AttentionShape {
 };
 Status check_attention(const AttentionShape& s);
 Status check_heads(const subm_heads_t* t, int64_t rows, int heads, const AttentionShape& s, bool written, const char* what);
+Status check_forward(const subm_heads_t* q, const subm_heads_t* k, const subm_heads_t* v, const subm_heads_t* out,
+                     const float* lse, const AttentionShape& s);
+// (attention_backward.hip)
+Status check_backward(const subm_heads_t* dout, const subm_heads_t* q, const subm_heads_t* k, const subm_heads_t* v,
+                      const subm_heads_t* out, const float* lse, const subm_heads_t* dq, const subm_heads_t* dk,
+                      const subm_heads_t* dv, const AttentionShape& s);
 
 }  // namespace submconv

@@ -1,0 +1,199 @@
+// What a row of a sliding window sees, and the tiles of keys or rows that this leaves.
+//
+// Query i of an item with nq queries and nk keys stands at key position p = i + nk - nq and sees key j if
+// j <= p + right and (j >= p - left or j < sinks).  Both ends of the range rise with i, so those of a block
+// of rows are its first row's first and its last row's last key.
+#pragma once
+
+#include "attention_common.h"
+#include "row_lanes.h"
+
+namespace submconv {
+
+struct Window {
+  int64_t left, right;  // at most kOpen, which is more than there are keys
+  int sinks;
+  const int64_t* k_lengths;  // keys of each item that are there, or null: all its rows
+
+  // How many keys an item with `rows` rows of keys has.
+  __device__ __forceinline__ int keys(int item, int rows) const {
+    if (k_lengths == nullptr) return rows;
+    const int64_t n = k_lengths[item];
+    return n < 0 ? 0 : n < rows ? (int)n : rows;
+  }
+  // Of position p: the first key (0 if the sinks reach it) and the last, -1 if there is none.
+  __device__ __forceinline__ void range(int64_t p, int nk, int* lo, int* hi) const {
+    const int64_t first = p - left, last = p + right;
+    *lo = first <= sinks ? 0 : (int)(first < nk ? first : nk);
+    *hi = last < 0 ? -1 : last < nk ? (int)last : nk - 1;
+  }
+  __device__ __forceinline__ bool sees(int64_t p, int j) const {
+    return j <= p + right && (j >= p - left || j < sinks);
+  }
+  // The packed rows (`group` a token) that see key j of an item: *from .. *to - 1.
+  __device__ __forceinline__ void rows(int j, bool sink, int nq, int shift, int group, int* from, int* to) const {
+    const int64_t first = (int64_t)j - right - shift, past = (int64_t)j + left - shift + 1;
+    *from = (int)(first < 0 ? 0 : first < nq ? first : nq) * group;
+    *to = (sink ? nq : (int)(past < 0 ? 0 : past < nq ? past : nq)) * group;
+  }
+  // Host: keys of an item of `keys` that a block of `rows` tokens walks, at most.
+  int64_t walked(int64_t keys, int64_t rows) const {
+    const int64_t most = left + right + sinks + rows;
+    return most < keys ? most : keys;
+  }
+};
+
+constexpr int64_t kOpen = int64_t(1) << 31;  // a window's end that no position reaches
+constexpr int kMaxSinks = 128;
+
+// Host (window_attention.hip).
+Status check_window(int64_t left, int64_t right, int sinks, const int64_t* k_lengths, Window* w);
+
+// The tiles of KEYS keys that a block of rows walks: the sinks, if the window does not reach them, and the
+// window from its first key on.
+template <int KEYS> struct KeyTiles {
+  int sink_tiles, sink_end;  // keys 0 .. sink_end - 1
+  int low, high;             // keys low .. high - 1
+  int first, tiles;          // tiles first .. first + tiles - 1 of them all are this workgroup's
+
+  __device__ __forceinline__ void place(const Window& w, int nk, int shift, int first_token, int last_token) {
+    int unused, hi;
+    w.range((int64_t)first_token + shift, nk, &low, &unused);
+    w.range((int64_t)last_token + shift, nk, &unused, &hi);
+    low = first_lane(low);  // (its token comes from a division)
+    high = first_lane(hi) + 1;
+    sink_end = low == 0 ? 0 : min(w.sinks, high);
+    sink_tiles = (sink_end + KEYS - 1) / KEYS;
+    first = 0;
+    tiles = sink_tiles + max(0, (high - low + KEYS - 1) / KEYS);
+  }
+  __device__ __forceinline__ void cut(int from, int count) {
+    first = from;
+    tiles = count;
+  }
+  // Of tile t: its first key, and where its keys end (0 past the last tile).
+  __device__ __forceinline__ int key(int t) const {
+    t += first;
+    return t < sink_tiles ? t * KEYS : low + (t - sink_tiles) * KEYS;
+  }
+  __device__ __forceinline__ int end(int t) const { return t >= tiles ? 0 : t + first < sink_tiles ? sink_end : high; }
+};
+
+// What a lane's own query row sees, and what all rows of its wave do.
+struct RowView {
+  int lo, hi, sinks;
+  uint32_t span;         // the row sees lo .. lo + span (and the sinks)
+  int wave_lo, wave_hi;  // every row of the wave sees these and what lies between (and the sinks up to wave_hi)
+
+  __device__ __forceinline__ void place(const Window& w, int nk, int shift, int token, int first_token, int last_token) {
+    int unused;
+    w.range((int64_t)token + shift, nk, &lo, &hi);
+    w.range((int64_t)first_token + shift, nk, &unused, &wave_hi);
+    w.range((int64_t)last_token + shift, nk, &wave_lo, &unused);
+    wave_lo = first_lane(wave_lo);
+    wave_hi = first_lane(wave_hi);
+    sinks = w.sinks;
+    if (hi < lo) lo = INT32_MAX;  // (sees no more than sinks)
+    span = hi < lo ? 0u : (uint32_t)(hi - lo);
+  }
+  // Keys key .. key + n - 1, of which those from `end` on are not there.
+  __device__ __forceinline__ bool sees_all(int key, int n, int end) const {
+    return key + n <= end && key + n - 1 <= wave_hi && (key >= wave_lo || key + n <= sinks);
+  }
+  // Calls hide(kb, i) for element i of each 32 keys' scores that the row does not see.
+  template <int KB, typename Hide>
+  __device__ __forceinline__ void mask(int key, int end, int lane, const Hide& hide) const {
+    const int first = key + 4 * (lane >> 5);
+    if (key < sinks) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = first + kb * 32 + 8 * (i >> 2) + (i & 3);
+          if (!(j < end && j <= hi && (j >= lo || j < sinks))) hide(kb, i);
+        }
+    } else {
+      const uint32_t from = (uint32_t)first - (uint32_t)lo;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (from + (uint32_t)(kb * 32 + 8 * (i >> 2) + (i & 3)) > span) hide(kb, i);
+    }
+  }
+};
+
+// Which packed rows a lane's own key is seen by, and which all keys of its wave are.
+struct KeyView {
+  int from;
+  uint32_t span;  // the key is seen by rows from .. from + span - 1
+  int wave_from, wave_to;
+
+  __device__ __forceinline__ void place(const Window& w, bool sink, int nq, int shift, int group, int key, int first_key,
+                                        int last_key) {
+    int to, unused;
+    w.rows(key, sink, nq, shift, group, &from, &to);
+    w.rows(first_key, sink, nq, shift, group, &unused, &wave_to);
+    w.rows(last_key, sink, nq, shift, group, &wave_from, &unused);
+    wave_from = first_lane(wave_from);
+    wave_to = first_lane(wave_to);
+    span = to > from ? (uint32_t)(to - from) : 0u;
+  }
+  __device__ __forceinline__ bool sees_all(int row, int n) const { return row >= wave_from && row + n <= wave_to; }
+  // Calls hide(i) for element i of 32 rows' values that the key is not seen by.
+  template <typename Hide> __device__ __forceinline__ void mask(int row, int lane, const Hide& hide) const {
+    const uint32_t at = (uint32_t)(row + 4 * (lane >> 5)) - (uint32_t)from;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (at + (uint32_t)(8 * (i >> 2) + (i & 3)) >= span) hide(i);
+  }
+};
+
+// ------------------------------------------------------------------ rows that are not finite
+//
+// A matrix product adds 0 times a hidden key's value, which is NaN where the value is not finite.  A row
+// that ends so is computed again over what it sees alone, a wave a row, two channels a lane.
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// The own rows (bits 0 .. 31) with a value that is not finite, of those that `may` be computed again.
+template <int DC> __device__ __forceinline__ uint64_t odd_rows(const f32x16_t (&acc)[DC / 32], bool may) {
+  float z = 0.f;
+#pragma unroll
+  for (int db = 0; db < DC / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z = fmaf(acc[db][i], 0.f, z);
+  const uint64_t odd = __builtin_amdgcn_ballot_w64(may && !(z == 0.f));
+  return (odd | odd >> 32) & 0xffffffffu;
+}
+
+template <DT D> __device__ __forceinline__ float2 row_pair(const typename Elem<D>::T* row, int head_dim, int lane) {
+  if (2 * lane >= head_dim) return make_float2(0.f, 0.f);
+  return make_float2(to_float<D>(row[2 * lane]), to_float<D>(row[2 * lane + 1]));
+}
+template <DT D>
+__device__ __forceinline__ float row_dot(const typename Elem<D>::T* a, const typename Elem<D>::T* b, int head_dim, int lane) {
+  const float2 x = row_pair<D>(a, head_dim, lane), y = row_pair<D>(b, head_dim, lane);
+  return lanes_sum<64>(fmaf(x.x, y.x, x.y * y.y));
+}
+template <DT D>
+__device__ __forceinline__ void add_scaled(float2& o, float p, const typename Elem<D>::T* row, int head_dim, int lane) {
+  const float2 x = row_pair<D>(row, head_dim, lane);
+  o = make_float2(fmaf(p, x.x, o.x), fmaf(p, x.y, o.y));
+}
+
+// A row in that form into the accumulators of the lanes l and l + 32.
+template <int DC> __device__ __forceinline__ void put_row(f32x16_t (&acc)[DC / 32], float2 o, int l, int lane) {
+#pragma unroll
+  for (int db = 0; db < DC / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c = db * 32 + 8 * (i >> 2) + (i & 3);  // (and c + 4 in the upper half)
+      const float v0 = lane_value(c % 2 ? o.y : o.x, c / 2), v1 = lane_value(c % 2 ? o.y : o.x, c / 2 + 2);
+      if ((lane & 31) == l) acc[db][i] = lane < 32 ? v0 : v1;
+    }
+}
+
+}  // namespace submconv

@@ -1,0 +1,36 @@
+// Attention within a sliding window that keeps an item's first keys visible, backward pass
+// (include/sparse_transformer.h).
+//
+// The kernels of attention_backward.hip over fewer rows: dq walks the keys that the forward pass walks, dk and
+// dv of a block of keys the query rows from the first that sees its first key to the last that sees its
+// last.  The sinks are seen by nearly every row, which would make their blocks as long as the whole item:
+// chunks of rows leave float32 sums for them, which a last kernel adds up in order.
+#include "attention_gradient.h"
+
+using namespace submconv;
+
+extern "C" int sparse_window_attention_backward(const subm_heads_t* dout, const subm_heads_t* q, const subm_heads_t* k,
+                                                const subm_heads_t* v, const subm_heads_t* out, const float* lse,
+                                                int64_t nq, int64_t nk, const int64_t* q_offsets,
+                                                const int64_t* k_offsets, int items, int heads, int kv_heads,
+                                                int head_dim, int dtype, float scale, int64_t left, int64_t right,
+                                                int sinks, const subm_heads_t* dq, const subm_heads_t* dk,
+                                                const subm_heads_t* dv, hipStream_t stream) {
+  return no_throw([&]() -> int {
+    clear_error();
+    const AttentionShape shape{nq, nk, q_offsets, k_offsets, items, heads, kv_heads, head_dim, dtype, scale};
+    Window window{};
+    Status st = check_attention(shape);
+    if (st.ok()) st = check_window(left, right, sinks, nullptr, &window);
+    if (st.ok()) st = check_backward(dout, q, k, v, out, lse, dq, dk, dv, shape);
+    if (!st.ok()) return fail(st);
+    if (nq == 0 && nk == 0) return SUBM_OK;
+    BwdArgs a = backward_args(dout, q, k, v, out, lse, dq, dk, dv, shape);
+    a.window = window;
+    if (dtype == SUBM_F32) st = launch_dim<DT::F32, true>(a, stream);
+    else if (dtype == SUBM_F16) st = launch_dim<DT::F16, true>(a, stream);
+    else st = launch_dim<DT::BF16, true>(a, stream);
+    if (!st.ok()) return fail(st);
+    return SUBM_OK;
+  });
+}
