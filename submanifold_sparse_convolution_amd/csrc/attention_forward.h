@@ -84,6 +84,48 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
   return moves;
 }
 
+// The rows `odd` of a wave's accumulators key by key: see attention_window.h.  (From the kernel's arguments
+// on, so that nothing of it is kept in registers over the loop.)
+template <DT D, int DC, int W, int KEYS, int CUT>
+__device__ __forceinline__ void forward_again(f32x16_t (&acc)[DC / 32], uint64_t odd, float base, float c, int wave, int lane) {
+  const FwdArgs a = fresh_args<FwdArgs>();
+  const int group = a.heads / a.kv_heads;
+  const Share share = window_share<CUT>(a.cut, a.window, true);
+  int tile;
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, 32 * W, share.slot, &tile);
+  int64_t q0, k0;
+  int nq, nk;
+  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+  item_rows(a.k_offsets, a.nk, item, &k0, &nk);
+  nk = a.window.keys(item, nk);
+  const int first = tile * 32 * W, last = min(nq * group, first + 32 * W) - 1;
+  const RowMap qmap{q0, share.head * group, group};
+  const Heads<D> q = heads_of<D>(a.q), k = heads_of<D>(a.k), v = heads_of<D>(a.v);
+  const typename Elem<D>::T* kp = k.data + k0 * k.row + (int64_t)share.head * k.head;
+  const typename Elem<D>::T* vp = v.data + k0 * v.row + (int64_t)share.head * v.head;
+  KeyTiles<KEYS> walk;
+  walk.place(a.window, nk, nk - nq, first / group, last / group);
+  if constexpr (CUT != kNoCut) {
+    int tiles = walk.tiles;
+    const int from = part_steps(a.cut, share.part, &tiles);
+    walk.cut(from, tiles);
+  }
+  for (; odd != 0; odd &= odd - 1) {
+    const int l = __builtin_ctzll(odd), row = first + wave * 32 + l, p = row / group + nk - nq;
+    const typename Elem<D>::T* qr = qmap.at<D>(q, row);
+    const float b = lane_value(base, l);
+    float2 o = make_float2(0.f, 0.f);
+    for (int t = 0; t < walk.tiles; ++t)
+      for (int j = walk.key(t); j < min(walk.key(t) + KEYS, walk.end(t)); ++j) {
+        if (!a.window.sees(p, j)) continue;
+        const float s = row_dot<D>(qr, kp + (int64_t)j * k.row, a.head_dim, lane);
+        const float e = exp2_fast(fmaf(s, a.scale < 0.f ? -c : c, -b));
+        add_scaled<D>(o, to_float<D>(from_float<D>(e)), vp + (int64_t)j * v.row, a.head_dim, lane);
+      }
+    put_row<DC>(acc, o, l, lane);
+  }
+}
+
 // Streams the keys through LDS in tiles of KEYS, two of k and two of v; one step of the loop holds
 // three independent pieces of work, so that the matrix cores run while the exponentials do:
 //   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
@@ -107,8 +149,7 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
   const int lane = threadIdx.x & 63, every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = KG == 1 ? 0 : every / W, wave = KG == 1 ? every : every % W;
   const int group = a.heads / a.kv_heads;
-  Share share = share_of<CUT>(a.cut, blockIdx.x);
-  if constexpr (WINDOW && CUT == kNoCut) share.slot = a.cut.slots - 1 - share.slot;  // (with an open left end the last are the longest)
+  const Share share = WINDOW ? window_share<CUT>(a.cut, a.window, true) : share_of<CUT>(a.cut, blockIdx.x);
   const int head = share.head;
   int tile;
   const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
@@ -173,15 +214,23 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     }
   }
   // (t counts this part's tiles; t and slot apart: inside the loop the slot is a constant)
-  const auto key_of = [&](int t) { return WINDOW ? walk.key(t * KG + part) : (t * KG + part) * KEYS; };
-  const auto left_of = [&](int t, int key) { return WINDOW ? walk.end(t * KG + part) - key : left - key; };
   const auto load_k = [&](int t, int slot) {
-    const int key = key_of(t);
-    lk.load(kp + (int64_t)key * k.row, left_of(t, key), lds + slot * kTile);
+    if constexpr (WINDOW) {
+      const int key = walk.key(t * KG + part);
+      lk.load(kp + (int64_t)key * k.row, walk.end(t * KG + part) - key, lds + slot * kTile);
+    } else {
+      const int key = (t * KG + part) * KEYS;
+      lk.load(kp + (int64_t)key * k.row, left - key, lds + slot * kTile);
+    }
   };
   const auto load_v = [&](int t, int slot) {
-    const int key = t < 0 ? 0 : key_of(t);
-    lv.load(vp + (int64_t)key * v.row, t < 0 ? 0 : left_of(t, key), lds + (2 + slot) * kTile);
+    if constexpr (WINDOW) {
+      const int key = t < 0 ? 0 : walk.key(t * KG + part);
+      lv.load(vp + (int64_t)key * v.row, t < 0 ? 0 : walk.end(t * KG + part) - key, lds + (2 + slot) * kTile);
+    } else {
+      const int key = (t * KG + part) * KEYS;
+      lv.load(vp + (int64_t)key * v.row, t < 0 ? 0 : left - key, lds + (2 + slot) * kTile);
+    }
   };
   const auto scores = [&](int slot, f32x16_t (&s)[KB]) {
 #pragma unroll
@@ -217,23 +266,38 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
 #pragma unroll
       for (int i = 0; i < Elem<D>::kSize / 2; ++i) p[st].v[i] = make_uint4(0, 0, 0, 0);
     scores(0, s0);
+    // WINDOW: whether the wave sees any key of tile t - 1 (was), t (now) and t + 1 (soon).  It leaves out the
+    // steps without any: what it holds of such tiles is masked, and their p is 0, before a step reads it.  At 64
+    // channels, where exponentials bound (four items, 9,371 tokens, 12 heads, 256 keys each way: 54 -> 44 us), and
+    // whole tiles alone: elsewhere the branch costs as much (24,576 tokens, 16 heads of 128: 431 us, 437 with it).
+    constexpr bool kSkip = WINDOW && D != DT::F32 && DP == 64 && KG == 1 && CUT == kNoCut;
+    bool was = false, now = true;
+    if constexpr (kSkip) now = view.sees_any(walk.key(0), KEYS, walk.end(0));
     const auto step = [&](int t, int slot, f32x16_t (&s)[KB], f32x16_t (&next)[KB]) {
       wait_lgkmcnt0();  // this wave's reads of the slots that are about to be loaded have returned
       wait_vmcnt<0>();
       barrier_no_fence();
       load_k(t + 2, slot);
       load_v(t, slot);
-      const int key = key_of(t);
       if constexpr (WINDOW) {
-        const int end = walk.end(t * KG + part);
+        const int tt = t * KG + part, key = walk.key(tt), end = walk.end(tt);
+        if constexpr (kSkip) {
+          const bool soon = view.sees_any(walk.key(tt + 1), KEYS, walk.end(tt + 1)), any = was || now || soon;
+          was = now;
+          now = soon;
+          if (!any) return;
+        }
         if (!view.sees_all(key, KEYS, end))
-          view.mask<KB>(key, end, lane, [&](int kb, int i) { s[kb][i] = -INFINITY; });
-      } else if (key + KEYS > left) {  // keys past the end (perhaps all)
+          view.template mask<KB>(key, end, lane, [&](int kb, int i) { s[kb][i] = -INFINITY; });
+      } else {
+        const int key = (t * KG + part) * KEYS;
+        if (key + KEYS > left) {  // keys past the end (perhaps all)
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (key + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= left) s[kb][i] = -INFINITY;
+            for (int i = 0; i < 16; ++i)
+              if (key + kb * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= left) s[kb][i] = -INFINITY;
+        }
       }
       scores(slot ^ 1, next);
       float shrink;
@@ -282,25 +346,8 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     state.base = base;
   }
   if constexpr (WINDOW) {
-    // A value that is not finite has met the 0 of a row that does not see it: such rows again, key by key.
-    const auto score = [&](int r, const typename Elem<D>::T* key) { return row_dot<D>(qmap.at<D>(q, r), key, a.head_dim, lane); };
-    uint64_t odd = odd_rows<DC>(acc, there && isfinite(sum));
-    while (odd != 0) {
-      const int l = __builtin_ctzll(odd);
-      odd &= odd - 1;
-      const int r = tile * kRows + wave * 32 + l, p = r / group + nk - nq;
-      const float base = lane_value(state.base, l);
-      float2 o = make_float2(0.f, 0.f);
-      for (int t = 0; t < tiles; ++t) {
-        const int from = walk.key(t), to = min(from + KEYS, walk.end(t));
-        for (int j = from; j < to; ++j) {
-          if (!a.window.sees(p, j)) continue;
-          const float pj = exp2_fast(fmaf(score(r, kp + (int64_t)j * k.row), a.scale < 0.f ? -c : c, -base));
-          add_scaled<D>(o, to_float<D>(from_float<D>(pj)), vp + (int64_t)j * v.row, a.head_dim, lane);
-        }
-      }
-      put_row<DC>(acc, o, l, lane);
-    }
+    const uint64_t odd = odd_rows<DC>(acc, there && __builtin_isfinite(sum));
+    if (odd != 0) forward_again<D, DC, W, KEYS, CUT>(acc, odd, state.base, c, wave, lane);
   }
   if (!there) return;
   if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0)) {
@@ -417,17 +464,16 @@ Status launch(FwdArgs a, hipStream_t stream) {
   constexpr int kUnits = 256;
   constexpr bool kWide = D != DT::F32 && tile_width(DC) == 128;
   const int64_t rows = a.nq * (a.heads / a.kv_heads), spare = (int64_t)a.items * a.kv_heads;
-  // (of a window: those of a tile of 128 rows; its tiles differ in length, and the last are not cut)
+  // (of a window: those of a tile)
   const int64_t keys = WINDOW ? a.window.walked(a.nk / a.items, 128 / (a.heads / a.kv_heads)) : a.nk / a.items;
+  if constexpr (WINDOW) a.window.runs = a.window.in_runs(a.nk / a.items, a.heads / a.kv_heads);
   // float32 scores take 8 times as long, so its parts may be short.
-  constexpr int kShare = D == DT::F32 ? 32 : 512;
-  if constexpr (kWide) {
+  constexpr int kShare = D == DT::F32 ? 32 : WINDOW ? 256 : 512;
+  if constexpr (kWide && !WINDOW) {
     const int64_t slots = rows / 256 + a.items;
     if (slots * a.kv_heads >= kUnits && rows / a.items >= 256) {
-      a.cut = plan_cut(slots, a.kv_heads, spare, WINDOW ? 0 : keys, kShare, kUnits, 0, kGainAt128);
-      if constexpr (!WINDOW) {
-        if (a.cut.parts > 1) return launch_cut<D, DC, 8, kCutLast, WINDOW>(a, stream);
-      }
+      a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, kUnits, 0, kGainAt128);
+      if (a.cut.parts > 1) return launch_cut<D, DC, 8, kCutLast, WINDOW>(a, stream);
       SUBM_HIP_TRY((launch_tiles<D, DC, 8, 1, kNoCut, WINDOW>(a, stream)));
       return Status{};
     }
@@ -437,7 +483,12 @@ Status launch(FwdArgs a, hipStream_t stream) {
   // ms, 1.39 in parts), nor at the short items that are left here at 128.
   const int64_t slots = rows / 128 + a.items, tiles = slots * a.kv_heads;
   constexpr int kFew = kUnits * (D == DT::F32 ? 1 : 2);
-  a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, D == DT::F32 && !WINDOW ? kUnits : INT32_MAX, kFew, kGain);
+  if constexpr (WINDOW) {
+    constexpr int64_t kSlots = kUnits * (D == DT::F32 ? 1 : tile_width(DC) == 64 ? 3 : 2);
+    a.cut = plan_window_cut(a.window, slots, a.kv_heads, a.nk / a.items, keys, kShare, kSlots, kFew);
+  } else {
+    a.cut = plan_cut(slots, a.kv_heads, spare, keys, kShare, D == DT::F32 ? kUnits : INT32_MAX, kFew, kGain);
+  }
   // Where a compute unit gets one workgroup, two groups of waves on each tile (2,000 tokens, 16 heads
   // of 128: 42 us, 54 in two parts; with fewer than 512 keys the join eats the gain).  float32 waves
   // need the registers of two.

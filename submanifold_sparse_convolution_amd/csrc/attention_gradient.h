@@ -147,6 +147,99 @@ template <DT D> __global__ __launch_bounds__(256) void attention_norm_kernel(Bwd
   a.v_norm[head * a.v_slots + blockIdx.x] = sqrtf(sq);
 }
 
+// The rows `odd` of a wave's dq, or the keys `odd` of its dk and dv, one by one (see attention_window.h), from the
+// kernel's arguments on.
+template <DT D, int DC, int W, int CUT>
+__device__ __forceinline__ void dq_again(f32x16_t (&acc)[DC / 32], uint64_t odd, float base, float d, float unit, int wave, int lane) {
+  const BwdArgs a = fresh_args<BwdArgs>();
+  const int group = a.heads / a.kv_heads;
+  const Share share = window_share<CUT>(a.q_cut, a.window, true);
+  int tile;
+  const int item = find_item(a.q_offsets, a.nq, a.items, group, 32 * W, share.slot, &tile);
+  int64_t q0, k0;
+  int nq, nk;
+  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+  item_rows(a.k_offsets, a.nk, item, &k0, &nk);
+  const int first = tile * 32 * W, last = min(nq * group, first + 32 * W) - 1;
+  const RowMap qmap{q0, share.head * group, group};
+  const Heads<D> k = heads_of<D>(a.k), v = heads_of<D>(a.v);
+  const typename Elem<D>::T* kp = k.data + k0 * k.row + (int64_t)share.head * k.head;
+  const typename Elem<D>::T* vp = v.data + k0 * v.row + (int64_t)share.head * v.head;
+  KeyTiles<kStep> walk;
+  walk.place(a.window, nk, nk - nq, first / group, last / group);
+  if constexpr (CUT != kNoCut) {
+    int tiles = walk.tiles;
+    const int from = part_steps(a.q_cut, share.part, &tiles);
+    walk.cut(from, tiles);
+  }
+  for (; odd != 0; odd &= odd - 1) {
+    const int l = __builtin_ctzll(odd), row = first + wave * 32 + l, p = row / group + nk - nq;
+    const typename Elem<D>::T *qr = qmap.at<D>(heads_of<D>(a.q), row), *gr = qmap.at<D>(heads_of<D>(a.dout), row);
+    const float b = lane_value(base, l), dr = lane_value(d, l), u = lane_value(unit, l);
+    float2 o = make_float2(0.f, 0.f);
+    for (int t = 0; t < walk.tiles; ++t)
+      for (int j = walk.key(t); j < min(walk.key(t) + kStep, walk.end(t)); ++j) {
+        if (!a.window.sees(p, j)) continue;
+        const typename Elem<D>::T *kr = kp + (int64_t)j * k.row, *vr = vp + (int64_t)j * v.row;
+        const float e = exp2_fast(fmaf(row_dot<D>(qr, kr, a.head_dim, lane), a.scale * kLog2e, -b)) *
+                        (row_dot<D>(gr, vr, a.head_dim, lane) - dr) * u;
+        add_scaled<D>(o, to_float<D>(from_float<D>(e)), kr, a.head_dim, lane);
+      }
+    put_row<DC>(acc, o, l, lane);
+  }
+}
+
+template <DT D, int DC, int W, int CUT, bool SINKS>
+__device__ __forceinline__ void dkv_again(f32x16_t (&dk)[DC / 32], f32x16_t (&dv)[DC / 32], uint64_t odd, float unit, int wave, int lane) {
+  const BwdArgs a = fresh_args<BwdArgs>();
+  const int group = a.heads / a.kv_heads;
+  const Share share = !SINKS ? window_share<CUT>(a.k_cut, a.window, false) : share_of<CUT>(a.k_cut, blockIdx.x);
+  int tile, chunk = 0;
+  const int item = SINKS ? find_item(a.q_offsets, a.nq, a.items, group, a.sink_rows, share.slot, &chunk)
+                         : find_item(a.k_offsets, a.nk, a.items, 1, 32 * W, share.slot, &tile);
+  if constexpr (SINKS) tile = blockIdx.z;
+  int64_t q0, k0;
+  int nq, nk;
+  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+  item_rows(a.k_offsets, a.nk, item, &k0, &nk);
+  const int shift = nk - nq;
+  const RowMap qmap{q0, share.head * group, group}, kmap{k0, share.head, 1};
+  const float* norm = a.norm + share.head * (a.nq * group) + q0 * group;
+  const float* delta = a.delta + share.head * (a.nq * group) + q0 * group;
+  const float f = D == DT::F16 ? unit / 32768.f : 1.f;
+  // the rows of this workgroup: of the chunk, or of its part of those that the tile's keys are seen by
+  int begin = 0, end = nq * group;
+  if constexpr (SINKS) {
+    begin = chunk * a.sink_rows;
+    end = (int)min((int64_t)end, (int64_t)begin + a.sink_rows);
+  } else if constexpr (CUT != kNoCut) {
+    const int last = min(nk, (tile + 1) * 32 * W) - 1;
+    int unused;
+    a.window.rows(max(tile * 32 * W, min(a.window.sinks, last)), false, nq, shift, group, &begin, &unused);
+    a.window.rows(last, false, nq, shift, group, &unused, &end);
+    int steps = (max(end - begin, 0) + kStep - 1) / kStep;
+    begin += part_steps(a.k_cut, share.part, &steps) * kStep;
+    end = min(end, begin + steps * kStep);
+  }
+  for (; odd != 0; odd &= odd - 1) {
+    const int l = __builtin_ctzll(odd), j = tile * 32 * W + wave * 32 + l;
+    if (!SINKS && j < a.window.sinks) continue;  // (not this kernel's)
+    const typename Elem<D>::T *kr = kmap.at<D>(heads_of<D>(a.k), j), *vr = kmap.at<D>(heads_of<D>(a.v), j);
+    int from, to;
+    a.window.rows(j, SINKS, nq, shift, group, &from, &to);
+    float2 ok = make_float2(0.f, 0.f), ov = ok;
+    for (int i = max(from, begin); i < min(to, end); ++i) {
+      const typename Elem<D>::T *qr = qmap.at<D>(heads_of<D>(a.q), i), *gr = qmap.at<D>(heads_of<D>(a.dout), i);
+      const float p = exp2_fast(fmaf(row_dot<D>(qr, kr, a.head_dim, lane), a.scale * kLog2e, -norm[i]));
+      const float e = p * (row_dot<D>(gr, vr, a.head_dim, lane) - delta[i]) * f;
+      add_scaled<D>(ov, to_float<D>(from_float<D>(p)), gr, a.head_dim, lane);
+      add_scaled<D>(ok, to_float<D>(from_float<D>(e)), qr, a.head_dim, lane);
+    }
+    put_row<DC>(dk, ok, l, lane);
+    put_row<DC>(dv, ov, l, lane);
+  }
+}
+
 // d of the own query rows, then dq over the keys, which stream through LDS in tiles of 32.  As in
 // the forward pass a step holds independent pieces of work:
 //   scores and dp of tile t + 1 (k, v),  e of tile t,  product of tile t - 1 (k).
@@ -160,8 +253,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   __shared__ float s_norm[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads;
-  Share share = share_of<CUT>(a.q_cut, blockIdx.x);
-  if constexpr (WINDOW && CUT == kNoCut) share.slot = a.q_cut.slots - 1 - share.slot;  // (with an open left end the last are the longest)
+  const Share share = WINDOW ? window_share<CUT>(a.q_cut, a.window, true) : share_of<CUT>(a.q_cut, blockIdx.x);
   const int head = share.head;
   int tile;
   const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
@@ -246,12 +338,22 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
       vp += (int64_t)t0 * kStep * v.row;
     }
   }
-  const auto key_of = [&](int t) { return WINDOW ? walk.key(t) : t * kStep; };
-  const auto left_of = [&](int t) { return WINDOW ? walk.end(t) - walk.key(t) : left - t * kStep; };
   const auto load_k = [&](int t, int slot) {
-    lk.load(kp + (int64_t)(WINDOW && t < 0 ? 0 : key_of(t)) * k.row, t < 0 ? 0 : left_of(t), lds + slot * kTile);
+    if constexpr (WINDOW) {
+      const int key = t < 0 ? 0 : walk.key(t);
+      lk.load(kp + (int64_t)key * k.row, t < 0 ? 0 : walk.end(t) - key, lds + slot * kTile);
+    } else {
+      lk.load(kp + (int64_t)t * kStep * k.row, t < 0 ? 0 : left - t * kStep, lds + slot * kTile);
+    }
   };
-  const auto load_v = [&](int t, int slot) { lv.load(vp + (int64_t)key_of(t) * v.row, left_of(t), lds + (4 + slot) * kTile); };
+  const auto load_v = [&](int t, int slot) {
+    if constexpr (WINDOW) {
+      const int key = walk.key(t);
+      lv.load(vp + (int64_t)key * v.row, walk.end(t) - key, lds + (4 + slot) * kTile);
+    } else {
+      lv.load(vp + (int64_t)t * kStep * v.row, left - t * kStep, lds + (4 + slot) * kTile);
+    }
+  };
   const auto scores = [&](int slot, f32x16_t& s, f32x16_t& dp) {
     s = zero16();
     dp = zero16();
@@ -297,7 +399,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
       for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], c, -base)) * (dp[i] - d) * unit;
       if constexpr (WINDOW) {
         const int key = walk.key(t), end = walk.end(t);
-        if (!view.sees_all(key, kStep, end)) view.mask<1>(key, end, lane, [&](int, int i) { s[i] = 0.f; });
+        if (!view.sees_all(key, kStep, end)) view.template mask<1>(key, end, lane, [&](int, int i) { s[i] = 0.f; });
       } else if ((t + 1) * kStep > left) {  // (a key past the end scores 0, which p need not take to 0)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -321,27 +423,9 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     wait_vmcnt<0>();
     product((tiles - 1) % 4, e);
   }
-  if constexpr (WINDOW) {  // (as in the forward pass)
-    uint64_t odd = odd_rows<DC>(acc, there && isfinite(base) && isfinite(d));
-    while (odd != 0) {
-      const int l = __builtin_ctzll(odd);
-      odd &= odd - 1;
-      const int r = tile * kRows + wave * 32 + l, p = r / group + nk - nq;
-      const float lse2 = lane_value(base, l), dr = lane_value(d, l), ur = lane_value(unit, l);
-      const typename Elem<D>::T *qr = qmap.at<D>(heads_of<D>(a.q), r), *gr = qmap.at<D>(heads_of<D>(a.dout), r);
-      float2 o = make_float2(0.f, 0.f);
-      for (int t = 0; t < tiles; ++t) {
-        const int from = walk.key(t), to = min(from + kStep, walk.end(t));
-        for (int j = from; j < to; ++j) {
-          if (!a.window.sees(p, j)) continue;
-          const typename Elem<D>::T *kr = kp + (int64_t)j * k.row, *vr = vp + (int64_t)j * v.row;
-          const float e = exp2_fast(fmaf(row_dot<D>(qr, kr, a.head_dim, lane), c, -lse2)) *
-                          (row_dot<D>(gr, vr, a.head_dim, lane) - dr) * ur;
-          add_scaled<D>(o, to_float<D>(from_float<D>(e)), kr, a.head_dim, lane);
-        }
-      }
-      put_row<DC>(acc, o, l, lane);
-    }
+  if constexpr (WINDOW) {
+    const uint64_t odd = odd_rows<DC>(acc, there && __builtin_isfinite(base) && __builtin_isfinite(d));
+    if (odd != 0) dq_again<D, DC, W, CUT>(acc, odd, base, d, unit, wave, lane);
   }
   if (!there) return;
   if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0))
@@ -384,7 +468,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   __shared__ float2 s_peak[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.heads / a.kv_heads;
-  const Share share = share_of<CUT>(a.k_cut, blockIdx.x);
+  const Share share = WINDOW && !SINKS ? window_share<CUT>(a.k_cut, a.window, false) : share_of<CUT>(a.k_cut, blockIdx.x);
   const int head = share.head;
   int tile, chunk = 0;
   const int item = SINKS ? find_item(a.q_offsets, a.nq, a.items, group, a.sink_rows, share.slot, &chunk)
@@ -479,12 +563,11 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     r0 = (WINDOW ? row0 : 0) + part_steps(a.k_cut, share.part, &steps) * kStep;
     end = min(end, r0 + steps * kStep);
   }
-  const int begin = r0;
   int tok = r0 / group, rem = r0 - tok * group;  // of the next tile to load
   const int tok_step = kStep / group, rem_step = kStep % group;
   lq.place(q, a.head_dim, group, rem, magic);
   lg.place(g, a.head_dim, group, rem, magic);
-  const auto load = [&](int slot) {  // the next tile
+  const auto load = [&](int slot) __attribute__((always_inline)) {  // the next tile
     lq.load(qp + (int64_t)tok * q.row, end - r0, lds + slot * kTile);
     lg.load(gp + (int64_t)tok * g.row, end - r0, lds + (2 + slot) * kTile);
     if (wave == 0) load_stats(norm + r0, end - r0, stat + slot * 512, lane);
@@ -505,12 +588,15 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   f32x16_t dk[DC / 32], dv[DC / 32];
 #pragma unroll
   for (int db = 0; db < DC / 32; ++db) dk[db] = dv[db] = zero16();
-  const auto step = [&](int slot) {
+  const auto step = [&](int slot) __attribute__((always_inline)) {
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
     const int r = r0 - kStep;  // (the rows of this step; r0 is the next to load)
     load(slot ^ 1);
+    if constexpr (WINDOW) {
+      if (!view.sees_any(r, kStep)) return;
+    }
     f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < DC / 16; ++kk) {
@@ -553,31 +639,9 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     }
   }
   wait_vmcnt<0>();  // (the loads past the end)
-  if constexpr (WINDOW) {  // (as in the forward pass, a wave a key)
-    uint64_t odd = odd_rows<DC>(dk, there) | odd_rows<DC>(dv, there);
-    while (odd != 0) {
-      const int l = __builtin_ctzll(odd);
-      odd &= odd - 1;
-      const int j = tile * kKeys + wave * 32 + l;
-      if (!SINKS && j < a.window.sinks) continue;
-      const typename Elem<D>::T *kr = kmap.at<D>(heads_of<D>(a.k), j), *vr = kmap.at<D>(v, j);
-      int from, to;
-      a.window.rows(j, SINKS, nq, shift, group, &from, &to);
-      from = max(from, begin);
-      to = min(to, end);
-      const RowMap qmap{q0, head * group, group};
-      float2 ok = make_float2(0.f, 0.f), ov = ok;
-      for (int i = from; i < to; ++i) {
-        const typename Elem<D>::T *qr = qmap.at<D>(q, i), *gr = qmap.at<D>(g, i);
-        const float p = exp2_fast(fmaf(row_dot<D>(qr, kr, a.head_dim, lane), c, -norm[i]));
-        float e = p * (row_dot<D>(gr, vr, a.head_dim, lane) - delta[i]);
-        if constexpr (D == DT::F16) e *= unit * p_unit;
-        add_scaled<D>(ov, to_float<D>(from_float<D>(p)), gr, a.head_dim, lane);
-        add_scaled<D>(ok, to_float<D>(from_float<D>(e)), qr, a.head_dim, lane);
-      }
-      put_row<DC>(dk, ok, l, lane);
-      put_row<DC>(dv, ov, l, lane);
-    }
+  if constexpr (WINDOW) {
+    const uint64_t odd = odd_rows<DC>(dk, there) | odd_rows<DC>(dv, there);
+    if (odd != 0) dkv_again<D, DC, W, CUT, SINKS>(dk, dv, odd, unit, wave, lane);
   }
   if (!there) return;
   if constexpr (SINKS) {
@@ -720,7 +784,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
   const int group = a.heads / a.kv_heads;
   const int64_t rows = a.nq * group, spare = (int64_t)a.items * a.kv_heads;
   // 128 channels in 16 bits: 8 waves share a tile stream where they fill the compute units.
-  constexpr bool kWide = D != DT::F32 && DP == 128;
+  constexpr bool kWide = D != DT::F32 && DP == 128 && !WINDOW;
   const bool wide_q = kWide && (rows / 256 + a.items) * a.kv_heads >= kUnits && rows / a.items >= 256;
   const bool wide_k = kWide && (a.nk / 256 + a.items) * a.kv_heads >= kUnits && a.nk / a.items >= 256;
   const int q_rows = wide_q ? 256 : 128, k_rows = wide_k ? 256 : 128;
@@ -736,11 +800,13 @@ Status launch(BwdArgs a, hipStream_t stream) {
   constexpr double kLess = kWide ? kGainAt128 : kGain;
   const int64_t k_slots = a.nk / k_rows + a.items;
   const int64_t q_full = wide_q ? kUnits : kResident, k_full = wide_k ? kUnits : kResident;
-  if constexpr (WINDOW) {  // (tiles differ in length: the last are not cut)
-    const int64_t q_walks = a.window.walked(a.nk / a.items, 128 / group);
-    const int64_t k_walks = a.window.walked(a.nq / a.items, 128) * group;
-    a.q_cut = plan_cut(a.q_slots, a.kv_heads, spare, q_walks, kLeast, wide_q ? 0 : INT32_MAX, kFew, 0.0);
-    a.k_cut = plan_cut(k_slots, a.kv_heads, spare, k_walks, kLeast, wide_k ? 0 : INT32_MAX, kFew, 0.0);
+  if constexpr (WINDOW) {
+    const int64_t q_walks = a.window.walked(a.nk / a.items, q_rows / group);
+    const int64_t k_walks = a.window.walked(a.nq / a.items, k_rows) * group;
+    a.window.runs = a.window.in_runs(a.nk / a.items, group);
+    constexpr int64_t kSlots = kUnits * (D == DT::F32 ? 1 : DP == 64 ? 3 : 2);
+    a.q_cut = plan_window_cut(a.window, a.q_slots, a.kv_heads, a.nk / a.items, q_walks, kLeast, kSlots, kFew);
+    a.k_cut = plan_window_cut(a.window, k_slots, a.kv_heads, a.nq / a.items, k_walks, kLeast, kSlots, kFew);
   } else {
     a.q_cut = plan_cut(a.q_slots, a.kv_heads, spare, a.nk / a.items, kLeast, q_full, kFew, kLess);
     a.k_cut = plan_cut(k_slots, a.kv_heads, spare, rows / a.items, kLeast, k_full, kFew, kLess);

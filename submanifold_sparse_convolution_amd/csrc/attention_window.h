@@ -14,6 +14,7 @@ struct Window {
   int64_t left, right;  // at most kOpen, which is more than there are keys
   int sinks;
   const int64_t* k_lengths;  // keys of each item that are there, or null: all its rows
+  bool runs;                 // most tiles walk as many keys: runs of them to each XCD (window_share)
 
   // How many keys an item with `rows` rows of keys has.
   __device__ __forceinline__ int keys(int item, int rows) const {
@@ -41,7 +42,47 @@ struct Window {
     const int64_t most = left + right + sinks + rows;
     return most < keys ? most : keys;
   }
+  // Host: whether most tiles of items of `keys` walk the same number of keys, and heads are not grouped.
+  bool in_runs(int64_t keys, int group) const { return group == 1 && (left + right) * 2 < keys; }
 };
+
+// Host: plan_cut for windows, whose last tiles stay whole (in parts they measured the same).  `resident`: workgroups
+// that the machine holds.  Where most of an item is seen the longest tile takes twice the mean, and few tiles
+// leave compute units that wait for it: then in at least four parts (three and six, which the XCDs do not share
+// evenly, measured up to 30 % slower).  16,384 tokens, 8 / 2 heads of 128, causal, backward: 3.48 -> 1.81 ms; 9,000
+// tokens, 6 heads of 64, forward 153 -> 120 us, backward 422 -> 384; with more tiles two share a unit, and
+// the one left alone speeds up: 8,000 tokens, 8 heads of 128, forward 217 us whole and 231 in parts.
+inline Cut plan_window_cut(const Window& w, int64_t slots, int kv_heads, int64_t keys, int64_t walked, int least,
+                           int64_t resident, int64_t few) {
+  constexpr int kUneven = 4;
+  const int64_t tiles = slots * kv_heads;
+  const bool uneven = (w.left + w.right) * 4 >= keys * 3;
+  if (uneven && tiles * 4 <= resident * 3 && few < tiles * kUneven) few = tiles * kUneven;
+  return plan_cut(slots, kv_heads, 0, walked, least, INT32_MAX, few, kGain);
+}
+
+// The workgroup's tile (or part of one).  Neighbouring tiles of a window walk nearly the same keys, while the XCDs
+// take workgroups in turn and each has its own L2: every XCD gets a run of consecutive tiles, so that what
+// one loads the next finds there (24,576 tokens, 16 heads of 128, 2,048 keys: 493 -> 437 us).  Not with grouped
+// heads, whose tiles are that many times fewer tokens apart as it is (16,384 tokens, 8 / 2 heads: 150 us, 176 in
+// runs).  Where tiles differ in length (an open end) the longest go first (`last_first`: those of the last rows),
+// which walk the same keys from the start on (16,384 tokens, 8 / 2 heads of 128, causal: 673 -> 526 us).
+template <int CUT> __device__ __forceinline__ Share window_share(const Cut& c, const Window& w, bool last_first) {
+  Share s = share_of<CUT>(c, blockIdx.x);
+  if (CUT == kCutAll || s.part >= 0) return s;
+  if (w.runs) {
+    constexpr uint32_t kXcds = 8;
+    const uint32_t block = CUT == kNoCut ? blockIdx.x + gridDim.x * blockIdx.y : blockIdx.x;
+    const uint32_t all = CUT == kNoCut ? gridDim.x * gridDim.y : (uint32_t)c.whole;
+    const uint32_t xcd = block % kXcds, each = all / kXcds, more = all % kXcds;
+    const uint32_t id = xcd * each + min(xcd, more) + block / kXcds;
+    s.head = first_lane(id / (uint32_t)c.slots);
+    s.slot = (int)(id - (uint32_t)s.head * c.slots);
+  } else if (last_first && CUT == kNoCut) {
+    s.slot = c.slots - 1 - s.slot;
+  }
+  return s;
+}
 
 constexpr int64_t kOpen = int64_t(1) << 31;  // a window's end that no position reaches
 constexpr int kMaxSinks = 128;
@@ -84,14 +125,16 @@ struct RowView {
   int lo, hi, sinks;
   uint32_t span;         // the row sees lo .. lo + span (and the sinks)
   int wave_lo, wave_hi;  // every row of the wave sees these and what lies between (and the sinks up to wave_hi)
+  int wave_low, wave_high;  // some row of the wave sees these, and none sees any before (but sinks) or after
 
   __device__ __forceinline__ void place(const Window& w, int nk, int shift, int token, int first_token, int last_token) {
-    int unused;
     w.range((int64_t)token + shift, nk, &lo, &hi);
-    w.range((int64_t)first_token + shift, nk, &unused, &wave_hi);
-    w.range((int64_t)last_token + shift, nk, &wave_lo, &unused);
+    w.range((int64_t)first_token + shift, nk, &wave_low, &wave_hi);
+    w.range((int64_t)last_token + shift, nk, &wave_lo, &wave_high);
     wave_lo = first_lane(wave_lo);
     wave_hi = first_lane(wave_hi);
+    wave_low = first_lane(wave_low);
+    wave_high = first_lane(wave_high);
     sinks = w.sinks;
     if (hi < lo) lo = INT32_MAX;  // (sees no more than sinks)
     span = hi < lo ? 0u : (uint32_t)(hi - lo);
@@ -99,6 +142,9 @@ struct RowView {
   // Keys key .. key + n - 1, of which those from `end` on are not there.
   __device__ __forceinline__ bool sees_all(int key, int n, int end) const {
     return key + n <= end && key + n - 1 <= wave_hi && (key >= wave_lo || key + n <= sinks);
+  }
+  __device__ __forceinline__ bool sees_any(int key, int n, int end) const {
+    return key < end && key <= wave_high && (key + n > wave_low || key < sinks);
   }
   // Calls hide(kb, i) for element i of each 32 keys' scores that the row does not see.
   template <int KB, typename Hide>
@@ -127,19 +173,23 @@ struct RowView {
 struct KeyView {
   int from;
   uint32_t span;  // the key is seen by rows from .. from + span - 1
-  int wave_from, wave_to;
+  int wave_from, wave_to;    // every key of the wave is seen by rows wave_from .. wave_to - 1,
+  int wave_first, wave_end;  // some key by these and none by others
 
   __device__ __forceinline__ void place(const Window& w, bool sink, int nq, int shift, int group, int key, int first_key,
                                         int last_key) {
-    int to, unused;
+    int to;
     w.rows(key, sink, nq, shift, group, &from, &to);
-    w.rows(first_key, sink, nq, shift, group, &unused, &wave_to);
-    w.rows(last_key, sink, nq, shift, group, &wave_from, &unused);
+    w.rows(first_key, sink, nq, shift, group, &wave_first, &wave_to);
+    w.rows(last_key, sink, nq, shift, group, &wave_from, &wave_end);
     wave_from = first_lane(wave_from);
     wave_to = first_lane(wave_to);
+    wave_first = first_lane(wave_first);
+    wave_end = first_lane(wave_end);
     span = to > from ? (uint32_t)(to - from) : 0u;
   }
   __device__ __forceinline__ bool sees_all(int row, int n) const { return row >= wave_from && row + n <= wave_to; }
+  __device__ __forceinline__ bool sees_any(int row, int n) const { return row < wave_end && row + n > wave_first; }
   // Calls hide(i) for element i of 32 rows' values that the key is not seen by.
   template <typename Hide> __device__ __forceinline__ void mask(int row, int lane, const Hide& hide) const {
     const uint32_t at = (uint32_t)(row + 4 * (lane >> 5)) - (uint32_t)from;
@@ -153,6 +203,18 @@ struct KeyView {
 //
 // A matrix product adds 0 times a hidden key's value, which is NaN where the value is not finite.  A row
 // that ends so is computed again over what it sees alone, a wave a row, two channels a lane.
+
+// The kernel's arguments, read again: what only this rare work needs of them is not kept in registers.
+template <typename A> __device__ __forceinline__ A fresh_args() {
+  static_assert(sizeof(A) % 4 == 0, "whole words");
+  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  const auto* words = (const __attribute__((address_space(4))) uint32_t*)p;
+  struct Words { uint32_t w[sizeof(A) / 4]; } all;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(A) / 4); ++i) all.w[i] = words[i];
+  return __builtin_bit_cast(A, all);
+}
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
@@ -191,8 +253,9 @@ template <int DC> __device__ __forceinline__ void put_row(f32x16_t (&acc)[DC / 3
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int c = db * 32 + 8 * (i >> 2) + (i & 3);  // (and c + 4 in the upper half)
-      const float v0 = lane_value(c % 2 ? o.y : o.x, c / 2), v1 = lane_value(c % 2 ? o.y : o.x, c / 2 + 2);
-      if ((lane & 31) == l) acc[db][i] = lane < 32 ? v0 : v1;
+      const float v = __shfl(c % 2 ? o.y : o.x, c / 2 + 2 * (lane >> 5), 64);
+      if ((lane & 31) == l) acc[db][i] = v;
+      __builtin_amdgcn_sched_barrier(0);  // (one after the other: together they would need 64 registers more)
     }
 }
 

@@ -13,7 +13,7 @@ Status check_window(int64_t left, int64_t right, int sinks, const int64_t* k_len
   if (sinks > kMaxSinks) return make_status(SUBM_ERR_UNSUPPORTED, "sinks exceeds 128");
   if ((reinterpret_cast<uintptr_t>(k_lengths) & 7u) != 0)
     return make_status(SUBM_ERR_INVALID_ARG, "k_lengths is not 8-byte aligned");
-  *w = Window{std::min(left, kOpen), std::min(right, kOpen), left >= kOpen ? 0 : sinks, k_lengths};
+  *w = Window{std::min(left, kOpen), std::min(right, kOpen), left >= kOpen ? 0 : sinks, k_lengths, false};
   return Status{};
 }
 
