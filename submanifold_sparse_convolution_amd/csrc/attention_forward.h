@@ -131,9 +131,9 @@ __device__ __forceinline__ void forward_again(f32x16_t (&acc)[DC / 32], uint64_t
 //   scores of tile t + 1 (k),  softmax of tile t,  product of tile t - 1 (v).
 // (Four tiles of each in flight: the same time.)
 //
-// KG = 2: two groups of W waves hold the same rows and take every other tile of keys, joined through
+// KG > 1: that many groups of W waves hold the same rows and take every KG-th tile of keys, joined through
 // LDS at the end: where a compute unit gets one workgroup, a lone wave a SIMD would wait for each
-// instruction's result in turn.
+// instruction's result in turn; and few rows are one wave's.
 //
 // WINDOW: each row sees a range of keys and the first `sinks`.  The tiles are those of the sinks and those
 // from the first key to the last that one of the tile's rows sees; scores are masked in the tiles that some
@@ -145,19 +145,22 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
   constexpr int kRows = 32 * W;
   using Loader = TileLoader<D, DP, KEYS, W>;
   __shared__ __attribute__((aligned(1024))) unsigned char s_kv[KG * 4 * kTile];
-  __shared__ float2 s_join[KG == 1 ? 1 : W * 64];
+  __shared__ float2 s_join[KG == 1 ? 1 : (KG - 1) * W * 64];
   const int lane = threadIdx.x & 63, every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = KG == 1 ? 0 : every / W, wave = KG == 1 ? every : every % W;
   const int group = a.heads / a.kv_heads;
   const Share share = WINDOW ? window_share<CUT>(a.cut, a.window, true) : share_of<CUT>(a.cut, blockIdx.x);
   const int head = share.head;
-  int tile;
-  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
+  int item, tile, nq, nk;
   int64_t q0, k0;
-  int nq, nk;
-  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
-  item_rows(a.k_offsets, a.nk, item, &k0, &nk);
-  if constexpr (WINDOW) nk = a.window.keys(item, nk);
+  if constexpr (WINDOW) {
+    const Item it = find_rows<false>(a, a.window, group, kRows, share.slot);
+    item = it.index, tile = it.tile, q0 = it.q0, nq = it.nq, k0 = it.k0, nk = it.nk;
+  } else {
+    item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
+    item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+    item_rows(a.k_offsets, a.nk, item, &k0, &nk);
+  }
   const int rows = nq * group;
   if ((int64_t)tile * kRows >= rows) return;
   const RowMap qmap{q0, head * group, group};
@@ -171,16 +174,19 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
   const typename Elem<D>::T* qrow = qmap.at<D>(q, there ? row : 0);
   // a negative scale goes into q, so that the largest score is the largest product
   const uint32_t flip = a.scale < 0.f ? (D == DT::F32 ? 0x80000000u : 0x80008000u) : 0u;
+  const auto flip_frag = [&](Frag<D>& f) {
+#pragma unroll
+    for (int i = 0; i < Elem<D>::kSize / 2; ++i) {
+      f.v[i].x ^= flip;
+      f.v[i].y ^= flip;
+      f.v[i].z ^= flip;
+      f.v[i].w ^= flip;
+    }
+  };
 #pragma unroll
   for (int kk = 0; kk < DC / 16; ++kk) {
     qf[kk] = own_frag<D>(qrow, there, kk, a.head_dim, lane);
-#pragma unroll
-    for (int i = 0; i < Elem<D>::kSize / 2; ++i) {
-      qf[kk].v[i].x ^= flip;
-      qf[kk].v[i].y ^= flip;
-      qf[kk].v[i].z ^= flip;
-      qf[kk].v[i].w ^= flip;
-    }
+    if constexpr (!WINDOW) flip_frag(qf[kk]);
   }
   // (a scale of 0 becomes tiny: a key past the end must still score -infinity)
   const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
@@ -257,6 +263,10 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     load_k(0, 0);
     load_k(1, 1);
     load_v(-1, 1);
+    if constexpr (WINDOW) {  // (short walks: not before the first tiles are on their way)
+#pragma unroll
+      for (int kk = 0; kk < DC / 16; ++kk) flip_frag(qf[kk]);
+    }
     wait_vmcnt<2 * Loader::N>();
     barrier_no_fence();
     f32x16_t s0[KB], s1[KB];
@@ -328,22 +338,27 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     product((steps - 1) % 2, p);
   }
   float sum = half_sum(state.sum);
-  if constexpr (KG == 2) {
-    const uint32_t at = lds_offset(s_kv) + wave * (DC / 32 * 4096);
+  if constexpr (KG > 1) {
+    constexpr int kArea = DC / 32 * 4096;
+    static_assert((KG - 1) * W * kArea <= KG * 4 * kTile, "the tiles make room");
+    const uint32_t at = lds_offset(s_kv) + wave * kArea;
     wait_lgkmcnt0();
     __syncthreads();  // (every part is done with its tiles)
-    if (part == 1) {
-      put_acc<DC>(at, acc, lane);
-      s_join[wave * 64 + lane] = make_float2(state.base, sum);
+    if (part > 0) {
+      put_acc<DC>(at + (part - 1) * W * kArea, acc, lane);
+      s_join[((part - 1) * W + wave) * 64 + lane] = make_float2(state.base, sum);
     }
     __syncthreads();
-    if (part == 1) return;
-    const float2 other = s_join[wave * 64 + lane];
-    const float base = fmaxf(state.base, other.x);
-    const float mine = exp2_fast(state.base - base), theirs = exp2_fast(other.x - base);
-    add_acc<DC>(at, acc, mine, theirs, lane);
-    sum = fmaf(other.y, theirs, sum * mine);
-    state.base = base;
+    if (part > 0) return;
+#pragma unroll
+    for (int o = 0; o < KG - 1; ++o) {
+      const float2 other = s_join[(o * W + wave) * 64 + lane];
+      const float base = fmaxf(state.base, other.x);
+      const float mine = exp2_fast(state.base - base), theirs = exp2_fast(other.x - base);
+      add_acc<DC>(at + o * W * kArea, acc, mine, theirs, lane);
+      sum = fmaf(other.y, theirs, sum * mine);
+      state.base = base;
+    }
   }
   if constexpr (WINDOW) {
     const uint64_t odd = odd_rows<DC>(acc, there && __builtin_isfinite(sum));
@@ -376,11 +391,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   constexpr int kThreads = DP / 4, kRows = 32 * W;
   const int group = a.heads / a.kv_heads, parts = a.cut.parts;
   const Share share = tile_share(a.cut, blockIdx.x);
-  int tile;
-  const int item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
+  int item, tile, nq;
   int64_t q0;
-  int nq;
-  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+  if constexpr (WINDOW) {
+    const Item it = find_rows<false>(a, a.window, group, kRows, share.slot);
+    item = it.index, tile = it.tile, q0 = it.q0, nq = it.nq;
+  } else {
+    item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
+    item_rows(a.q_offsets, a.nq, item, &q0, &nq);
+  }
   const int rows = nq * group;
   const RowMap qmap{q0, share.head * group, group};
   const Heads<D> out = heads_of<D>(a.out);
@@ -431,14 +450,80 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   if (a.lse != nullptr && c == 0) a.lse[qmap.stat((int)row, a.heads)] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
 }
 
+// The same for few rows in many parts: a workgroup a row (blockIdx.y) of a tile of 32, its parts shared by groups
+// of DP / 4 threads, joined through LDS in order.
+template <DT D, int DP> __global__ __launch_bounds__(256) void attention_join_rows_kernel(FwdArgs a) {
+  constexpr int kThreads = DP / 4, kGroups = 256 / kThreads;
+  __shared__ float4 s_part[256];
+  __shared__ float2 s_state[kGroups];
+  const int group = a.heads / a.kv_heads, parts = a.cut.parts;
+  const Share share = tile_share(a.cut, blockIdx.x);
+  const Item it = find_rows<false>(a, a.window, group, 32, share.slot);
+  const int64_t row = (int64_t)it.tile * 32 + blockIdx.y;
+  if (row >= (int64_t)it.nq * group) return;
+  const int c = threadIdx.x % kThreads * 4, mine = threadIdx.x / kThreads;
+  const int64_t first = (int64_t)share.place * 32 + blockIdx.y;
+  constexpr int kBatch = 8;
+  float base = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](float2 st, float4 p, bool some) {  // (base has been raised to st.x)
+    const float w = some ? exp2_fast(st.x - base) : 0.f;
+    sum = fmaf(w, some ? st.y : 0.f, sum);
+    o.x = fmaf(w, some ? p.x : 0.f, o.x);
+    o.y = fmaf(w, some ? p.y : 0.f, o.y);
+    o.z = fmaf(w, some ? p.z : 0.f, o.z);
+    o.w = fmaf(w, some ? p.w : 0.f, o.w);
+  };
+  const auto raise = [&](float top) {
+    const float shrink = exp2_fast(base - top);
+    base = top;
+    sum *= shrink;
+    o = make_float4(o.x * shrink, o.y * shrink, o.z * shrink, o.w * shrink);
+  };
+  for (int s0 = mine; s0 < parts; s0 += kBatch * kGroups) {
+    float2 st[kBatch];
+    float4 p[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t at = first + (int64_t)min(s0 + i * kGroups, parts - 1) * 32;
+      st[i] = a.state[at];
+      p[i] = *reinterpret_cast<const float4*>(a.part + at * DP + c);
+    }
+    float top = base;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, st[i].x);
+    if (top == -INFINITY) continue;
+    raise(top);
+    // (a share without keys has a sum of 0 and wrote no part)
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) add(st[i], p[i], s0 + i * kGroups < parts && st[i].y != 0.f);
+  }
+  s_part[threadIdx.x] = o;
+  if (c == 0) s_state[mine] = make_float2(base, sum);
+  __syncthreads();
+  if (mine != 0) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) {
+    const float2 st = s_state[k];
+    if (st.y == 0.f) continue;  // (no parts, or none with keys)
+    raise(fmaxf(base, st.x));
+    add(st, s_part[k * kThreads + threadIdx.x], true);
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const RowMap qmap{it.q0, share.head * group, group};
+  if (c < a.head_dim) store4<D>(qmap.at<D>(heads_of<D>(a.out), (int)row) + c, o.x * f, o.y * f, o.z * f, o.w * f);
+  if (a.lse != nullptr && c == 0) a.lse[qmap.stat((int)row, a.heads)] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+}
+
 template <DT D, int DC, int W, int KG, int CUT, bool WINDOW> hipError_t launch_tiles(const FwdArgs& a, hipStream_t stream) {
-  constexpr int KEYS = D == DT::F32 ? 32 : 64, OCC = D == DT::F32 ? 1 : DC <= 64 && KG == 1 && CUT == kNoCut ? 3 : 2;
+  constexpr int KEYS = D == DT::F32 || W == 1 ? 32 : 64;
+  constexpr int OCC = D == DT::F32 || (W == 1 && DC > 64) ? 1 : DC <= 64 && KG == 1 && CUT == kNoCut ? 3 : 2;
   const dim3 grid = CUT == kNoCut ? dim3((unsigned)a.cut.slots, (unsigned)a.kv_heads) : dim3((unsigned)cut_blocks(a.cut));
   attention_forward_kernel<D, DC, W, KG, KEYS, OCC, CUT, WINDOW><<<grid, KG * W * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <DT D, int DC, int W, int CUT, bool WINDOW> Status launch_cut(FwdArgs a, hipStream_t stream) {
+template <DT D, int DC, int W, int CUT, bool WINDOW, int KG = 1> Status launch_cut(FwdArgs a, hipStream_t stream) {
   constexpr int DP = tile_width(DC);
   int dev = 0;
   SUBM_HIP_TRY(hipGetDevice(&dev));
@@ -449,9 +534,34 @@ template <DT D, int DC, int W, int CUT, bool WINDOW> Status launch_cut(FwdArgs a
   if (!st.ok()) return st;
   a.part = static_cast<float*>(scratch);
   a.state = reinterpret_cast<float2*>(a.part + rows * DP);
-  SUBM_HIP_TRY((launch_tiles<D, DC, W, 1, CUT, WINDOW>(a, stream)));
+  SUBM_HIP_TRY((launch_tiles<D, DC, W, KG, CUT, WINDOW>(a, stream)));
+  if constexpr (W == 1) {
+    attention_join_rows_kernel<D, DP><<<dim3((unsigned)a.cut.cut, (unsigned)std::min<int64_t>(32, a.nq * (a.heads / a.kv_heads))), 256, 0, stream>>>(a);
+    SUBM_HIP_TRY(hipGetLastError());
+    return Status{};
+  }
   attention_join_kernel<D, DP, W, WINDOW><<<dim3((unsigned)a.cut.cut, 32 * W * (DP / 4) / 256), 256, 0, stream>>>(a);
   SUBM_HIP_TRY(hipGetLastError());
+  return Status{};
+}
+
+// Windows with few rows an item (single tokens of grouped heads): tiles of 32 rows, which one wave holds, and KG
+// waves that take every KG-th 32 keys.  Kernel and join, against tiles of 128 rows: one token, 4 / 1 heads of 128,
+// 60,000 keys: 19 and 41 us; 3 tokens, 12 heads of 64, 3,000 keys: 15 and 16; 8 tokens, 4 heads of 128, 2,000 keys,
+// float32: 39 and 52; 8 tokens, 16 / 4 heads of 128, 4,096 keys each: 22 both, of which 59 MB take 11: a step's loads
+// have one step's time to arrive, and with one wave's rows that is less than memory takes.  At 128 channels two
+// waves a workgroup where there are many items (17 tokens, 16 / 4 heads, 8,000 keys: 44 us, 52 with four).
+template <DT D, int DC, int KG> Status launch_few(FwdArgs a, int64_t rows, hipStream_t stream) {
+  constexpr int kTileBytes = KG * 4 * 32 * kRowBytes<D, tile_width(DC)>, kResident = 256 * (kTileBytes > 65536 ? 1 : 2);
+  const int64_t slots = rows / 32 + a.items, walked = a.window.walked(a.nk / a.items, 32);
+  constexpr int kLeast = D == DT::F32 ? 64 : 128, kWhole = D == DT::F32 ? 64 : 512;
+  const int64_t parts = walked <= kWhole ? 1 : std::min<int64_t>(kResident / ((int64_t)a.items * a.kv_heads), walked / kLeast);
+  if (parts > 1) {
+    a.cut = Cut{(int)slots, 0, (int)(slots * a.kv_heads), (int)parts, parts % 8 == 0 || 8 % parts == 0};
+    return launch_cut<D, DC, 1, kCutAll, true, KG>(a, stream);
+  }
+  a.cut = Cut{(int)slots, (int)(slots * a.kv_heads), 0, 1, false};
+  SUBM_HIP_TRY((launch_tiles<D, DC, 1, KG, kNoCut, true>(a, stream)));
   return Status{};
 }
 
@@ -466,7 +576,15 @@ Status launch(FwdArgs a, hipStream_t stream) {
   const int64_t rows = a.nq * (a.heads / a.kv_heads), spare = (int64_t)a.items * a.kv_heads;
   // (of a window: those of a tile)
   const int64_t keys = WINDOW ? a.window.walked(a.nk / a.items, 128 / (a.heads / a.kv_heads)) : a.nk / a.items;
-  if constexpr (WINDOW) a.window.runs = a.window.in_runs(a.nk / a.items, a.heads / a.kv_heads);
+  if constexpr (WINDOW) {
+    a.window.runs = a.window.in_runs(a.nk / a.items, a.heads / a.kv_heads);
+    // Single tokens and the like: a wave holds an item's rows, and the waves of a workgroup share its keys.
+    if (rows <= 32 * (int64_t)a.items) {
+      if constexpr (D == DT::F32) return launch_few<D, DC, 2>(a, rows, stream);
+      else if constexpr (tile_width(DC) == 64) return launch_few<D, DC, 4>(a, rows, stream);
+      else return spare < kUnits / 4 ? launch_few<D, DC, 4>(a, rows, stream) : launch_few<D, DC, 2>(a, rows, stream);
+    }
+  }
   // float32 scores take 8 times as long, so its parts may be short.
   constexpr int kShare = D == DT::F32 ? 32 : WINDOW ? 256 : 512;
   if constexpr (kWide && !WINDOW) {

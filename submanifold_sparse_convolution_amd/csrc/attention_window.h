@@ -46,6 +46,60 @@ struct Window {
   bool in_runs(int64_t keys, int group) const { return group == 1 && (left + right) * 2 < keys; }
 };
 
+// ------------------------------------------------------------------ the item of a tile
+//
+// A workgroup of a window has little to do, and a chain of dependent loads before it (a search through the
+// offsets, then the item's) is a good part of its time.  A wave therefore looks at 64 items at once, with
+// everything of the item in flight at the same time.
+
+struct Item {
+  int index, tile;
+  int64_t q0, k0;
+  int nq, nk;
+};
+
+__device__ __forceinline__ int64_t lane_value64(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// find_item and item_rows of slot `slot` in the tiling of the queries (BY_KEYS: of the keys) by `block` packed
+// rows, in one; every lane of the wave calls it.
+template <bool BY_KEYS, typename Args>
+__device__ __forceinline__ Item find_rows(const Args& a, const Window& w, int group, int block, int64_t slot) {
+  const int lane = threadIdx.x & 63;
+  const int64_t* by = BY_KEYS ? a.k_offsets : a.q_offsets;
+  const int64_t total = BY_KEYS ? a.nk : a.nq;
+  const auto start = [&](int64_t o, int b) { return (o < 0 ? 0 : o > total ? total : o) * group / block + b; };
+  int first = 0, count = a.items;  // the item is one of first .. first + count - 1
+  while (count > 64) {
+    const int stride = (count + 63) / 64, at = lane * stride;
+    const bool before = at < count && start(by[first + min(at, count - 1)], first + at) <= slot;
+    const int n = max(1, (int)__popcll(__builtin_amdgcn_ballot_w64(before)));
+    first += (n - 1) * stride;
+    count = min(stride, count - (n - 1) * stride);
+  }
+  const int mine = first + min(lane, count - 1);
+  const int64_t q_from = a.q_offsets[mine], q_to = a.q_offsets[mine + 1], k_from = a.k_offsets[mine], k_to = a.k_offsets[mine + 1];
+  const int64_t there = w.k_lengths != nullptr ? w.k_lengths[mine] : INT64_MAX;
+  const int64_t at = start(BY_KEYS ? k_from : q_from, mine);
+  const int n = max(1, (int)__popcll(__builtin_amdgcn_ballot_w64(lane < count && at <= slot)));
+  const auto rows = [&](int64_t from, int64_t to, int64_t most, int64_t* first_row, int* number) {
+    const int64_t s = lane_value64(from, n - 1), e = lane_value64(to, n - 1);
+    *first_row = s < 0 ? 0 : s > most ? most : s;
+    *number = (int)((e < *first_row ? *first_row : e > most ? most : e) - *first_row);
+  };
+  Item item;
+  item.index = first + n - 1;
+  const int64_t t = slot - lane_value64(at, n - 1);
+  item.tile = t < 0 ? INT32_MAX / block : (int)t;  // (only for offsets that do not rise: no such rows)
+  rows(q_from, q_to, a.nq, &item.q0, &item.nq);
+  rows(k_from, k_to, a.nk, &item.k0, &item.nk);
+  const int64_t most = lane_value64(there, n - 1);
+  item.nk = most < 0 ? 0 : most < item.nk ? (int)most : item.nk;
+  return item;
+}
+
 // Host: plan_cut for windows, whose last tiles stay whole (in parts they measured the same).  `resident`: workgroups
 // that the machine holds.  Where most of an item is seen the longest tile takes twice the mean, and few tiles
 // leave compute units that wait for it: then in at least four parts (three and six, which the XCDs do not share
@@ -150,7 +204,7 @@ struct RowView {
   template <int KB, typename Hide>
   __device__ __forceinline__ void mask(int key, int end, int lane, const Hide& hide) const {
     const int first = key + 4 * (lane >> 5);
-    if (key < sinks) {
+    if (key < sinks || end <= key) {  // (a part's tiles may end before the window does)
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
