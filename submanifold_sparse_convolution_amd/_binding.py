@@ -839,22 +839,30 @@ def sparse_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
     return out, dgamma, dbeta
 
 
+def _alike(t, shape, like, what):
+    """_vector of a tensor's dtype and device, with few attribute reads."""
+    if isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
+        return t.data_ptr()
+    return _vector(t, tuple(shape), like.dtype, like.device, what)
+
+
 def _rms_norm_args(x, gamma, residual, total, stats, stream):
     """(rows, channels, dtype code, pointers of gamma and residual, total and its pointer, rstd and its)."""
     n, c, code = _matrix(x, "x")
-    g = None if gamma is None else _vector(gamma, (c,), x.dtype, x.device, "gamma")
-    if residual is None:
-        r = None
-        t = None if total is None else _vector(total, (n, c), x.dtype, x.device, "total")
-    else:
-        r = _vector(residual, (n, c), x.dtype, x.device, "residual")
+    g = r = t = rstd = rstd_ptr = None
+    if gamma is not None:
+        g = _alike(gamma, (c,), x, "gamma")
+    if residual is not None:
+        r = _alike(residual, x.shape, x, "residual")
         if total is None:
             total = _empty_like(x, stream)
             t = total.data_ptr()
-        else:
-            t = _vector(total, (n, c), x.dtype, x.device, "total")
-    rstd = _empty((n,), torch.float32, x.device, stream) if stats else None
-    return n, c, code, g, r, total, t, rstd, None if rstd is None else rstd.data_ptr()
+    if total is not None and t is None:
+        t = _alike(total, x.shape, x, "total")
+    if stats:
+        rstd = _empty((n,), torch.float32, x.device, stream)
+        rstd_ptr = rstd.data_ptr()
+    return n, c, code, g, r, total, t, rstd, rstd_ptr
 
 
 def sparse_rms_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
@@ -868,7 +876,7 @@ def sparse_rms_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, 
         out = _empty_like(x, stream)
         y = out.data_ptr()
     else:
-        y = _vector(out, (n, c), x.dtype, x.device, "out")
+        y = _alike(out, x.shape, x, "out")
     _run("sparse_rms_norm_forward", x.get_device(), stream, x.data_ptr(), r, n, c, code, g, eps, y, t, rstd_ptr)
     return out, total, rstd
 
@@ -895,15 +903,15 @@ def sparse_rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, rstd: torch.
     n, c, code = _matrix(total, "total")
     if dy is None or rstd is None:
         raise ValueError("dy and rstd are required")
-    dy_ptr = _vector(dy, (n, c), total.dtype, total.device, "dy")
+    dy_ptr = _alike(dy, total.shape, total, "dy")
     r = _vector(rstd, (n,), torch.float32, total.device, "rstd")
-    g = None if gamma is None else _vector(gamma, (c,), total.dtype, total.device, "gamma")
-    dt = None if dtotal is None else _vector(dtotal, (n, c), total.dtype, total.device, "dtotal")
+    g = None if gamma is None else _alike(gamma, (c,), total, "gamma")
+    dt = None if dtotal is None else _alike(dtotal, total.shape, total, "dtotal")
     if out is None:
         out = _empty_like(total, stream)
         dx = out.data_ptr()
     else:
-        dx = _vector(out, (n, c), total.dtype, total.device, "out")
+        dx = _alike(out, total.shape, total, "out")
     dgamma = _empty((c,), total.dtype, total.device, stream) if weight_grads else None
     _run("sparse_rms_norm_backward", total.get_device(), stream, dy_ptr, total.data_ptr(), dt, n, c, code, g, r, dx,
          None if dgamma is None else dgamma.data_ptr())
@@ -928,7 +936,7 @@ def sparse_embedding_forward(table: torch.Tensor, tokens: torch.Tensor, scale: f
         out = _empty((n, c), table.dtype, table.device, stream)
         y = out.data_ptr()
     else:
-        y = _vector(out, (n, c), table.dtype, table.device, "out")
+        y = _alike(out, (n, c), table, "out")
     _run("sparse_embedding_forward", table.get_device(), stream, table.data_ptr(), rows, c, code, t, size, n, scale, y)
     return out
 
@@ -946,7 +954,7 @@ def sparse_embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, rows: in
         out = _empty((rows, c), dout.dtype, dout.device, stream)
         d = out.data_ptr()
     else:
-        d = _vector(out, (rows, c), dout.dtype, dout.device, "out")
+        d = _alike(out, (rows, c), dout, "out")
     _run("sparse_embedding_backward", dout.get_device(), stream, dout.data_ptr(), rows, c, code, t, size, n, scale, d)
     return out
 
