@@ -126,6 +126,17 @@ def test_machines_full_of_tiles(dtype, ql, kl, heads, kv_heads, d, window):
     check(*make(ql, kl, heads, kv_heads, d, dtype, 16), offsets(ql), offsets(kl), dtype, window, heads=sorted({0, kv_heads // 2, kv_heads - 1}))
 
 
+@pytest.mark.parametrize("items", [63, 64, 65, 130, 4500])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_items(dtype, items):
+    # the search through the offsets goes 64 items at a time
+    rng = np.random.default_rng(items)
+    kl = rng.integers(0, 9, items)
+    ql = np.minimum(rng.integers(0, 4, items), kl + 1)
+    q, k, v, g = make([int(ql.sum())], [int(kl.sum())], 2, 1, 32, dtype, items)
+    check(q, k, v, g, offsets(ql), offsets(kl), dtype, (3, 0, 1))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_open_windows_are_the_whole_item(dtype):
     ql, kl = [70, 3, 200], [90, 3, 180]
@@ -222,6 +233,36 @@ def test_hidden_values_do_not_matter(dtype, window, n, d):
         near(back[1], 3, ~seen[i], f"row {i} dk")
         near(back[2], 4, ~seen[i], "dv")
         assert not torch.isfinite(back[2][torch.from_numpy(seen[i]).to(DEV)][:, :, 1:3]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [(40, 0, 4), (None, 0, 0), (700, 0, 4)])
+def test_hidden_values_beside_few_rows(dtype, d, window):
+    # a few tokens after long caches, whose older keys and values hold anything
+    ql, kl = [5, 1, 8], [900, 2100, 64]
+    q, k, v, g = make(ql, kl, 4, 1, d, dtype, 14)
+    qo, ko = offsets(ql), offsets(kl)
+    for b in range(3):
+        last = ref.window_mask(ql[b], kl[b], *window)
+        for j in np.flatnonzero(~last.all(axis=0)):  # some row does not see it
+            if not last[:, j].any() or last[:, j].sum() < ql[b] and j % 2:
+                k[ko[b] + j, :, 1], v[ko[b] + j, :, 2] = float("nan"), float("inf")
+    out, lse = sc.sparse_window_attention_forward(q, k, v, on_device(qo), on_device(ko), *window)
+    a = [f64(t) for t in (q, k, v)]
+    clean = [a[0], np.nan_to_num(a[1], nan=0.0), np.nan_to_num(a[2], posinf=0.0)]
+    want, wlse = ref.window_attention(*clean, qo, ko, d ** -0.5, *window)
+    bound, blse = ref.window_attention_error_bounds(*clean, qo, ko, d ** -0.5, U[dtype], TINY[dtype], 0.0 if dtype == "f32" else U[dtype], None, *window)
+    odd = ~np.isfinite(a[2]).all(axis=(1, 2))
+    for b in range(3):
+        seen = ref.window_mask(ql[b], kl[b], *window)
+        for i in range(ql[b]):
+            row = slice(qo[b] + i, qo[b] + i + 1)
+            if (seen[i] & odd[ko[b]:ko[b + 1]]).any():
+                assert not torch.isfinite(out[row]).all()
+            else:
+                within(out[row], want[row], bound[row] + TINY[dtype], f"item {b} row {i} out")
+                within(lse[row], wlse[row], blse[row], "lse")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
