@@ -112,17 +112,19 @@ __device__ __forceinline__ void forward_again(f32x16_t (&acc)[DC / 32], uint64_t
   }
   for (; odd != 0; odd &= odd - 1) {
     const int l = __builtin_ctzll(odd), row = first + wave * 32 + l, p = row / group + nk - nq;
-    const typename Elem<D>::T* qr = qmap.at<D>(q, row);
+    if (!hidden_odd<D>(a.window, walk, p, nk, vp, v.row, a.head_dim, lane)) continue;
+    const float2 qr = row_pair<D>(qmap.at<D>(q, row), a.head_dim, lane);
     const float b = lane_value(base, l);
+    const float2 was = take_row<DC>(acc, l, a.head_dim, lane);
     float2 o = make_float2(0.f, 0.f);
-    for (int t = 0; t < walk.tiles; ++t)
+    for (int t = 0; t < walk.tiles && still_finite(was, o); ++t)
       for (int j = walk.key(t); j < min(walk.key(t) + KEYS, walk.end(t)); ++j) {
         if (!a.window.sees(p, j)) continue;
-        const float s = row_dot<D>(qr, kp + (int64_t)j * k.row, a.head_dim, lane);
+        const float s = pair_dot(qr, row_pair<D>(kp + (int64_t)j * k.row, a.head_dim, lane));
         const float e = exp2_fast(fmaf(s, a.scale < 0.f ? -c : c, -b));
-        add_scaled<D>(o, to_float<D>(from_float<D>(e)), vp + (int64_t)j * v.row, a.head_dim, lane);
+        add_scaled(o, to_float<D>(from_float<D>(e)), row_pair<D>(vp + (int64_t)j * v.row, a.head_dim, lane));
       }
-    put_row<DC>(acc, o, l, lane);
+    put_row<DC>(acc, mended(was, o), l, lane);
   }
 }
 
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     // steps without any: what it holds of such tiles is masked, and their p is 0, before a step reads it.  At 64
     // channels, where exponentials bound (four items, 9,371 tokens, 12 heads, 256 keys each way: 54 -> 44 us), and
     // whole tiles alone: elsewhere the branch costs as much (24,576 tokens, 16 heads of 128: 431 us, 437 with it).
-    constexpr bool kSkip = WINDOW && D != DT::F32 && DP == 64 && KG == 1 && CUT == kNoCut;
+    constexpr bool kSkip = WINDOW && KG == 1 && (D == DT::F32 || (DP == 64 && CUT == kNoCut));
     bool was = false, now = true;
     if constexpr (kSkip) now = view.sees_any(walk.key(0), KEYS, walk.end(0));
     const auto step = [&](int t, int slot, f32x16_t (&s)[KB], f32x16_t (&next)[KB]) {

@@ -148,9 +148,17 @@ template <DT D> __global__ __launch_bounds__(256) void attention_norm_kernel(Bwd
 }
 
 // The rows `odd` of a wave's dq, or the keys `odd` of its dk and dv, one by one (see attention_window.h), from the
-// kernel's arguments on.
+// kernel's arguments and what was stored on, so that the accumulators need not outlive their store.
+template <DT D> __device__ __forceinline__ void put_pair(typename Elem<D>::T* row, float2 o, int head_dim, int lane) {
+  if (2 * lane >= head_dim) return;
+  row[2 * lane] = from_float<D>(o.x);
+  row[2 * lane + 1] = from_float<D>(o.y);
+}
+
 template <DT D, int DC, int W, int CUT>
-__device__ __forceinline__ void dq_again(f32x16_t (&acc)[DC / 32], uint64_t odd, float base, float d, float unit, int wave, int lane) {
+__device__ __forceinline__ void dq_again(uint64_t odd, float base, float d, float unit, int wave, int lane) {
+  constexpr DT S = CUT == kNoCut ? D : DT::F32;  // of what was stored
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
   const BwdArgs a = fresh_args<BwdArgs>();
   const int group = a.heads / a.kv_heads;
   const Share share = window_share<CUT>(a.q_cut, a.window, true);
@@ -174,69 +182,124 @@ __device__ __forceinline__ void dq_again(f32x16_t (&acc)[DC / 32], uint64_t odd,
   }
   for (; odd != 0; odd &= odd - 1) {
     const int l = __builtin_ctzll(odd), row = first + wave * 32 + l, p = row / group + nk - nq;
-    const typename Elem<D>::T *qr = qmap.at<D>(heads_of<D>(a.q), row), *gr = qmap.at<D>(heads_of<D>(a.dout), row);
+    if (!hidden_odd<D>(a.window, walk, p, nk, kp, k.row, a.head_dim, lane)) continue;
+    const float2 qr = row_pair<D>(qmap.at<D>(heads_of<D>(a.q), row), a.head_dim, lane);
+    const float2 gr = row_pair<D>(qmap.at<D>(heads_of<D>(a.dout), row), a.head_dim, lane);
     const float b = lane_value(base, l), dr = lane_value(d, l), u = lane_value(unit, l);
+    typename Elem<S>::T* stored;
+    if constexpr (CUT == kNoCut) stored = qmap.at<D>(heads_of<D>(a.dq), row);
+    else stored = a.dq_part + ((int64_t)share.place * 32 * W + wave * 32 + l) * tile_width(DC);
+    const float2 was = row_pair<S>(stored, a.head_dim, lane);
     float2 o = make_float2(0.f, 0.f);
-    for (int t = 0; t < walk.tiles; ++t)
+    for (int t = 0; t < walk.tiles && still_finite(was, o); ++t)
       for (int j = walk.key(t); j < min(walk.key(t) + kStep, walk.end(t)); ++j) {
         if (!a.window.sees(p, j)) continue;
-        const typename Elem<D>::T *kr = kp + (int64_t)j * k.row, *vr = vp + (int64_t)j * v.row;
-        const float e = exp2_fast(fmaf(row_dot<D>(qr, kr, a.head_dim, lane), a.scale * kLog2e, -b)) *
-                        (row_dot<D>(gr, vr, a.head_dim, lane) - dr) * u;
-        add_scaled<D>(o, to_float<D>(from_float<D>(e)), kr, a.head_dim, lane);
+        const float2 kr = row_pair<D>(kp + (int64_t)j * k.row, a.head_dim, lane);
+        const float2 vr = row_pair<D>(vp + (int64_t)j * v.row, a.head_dim, lane);
+        const float e = exp2_fast(fmaf(pair_dot(qr, kr), a.scale * kLog2e, -b)) * (pair_dot(gr, vr) - dr) * u;
+        add_scaled(o, to_float<D>(from_float<D>(e)), kr);
       }
-    put_row<DC>(acc, o, l, lane);
+    const float f = a.scale / u;
+    put_pair<S>(stored, mended(was, make_float2(o.x * f, o.y * f)), a.head_dim, lane);
   }
 }
 
-template <DT D, int DC, int W, int CUT, bool SINKS>
-__device__ __forceinline__ void dkv_again(f32x16_t (&dk)[DC / 32], f32x16_t (&dv)[DC / 32], uint64_t odd, float unit, int wave, int lane) {
-  const BwdArgs a = fresh_args<BwdArgs>();
-  const int group = a.heads / a.kv_heads;
+// Of key l of a wave of the dk and dv kernel: the query rows that this workgroup walks for it, and those that see it.
+struct KeyRows {
+  int share_head, share_place, group, key;
+  int64_t q0, k0;
+  int begin, end, from, to;
+};
+template <DT D, int W, int CUT, bool SINKS> __device__ __forceinline__ KeyRows key_rows(const BwdArgs& a, int wave, int l) {
+  KeyRows r;
+  r.group = a.heads / a.kv_heads;
   const Share share = !SINKS ? window_share<CUT>(a.k_cut, a.window, false) : share_of<CUT>(a.k_cut, blockIdx.x);
+  r.share_head = share.head;
+  r.share_place = SINKS ? share.slot : share.place;
   int tile, chunk = 0;
-  const int item = SINKS ? find_item(a.q_offsets, a.nq, a.items, group, a.sink_rows, share.slot, &chunk)
+  const int item = SINKS ? find_item(a.q_offsets, a.nq, a.items, r.group, a.sink_rows, share.slot, &chunk)
                          : find_item(a.k_offsets, a.nk, a.items, 1, 32 * W, share.slot, &tile);
   if constexpr (SINKS) tile = blockIdx.z;
-  int64_t q0, k0;
   int nq, nk;
-  item_rows(a.q_offsets, a.nq, item, &q0, &nq);
-  item_rows(a.k_offsets, a.nk, item, &k0, &nk);
-  const int shift = nk - nq;
-  const RowMap qmap{q0, share.head * group, group}, kmap{k0, share.head, 1};
-  const float* norm = a.norm + share.head * (a.nq * group) + q0 * group;
-  const float* delta = a.delta + share.head * (a.nq * group) + q0 * group;
-  const float f = D == DT::F16 ? unit / 32768.f : 1.f;
-  // the rows of this workgroup: of the chunk, or of its part of those that the tile's keys are seen by
-  int begin = 0, end = nq * group;
+  item_rows(a.q_offsets, a.nq, item, &r.q0, &nq);
+  item_rows(a.k_offsets, a.nk, item, &r.k0, &nk);
+  const int shift = nk - nq, first = tile * 32 * W, last = min(SINKS ? min(nk, a.window.sinks) : nk, first + 32 * W) - 1;
+  int unused;
+  a.window.rows(SINKS ? first : max(first, min(a.window.sinks, last)), SINKS, nq, shift, r.group, &r.begin, &unused);
+  a.window.rows(last, SINKS, nq, shift, r.group, &unused, &r.end);
   if constexpr (SINKS) {
-    begin = chunk * a.sink_rows;
-    end = (int)min((int64_t)end, (int64_t)begin + a.sink_rows);
+    r.begin = max(r.begin, chunk * a.sink_rows);
+    r.end = (int)min((int64_t)r.end, (int64_t)(chunk + 1) * a.sink_rows);
   } else if constexpr (CUT != kNoCut) {
-    const int last = min(nk, (tile + 1) * 32 * W) - 1;
-    int unused;
-    a.window.rows(max(tile * 32 * W, min(a.window.sinks, last)), false, nq, shift, group, &begin, &unused);
-    a.window.rows(last, false, nq, shift, group, &unused, &end);
-    int steps = (max(end - begin, 0) + kStep - 1) / kStep;
-    begin += part_steps(a.k_cut, share.part, &steps) * kStep;
-    end = min(end, begin + steps * kStep);
+    int steps = (max(r.end - r.begin, 0) + kStep - 1) / kStep;
+    r.begin += part_steps(a.k_cut, share.part, &steps) * kStep;
+    r.end = min(r.end, r.begin + steps * kStep);
   }
-  for (; odd != 0; odd &= odd - 1) {
-    const int l = __builtin_ctzll(odd), j = tile * 32 * W + wave * 32 + l;
-    if (!SINKS && j < a.window.sinks) continue;  // (not this kernel's)
-    const typename Elem<D>::T *kr = kmap.at<D>(heads_of<D>(a.k), j), *vr = kmap.at<D>(heads_of<D>(a.v), j);
-    int from, to;
-    a.window.rows(j, SINKS, nq, shift, group, &from, &to);
-    float2 ok = make_float2(0.f, 0.f), ov = ok;
-    for (int i = max(from, begin); i < min(to, end); ++i) {
-      const typename Elem<D>::T *qr = qmap.at<D>(heads_of<D>(a.q), i), *gr = qmap.at<D>(heads_of<D>(a.dout), i);
-      const float p = exp2_fast(fmaf(row_dot<D>(qr, kr, a.head_dim, lane), a.scale * kLog2e, -norm[i]));
-      const float e = p * (row_dot<D>(gr, vr, a.head_dim, lane) - delta[i]) * f;
-      add_scaled<D>(ov, to_float<D>(from_float<D>(p)), gr, a.head_dim, lane);
-      add_scaled<D>(ok, to_float<D>(from_float<D>(e)), qr, a.head_dim, lane);
+  r.key = first + wave * 32 + l;
+  a.window.rows(r.key, SINKS, nq, shift, r.group, &r.from, &r.to);
+  return r;
+}
+
+// (hidden_odd of attention_window.h, of the rows that do not see key l.  From the arguments on once more, as what it
+// and dkv_again need at once would not fit the scalar registers.)
+template <DT D, int W, int CUT, bool SINKS> __device__ __forceinline__ bool dkv_hidden_odd(int l, int wave, int lane) {
+  const BwdArgs a = fresh_args<BwdArgs>();
+  const KeyRows r = key_rows<D, W, CUT, SINKS>(a, wave, l);
+  if (!SINKS && r.key < a.window.sinks) return false;  // (not this kernel's)
+  const RowMap qmap{r.q0, r.share_head * r.group, r.group};
+  float z = 0.f;
+#pragma unroll 1
+  for (int i = r.begin; i < r.end; ++i) {
+    if (i >= r.from && i < r.to) {
+      i = r.to - 1;
+      continue;
     }
-    put_row<DC>(dk, ok, l, lane);
-    put_row<DC>(dv, ov, l, lane);
+    add_odd<D>(z, qmap.at<D>(heads_of<D>(a.q), i), a.head_dim, lane);
+    add_odd<D>(z, qmap.at<D>(heads_of<D>(a.dout), i), a.head_dim, lane);
+  }
+  return __builtin_amdgcn_ballot_w64(!(z == 0.f)) != 0;
+}
+
+template <DT D, int DC, int W, int CUT, bool SINKS> __device__ __forceinline__ void dkv_again(uint64_t odd, float unit, int wave, int lane) {
+  constexpr bool kPart = SINKS || CUT != kNoCut;
+  constexpr DT S = kPart ? DT::F32 : D;
+  constexpr int DP = tile_width(DC);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+  for (; odd != 0; odd &= odd - 1) {
+    const int l = __builtin_ctzll(odd);
+    if (!dkv_hidden_odd<D, W, CUT, SINKS>(l, wave, lane)) continue;
+    const BwdArgs a = fresh_args<BwdArgs>();
+    const KeyRows r = key_rows<D, W, CUT, SINKS>(a, wave, l);
+    const RowMap qmap{r.q0, r.share_head * r.group, r.group}, kmap{r.k0, r.share_head, 1};
+    const int64_t stats = r.share_head * (a.nq * r.group) + r.q0 * r.group;
+    const float f = D == DT::F16 ? unit / 32768.f : 1.f;
+    const float2 kr = row_pair<D>(kmap.at<D>(heads_of<D>(a.k), r.key), a.head_dim, lane);
+    const float2 vr = row_pair<D>(kmap.at<D>(heads_of<D>(a.v), r.key), a.head_dim, lane);
+    typename Elem<S>::T *dk, *dv;
+    if constexpr (SINKS) {
+      dk = a.sink_part + (((int64_t)r.share_head * a.sink_slots + r.share_place) * a.sink_keys + r.key) * 2 * DP;
+      dv = dk + DP;
+    } else if constexpr (kPart) {
+      const int64_t at = ((int64_t)r.share_place * 32 * W + wave * 32 + l) * DP;
+      dk = a.dk_part + at;
+      dv = a.dv_part + at;
+    } else {
+      dk = kmap.at<D>(heads_of<D>(a.dk), r.key);
+      dv = kmap.at<D>(heads_of<D>(a.dv), r.key);
+    }
+    const float2 was_k = row_pair<S>(dk, a.head_dim, lane), was_v = row_pair<S>(dv, a.head_dim, lane);
+    float2 ok = make_float2(0.f, 0.f), ov = ok;
+    for (int i = max(r.from, r.begin); i < min(r.to, r.end) && (still_finite(was_k, ok) || still_finite(was_v, ov)); ++i) {
+      const float2 qr = row_pair<D>(qmap.at<D>(heads_of<D>(a.q), i), a.head_dim, lane);
+      const float2 gr = row_pair<D>(qmap.at<D>(heads_of<D>(a.dout), i), a.head_dim, lane);
+      const float p = exp2_fast(fmaf(pair_dot(qr, kr), a.scale * kLog2e, -a.norm[stats + i]));
+      const float e = p * (pair_dot(gr, vr) - a.delta[stats + i]) * f;
+      add_scaled(ov, to_float<D>(from_float<D>(p)), gr);
+      add_scaled(ok, to_float<D>(from_float<D>(e)), qr);
+    }
+    const float fk = a.scale / unit, fv = D == DT::F16 ? 1.f / 32768.f : 1.f;
+    put_pair<S>(dk, mended(was_k, make_float2(ok.x * fk, ok.y * fk)), a.head_dim, lane);
+    put_pair<S>(dv, mended(was_v, make_float2(ov.x * fv, ov.y * fv)), a.head_dim, lane);
   }
 }
 
@@ -425,7 +488,14 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
   }
   if constexpr (WINDOW) {
     const uint64_t odd = odd_rows<DC>(acc, there && __builtin_isfinite(base) && __builtin_isfinite(d));
-    if (odd != 0) dq_again<D, DC, W, CUT>(acc, odd, base, d, unit, wave, lane);
+    if (there) {
+      if constexpr (CUT != kNoCut)
+        store_part<DC>(a.dq_part + ((int64_t)share.place * kRows + wave * 32 + (lane & 31)) * DP, acc, a.scale / unit, lane);
+      else
+        store_row<D, DC>(qmap.at<D>(heads_of<D>(a.dq), row), acc, a.scale / unit, a.head_dim, lane);
+    }
+    if (odd != 0) dq_again<D, DC, W, CUT>(odd, base, d, unit, wave, lane);
+    return;
   }
   if (!there) return;
   if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0))
@@ -450,7 +520,8 @@ __device__ __forceinline__ void load_stats(const float* p, int left, uint32_t ld
 // dk and dv of the own keys, over the query rows of all heads that share the key head, which
 // stream through LDS in tiles of 32.  Two waves a SIMD overlap each other's exponentials and
 // products.  At 128 channels in 16 bits the own rows of v stay in LDS: with the two accumulators
-// and k there is no room for them in 256 registers.
+// and k there is no room for them in 256 registers.  Windows at 64 channels park them too, where three workgroups
+// a compute unit have 168 (9,000 tokens, 6 heads, 2,048 keys: 205 us without, of k and v some in scratch memory, and 190).
 //
 // WINDOW: the rows from the first that sees the tile's first key to the last that sees its last, but not of
 // the sinks, which are left to the kernel with SINKS: 32 of those and a chunk of rows a workgroup (of one
@@ -459,7 +530,7 @@ template <DT D, int DC, int W, int OCC, int CUT, bool WINDOW, bool SINKS>
 __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   constexpr int DP = tile_width(DC), kKeys = 32 * W;
   constexpr int kTile = kStep * kRowBytes<D, DP>;
-  constexpr bool kParked = D != DT::F32 && DP == 128;
+  constexpr bool kParked = D != DT::F32 && (DP == 128 || (WINDOW && !SINKS && DC == 64));
   using Loader = TileLoader<D, DP, kStep, W>;
   using Parker = TileLoader<D, DP, kKeys, W>;
   // q, q, dout, dout, own v
@@ -524,6 +595,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
 #pragma unroll
     for (int w = 0; w < W; ++w) top = make_float2(fmaxf(top.x, s_peak[w].x), fmaxf(top.y, s_peak[w].y));
     unit = e_scale(top.x, top.y);
+    if constexpr (WINDOW) unit = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(unit)));
   }
   const float p_unit = D == DT::F16 ? 1.f / 32768.f : 1.f;
 
@@ -640,21 +712,35 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   }
   wait_vmcnt<0>();  // (the loads past the end)
   if constexpr (WINDOW) {
+    // (64 channels: what the lane's number gives is not kept over the loop)
+    const int own_lane = DP == 64 ? fresh_lane() : lane, key = tile * kKeys + wave * 32 + (own_lane & 31);
+    const bool there = key < nk;
     const uint64_t odd = odd_rows<DC>(dk, there) | odd_rows<DC>(dv, there);
-    if (odd != 0) dkv_again<D, DC, W, CUT, SINKS>(dk, dv, odd, unit, wave, lane);
-  }
-  if (!there) return;
-  if constexpr (SINKS) {
-    const int64_t at = (((int64_t)head * a.sink_slots + share.slot) * a.sink_keys + key) * 2 * DP;
-    store_part<DC>(a.sink_part + at, dk, a.scale / unit, lane);
-    store_part<DC>(a.sink_part + at + DP, dv, p_unit, lane);
+    if constexpr (SINKS) {
+      const int64_t at = (((int64_t)head * a.sink_slots + share.slot) * a.sink_keys + key) * 2 * DP;
+      if (there) {
+        store_part<DC>(a.sink_part + at, dk, a.scale / unit, own_lane);
+        store_part<DC>(a.sink_part + at + DP, dv, p_unit, own_lane);
+      }
+    } else if constexpr (CUT != kNoCut) {
+      const int64_t at = ((int64_t)share.place * kKeys + wave * 32 + (own_lane & 31)) * DP;
+      if (there) {
+        store_part<DC>(a.dk_part + at, dk, a.scale / unit, own_lane);
+        store_part<DC>(a.dv_part + at, dv, p_unit, own_lane);
+      }
+    } else if (there && key >= a.window.sinks) {
+      store_row<D, DC>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, own_lane);
+      store_row<D, DC>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, own_lane);
+    }
+    if (odd != 0) dkv_again<D, DC, W, CUT, SINKS>(odd, unit, wave, own_lane);
     return;
   }
+  if (!there) return;
   if (CUT == kCutAll || (CUT == kCutLast && share.part >= 0)) {
     const int64_t at = ((int64_t)share.place * kKeys + wave * 32 + (lane & 31)) * DP;
     store_part<DC>(a.dk_part + at, dk, a.scale / unit, lane);
     store_part<DC>(a.dv_part + at, dv, p_unit, lane);
-  } else if (!WINDOW || key >= a.window.sinks) {
+  } else {
     store_row<D, DC>(kmap.at<D>(heads_of<D>(a.dk), key), dk, a.scale / unit, a.head_dim, lane);
     store_row<D, DC>(kmap.at<D>(heads_of<D>(a.dv), key), dv, p_unit, a.head_dim, lane);
   }

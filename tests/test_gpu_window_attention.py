@@ -366,3 +366,34 @@ def test_no_rows():
     assert torch.equal(out, torch.zeros_like(k)) and torch.isneginf(lse).all()
     dq, dk, dv = sc.sparse_window_attention_backward(k, k, q, q, out, lse, ok, oq, 3, 0, 2)
     assert torch.equal(dq, torch.zeros_like(k)) and dk.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("window", [(255, 0, 4), (None, 0, 0), (100, 100, 0)])
+@pytest.mark.parametrize("bad", ["all", "v", "dout", "q"])
+def test_values_that_are_not_finite_everywhere(bad, window):
+    # where something non-finite is seen the results are, elsewhere they are what clean inputs give; the rows
+    # beside what is hidden are computed again, which many of them must not do over all that they see
+    n, heads, d = 2000, 2, 64
+    rng = np.random.default_rng(15)
+    q, k, v, g = (synth.round_to(rng.standard_normal((n, heads, d)), "bf16").to(DEV) for _ in range(4))
+    o = on_device([0, n])
+    clean_out, clean_lse = sc.sparse_window_attention_forward(q, k, v, o, None, *window)
+    clean = sc.sparse_window_attention_backward(g, q, k, v, clean_out, clean_lse, o, None, *window)
+    at = np.zeros(n, dtype=bool)
+    at[::1 if bad == "all" else 301] = True
+    where = torch.from_numpy(at).to(DEV)
+    mask = ref.window_mask(n, n, *window)
+    rows_hit, keys_hit = mask[:, at].any(1), mask[at].any(0)
+    seen_by_hit = mask[rows_hit].any(0)
+    for t in {"all": (q, k, v, g), "v": (v,), "dout": (g,), "q": (q,)}[bad]:
+        t[where, :, ::7] = float("nan") if bad != "v" else float("inf")
+    out, lse = sc.sparse_window_attention_forward(q, k, v, o, None, *window)
+    dq, dk, dv = sc.sparse_window_attention_backward(g, q, k, v, out, lse, o, None, *window)
+    odd = {"all": (rows_hit, rows_hit, seen_by_hit, seen_by_hit), "v": (rows_hit, rows_hit, seen_by_hit, ~seen_by_hit & False),
+           "dout": (~rows_hit & False, at, keys_hit, keys_hit), "q": (at, at, keys_hit, keys_hit)}[bad]
+    for got, want, hit, what in zip((out, dq, dk, dv), (clean_out, *clean), odd, ("out", "dq", "dk", "dv")):
+        finite = torch.isfinite(got).all(2).all(1).cpu().numpy()
+        assert np.array_equal(finite, ~hit), what
+        rows = torch.from_numpy(~hit).to(DEV)
+        near = np.abs(f64(got[rows]) - f64(want[rows])) <= 2 ** -6 * np.abs(f64(want[rows])).max(initial=1.0)  # (each is its clean value to roundings of 2^-8)
+        assert near.all(), what
