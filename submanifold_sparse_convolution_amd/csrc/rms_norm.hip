@@ -7,6 +7,10 @@
 //
 // Bound by HBM: a row is read once and stays in registers, spread over TPR lanes in 16-byte chunks,
 // from its loads to its stores.  The norm is of the float32 sum, not of its rounding that is stored.
+//
+// Measured: 135,826 rows of 1,024 channels, bf16, with a residual: to 8 bits in groups 176 us (973 MB, 5.5 TB/s),
+// backward with both gradients 207 us (1,113 MB, 5.4 TB/s); a 1 GiB copy reaches 5.49 TB/s.  4,099 rows of 675,
+// float32, backward: 10 us and 4 for the weight's gradient, latency; 450 rows of 768, f16: 3.7 us.
 #include <algorithm>
 #include <cmath>
 
