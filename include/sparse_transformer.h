@@ -286,8 +286,9 @@ int sparse_attention_backward(const subm_heads_t* dout, const subm_heads_t* q, c
  *                behind its tokens); values outside 0 .. its rows are taken as the nearest.  Rows past it are not read.
  * A query that sees no key (p + right < 0, or an item without keys) gets out = 0 and lse = -infinity.  A key or
  * value that a query does not see, NaN and infinities included, does not change the query's result (a tile in
- * which such a value meets other rows is computed again row by row, which is slow).  Only the tiles of keys
- * that some row of a block sees are read.  All other arguments, limits and errors are those of
+ * which such a value meets other rows is computed again row by row, which is slow; where a row
+ * that sees such a value itself is not finite, infinity and NaN may stand for each other).  Only the tiles
+ * of keys that some row of a block sees are read.  All other arguments, limits and errors are those of
  * sparse_attention_forward, and SUBM_ERR_INVALID_ARG for a negative left, right or sinks.
  */
 int sparse_window_attention_forward(const subm_heads_t* q, const subm_heads_t* k, const subm_heads_t* v, int64_t nq,

@@ -279,9 +279,10 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
       for (int i = 0; i < Elem<D>::kSize / 2; ++i) p[st].v[i] = make_uint4(0, 0, 0, 0);
     scores(0, s0);
     // WINDOW: whether the wave sees any key of tile t - 1 (was), t (now) and t + 1 (soon).  It leaves out the
-    // steps without any: what it holds of such tiles is masked, and their p is 0, before a step reads it.  At 64
-    // channels, where exponentials bound (four items, 9,371 tokens, 12 heads, 256 keys each way: 54 -> 44 us), and
-    // whole tiles alone: elsewhere the branch costs as much (24,576 tokens, 16 heads of 128: 431 us, 437 with it).
+    // steps without any: what it holds of such tiles is masked, and their p is 0, before a step reads it.  In
+    // float32, whose products are slow (2,000 tokens, 6 / 3 heads of 80, causal: 121 -> 110 us), and at 64 channels, where
+    // exponentials bound (four items, 9,371 tokens, 12 heads, 256 keys each way: 54 -> 44 us), of whole tiles alone:
+    // elsewhere the branch costs as much (24,576 tokens, 16 heads of 128: 431 us, 437 with it).
     constexpr bool kSkip = WINDOW && KG == 1 && (D == DT::F32 || (DP == 64 && CUT == kNoCut));
     bool was = false, now = true;
     if constexpr (kSkip) now = view.sees_any(walk.key(0), KEYS, walk.end(0));

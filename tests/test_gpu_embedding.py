@@ -138,3 +138,8 @@ def test_against_the_plain_oracle():
     d = sc.sparse_embedding_backward(torch.from_numpy(g).float().to(DEV), t, 8, 0.5)
     # float32 inputs (2^-24), at most 40 additions
     assert np.abs(f64(out) - ref.embedding(table, tok, 0.5)).max() < 1e-6 and np.abs(f64(d) - ref.embedding_grad(g, tok, 8, 0.5)).max() < 1e-5
+
+
+@pytest.mark.parametrize("n,rows,kind", [(1100000, 2 ** 20 + 5, "even"), (9000, 2 ** 21, "skewed"), (70000, 600000, "padded"), (1100000, 900, "one")])
+def test_longest_lists_and_tables(n, rows, kind):
+    check(n, 5, rows, "f32", kind)

@@ -397,3 +397,20 @@ def test_values_that_are_not_finite_everywhere(bad, window):
         rows = torch.from_numpy(~hit).to(DEV)
         near = np.abs(f64(got[rows]) - f64(want[rows])) <= 2 ** -6 * np.abs(f64(want[rows])).max(initial=1.0)  # (each is its clean value to roundings of 2^-8)
         assert near.all(), what
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("window", [(20, 0, 3), (None, 0, 0), (40, 11, 70)])
+@pytest.mark.parametrize("heads", [128, 7])
+def test_many_heads_a_key_head(dtype, window, heads):
+    ql, kl = [1, 3, 40, 0], [300, 5, 40, 9]
+    q, k, v, g = make(ql, kl, heads, 1, 16, dtype, 16)
+    check(q, k, v, g, offsets(ql), offsets(kl), dtype, window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1.5])
+@pytest.mark.parametrize("ql,kl", [([200, 3], [200, 90]), ([2, 1], [900, 400])])
+def test_scales(dtype, scale, ql, kl):
+    q, k, v, g = make(ql, kl, 2, 2, 48, dtype, 17)
+    check(q, k, v, g, offsets(ql), offsets(kl), dtype, (50, 0, 5), scale=scale)
