@@ -10,12 +10,12 @@
 // workgroup a bucket sorts its tokens by counting, stores where each row's begin, and zeros the rows without
 // any (a table of at most 1,024 rows has a bucket a row, and nothing is left to sort); (3) pieces of
 // consecutive sorted positions, the same work for all whatever the tokens' frequencies, sum their rows of
-// dout: a row with at most a piece of tokens is summed where it begins, longer ones leave float32 sums a piece,
+// dout: a row of a few tokens is summed where it begins, one of more in several pieces leaves float32 sums a piece,
 // (4) which are joined in order.
 //
 // Measured, gradient of 135,826 tokens, 1,024 channels, bf16, on the device: table of 65,536 rows, tokens evenly
 // spread: 5 + 12 + 15 + 84 + 5 us (382 MB in (3): 4.5 TB/s); a twelfth of them one token, half of the rows without
-// any: 5 + 12 + 42 + 105 + 7 (the one bucket's list, and 72 MB of zeros beside it); table of 100 rows: 5 + 10 +
+// any: 5 + 12 + 42 + 86 + 8 (the first bucket's list, a third of all, and 72 MB of zeros beside it); table of 100 rows: 5 + 10 +
 // 50 + 6 (5.3 TB/s).  4,099 tokens, 1,021 rows of 675 channels, float32: 10 + 8 + 4, all of it latency.  Lookup of 450
 // tokens, 768 channels, f16: 3 us.
 #include <algorithm>
@@ -338,6 +338,7 @@ struct Sums {
   int32_t* joins;      // long rows so far, then
   int2* join;          // (the piece they begin in, how many they lie in), in any order
   int rows, channels, piece;
+  int shortest;  // rows of more tokens, in several pieces, are long
   float scale;
 };
 
@@ -364,7 +365,7 @@ __global__ __launch_bounds__(256) void embedding_piece_kernel(Sums a) {
   int cur = a.row[first];
   const int final = a.row[end - 1];
   const int cur_from = a.start[cur], cur_to = a.start[cur + 1], final_from = a.start[final], final_to = a.start[final + 1];
-  const bool began = cur_from < first && cur_to - cur_from > a.piece, goes_on = final_to > end && final_to - final_from > a.piece;
+  const bool began = cur_from < first && cur_to - cur_from > a.shortest, goes_on = final_to > end && final_to - final_from > a.shortest;
   const int64_t from = cur_from < first && !began ? cur_to : first, to = goes_on ? end : final_to;
   if (goes_on && final_from >= first && lane == 0 && blockIdx.y == 0)
     a.join[atomicAdd(a.joins, 1)] = make_int2((int)id, (int)((final_to - 1) / a.piece - id + 1));
@@ -484,6 +485,9 @@ template <DT D> Status backward(Sort s, Sums a, hipStream_t stream) {
   // steps: 70 us, with pieces of 32 76, of 16 89).
   a.piece = 8;
   while (s.n / a.piece > (a.piece < 64 ? 2048 : 65536)) a.piece *= 2;
+  // Beside its own positions a piece sums a row that is not long to its end, and all wait for the piece with most: (3)
+  // of the skewed list above takes 106 us where a row is long from a piece's 64 tokens on, 86 from 16.
+  a.shortest = std::max(a.piece / 4, 8);
   const int64_t pieces = (s.n + a.piece - 1) / a.piece;
 
   int dev = 0;
