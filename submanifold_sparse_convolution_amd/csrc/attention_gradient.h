@@ -487,7 +487,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     product((tiles - 1) % 4, e);
   }
   if constexpr (WINDOW) {
-    const uint64_t odd = odd_rows<DC>(acc, there && __builtin_isfinite(base) && __builtin_isfinite(d));
+    // (a row without any key, whose log sum is -infinity, meets hidden ones alone: 0 is its gradient)
+    const uint64_t odd = odd_rows<DC>(acc, there && (base == -INFINITY || (__builtin_isfinite(base) && __builtin_isfinite(d))));
     if (there) {
       if constexpr (CUT != kNoCut)
         store_part<DC>(a.dq_part + ((int64_t)share.place * kRows + wave * 32 + (lane & 31)) * DP, acc, a.scale / unit, lane);
