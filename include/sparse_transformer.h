@@ -300,7 +300,8 @@ int sparse_window_attention_forward(const subm_heads_t* q, const subm_heads_t* k
 /*
  * sparse_window_attention_backward -- gradients of sparse_window_attention_forward without k_lengths: those of
  * sparse_attention_backward, each sum over the keys that a query sees or the queries that see a key.  A key
- * that no query sees gets dk = dv = 0.  The sinks' sums go through float32 partial results, one a chunk
+ * that no query sees gets dk = dv = 0, and a query that sees no key dq = 0; what a query does not see changes
+ * neither its dq nor, through it, other keys' gradients.  The sinks' sums go through float32 partial results, one a chunk
  * of query rows.
  */
 int sparse_window_attention_backward(const subm_heads_t* dout, const subm_heads_t* q, const subm_heads_t* k,

@@ -16,9 +16,10 @@ struct BwdArgs {
   const float* lse;
   float *norm, *delta;  // [kv_heads, nq * group]: log2 of each packed row's normaliser (less kF16Shift), and d
   // float16 only: [kv_heads, q_slots] the largest |dout| and bound of |dp - d| of each query block,
-  // and [kv_heads, v_slots] a bound of |v|_2 over each block of kNormKeys keys
-  float2* peak;
-  float* v_norm;
+  // and [kv_heads, v_slots] a bound of |v|_2 over each block of kNormKeys keys; with WINDOW also those of
+  // each packed row, [kv_heads, nq * group], and |v|_2 of each key, [kv_heads, nk]
+  float2 *peak, *row_peak;
+  float *v_norm, *key_norm;
   const int64_t *q_offsets, *k_offsets;
   int64_t nq, nk, q_slots, v_slots;
   int items, heads, kv_heads, head_dim;
@@ -75,6 +76,104 @@ template <int W> __device__ __forceinline__ float item_norm(const BwdArgs& a, in
   return v;
 }
 
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float2 larger(float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y)); }
+
+// Of values >= 0: the largest of the own lane and of those after it up to 31 (lanes 0 .. 31), or of those before it
+// from 32 on (lanes 32 .. 63), in VALU instructions.
+__device__ __forceinline__ float max_outwards(float v, int lane) {
+  float after = v, before = v;  // in rows of 16: lanes shifted down, and up
+  after = dpp_max<0x101>(after);
+  after = dpp_max<0x102>(after);
+  after = dpp_max<0x104>(after);
+  after = dpp_max<0x108>(after);
+  before = dpp_max<0x111>(before);
+  before = dpp_max<0x112>(before);
+  before = dpp_max<0x114>(before);
+  before = dpp_max<0x118>(before);
+  if (lane < 16) after = fmaxf(after, lane_value(after, 16));
+  if (lane >= 48) before = fmaxf(before, lane_value(before, 47));
+  return lane < 32 ? after : before;
+}
+__device__ __forceinline__ float2 max_outwards(float2 v, int lane) {
+  return make_float2(max_outwards(v.x, lane), max_outwards(v.y, lane));
+}
+__device__ __forceinline__ float max_of_wave(float v) { return lanes_max(v, 64); }
+__device__ __forceinline__ float2 max_of_wave(float2 v) { return make_float2(lanes_max(v.x, 64), lanes_max(v.y, 64)); }
+__device__ __forceinline__ float max_of_halves(float v) { return half_max(v); }
+__device__ __forceinline__ float2 max_of_halves(float2 v) { return make_float2(half_max(v.x), half_max(v.y)); }
+
+// The largest of `one` over the lane's own range [lo, hi), which rises from lane to lane of 0 .. 31 by at most
+// `step` at either end (lanes l and l + 32: the same); `whole`: the largest of each `block` of them.  What all
+// lanes' ranges share is read by the wave together; to it come each lane's first `step` values and those of the
+// lanes after it, and each lane's last and those of the lanes before it.  (A value may be read twice; loads of a
+// batch are in flight at once.)
+template <typename V>
+__device__ __forceinline__ V range_max(int lo, int hi, int step, int block, const V* one, const V* whole, int lane) {
+  constexpr int kBatch = 4;
+  const int first = __builtin_amdgcn_readlane(lo, 31), end = __builtin_amdgcn_readlane(hi, 0);
+  const bool upper = lane >= 32;
+  V m{}, all{};
+  if (first < end) {
+    const V* edge = one + (upper ? hi - step : lo);
+    const int b0 = (first + block - 1) / block, b1 = max(end / block, b0);  // whole blocks b0 .. b1 - 1, values before and after
+    const bool any = b0 < b1;
+    const int before = any ? b0 * block - first : end - first, after = any ? end - b1 * block : 0;
+    const int count = before + after + b1 - b0;
+    const auto value = [&](int i) {
+      return *(i < before ? one + first + i : i < before + after ? one + b1 * block + (i - before) : whole + b0 + (i - before - after));
+    };
+    m = edge[0];
+    for (int i0 = lane; i0 < count; i0 += 64 * kBatch) {
+      V v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v[i] = value(min(i0 + i * 64, count - 1));
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) all = larger(all, v[i]);
+    }
+    for (int i0 = 1; i0 < step; i0 += 2 * kBatch) {
+      V v[2 * kBatch];
+#pragma unroll
+      for (int i = 0; i < 2 * kBatch; ++i) v[i] = edge[min(i0 + i, step - 1)];
+#pragma unroll
+      for (int i = 0; i < 2 * kBatch; ++i) m = larger(m, v[i]);
+    }
+    m = larger(max_outwards(m, lane), max_of_wave(all));
+  } else {  // a window of few rows: all of the lane's own
+    for (int i0 = lo + (upper ? 1 : 0); i0 < hi; i0 += 2 * kBatch) {
+      V v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v[i] = one[min(i0 + 2 * i, hi - 1)];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) m = larger(m, v[i]);
+    }
+  }
+  return max_of_halves(m);
+}
+
+// The largest |v|_2 of the keys that the lane's row, of token `token`, sees (rows rise by at most a token from
+// lane to lane).
+__device__ __forceinline__ float window_norm(const BwdArgs& a, int head, int item, int64_t k0, int nk, int64_t p, int lane) {
+  const float* keys = a.key_norm + head * a.nk + k0;
+  const float* blocks = a.v_norm + head * a.v_slots + k0 / kNormKeys + item;
+  const int64_t first = p - a.window.left, past = p + a.window.right + 1;
+  const int lo = (int)(first < 0 ? 0 : first < nk ? first : nk), hi = (int)(past < 0 ? 0 : past < nk ? past : nk);
+  float m = range_max(lo, hi, 1, kNormKeys, keys, blocks, lane);
+  if (a.window.sinks > 0) {  // those before p + right, from running maxima of the first 64 and the next
+    const int most = min(a.window.sinks, nk), mine = min(a.window.sinks, hi);
+    float low = lane < most ? keys[lane] : 0.f, high = lane + 64 < most ? keys[lane + 64] : 0.f;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const float a_low = __shfl_up(low, o, 64), a_high = __shfl_up(high, o, 64);
+      if (lane >= o) low = fmaxf(low, a_low), high = fmaxf(high, a_high);
+    }
+    const float in_low = __shfl(low, max(min(mine, 64) - 1, 0), 64), in_high = __shfl(high, max(mine - 65, 0), 64);
+    if (mine > 0) m = fmaxf(m, in_low);
+    if (mine > 64) m = fmaxf(m, in_high);
+  }
+  return m;
+}
+
 template <DT D> __device__ __forceinline__ float absmax_frag(const Frag<D>& f) {
   float m = 0.f;
   const uint32_t w[4] = {f.v[0].x, f.v[0].y, f.v[0].z, f.v[0].w};
@@ -113,8 +212,9 @@ template <int DC> __device__ __forceinline__ void store_part(float* row, const f
 
 // A bound of |v|_2 over each block of keys (blockIdx.x of those, blockIdx.y the key head): 16 lanes a
 // row, each with the largest square sum of its 8 channels, added up (one sum a block and not one a
-// row; the longest row's norm is between a quarter of the bound and all of it).
-template <DT D> __global__ __launch_bounds__(256) void attention_norm_kernel(BwdArgs a) {
+// row; the longest row's norm is between a quarter of the bound and all of it).  With WINDOW each key's own,
+// too, and the largest of them.
+template <DT D, bool WINDOW> __global__ __launch_bounds__(256) void attention_norm_kernel(BwdArgs a) {
   __shared__ float s_top[64];
   const int head = blockIdx.y, c = threadIdx.x % 16 * 8;
   int tile;
@@ -135,7 +235,15 @@ template <DT D> __global__ __launch_bounds__(256) void attention_norm_kernel(Bwd
   }
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < kNormKeys / 16; ++i) top = fmaxf(top, dot_frag<D>(f[i], f[i], 0.f));
+  for (int i = 0; i < kNormKeys / 16; ++i) {
+    float sq = dot_frag<D>(f[i], f[i], 0.f);
+    if constexpr (WINDOW) {
+      sq = lanes_sum<16>(sq);
+      const int r = i * 16 + threadIdx.x / 16;
+      if (c == 0 && r < rows) a.key_norm[head * a.nk + k0 + first + r] = sqrtf(sq);
+    }
+    top = fmaxf(top, sq);
+  }
   top = fmaxf(top, __shfl_xor(top, 16, 64));
   top = fmaxf(top, __shfl_xor(top, 32, 64));
   if ((threadIdx.x & 63) < 16) s_top[threadIdx.x / 64 * 16 + threadIdx.x % 64] = top;
@@ -143,7 +251,7 @@ template <DT D> __global__ __launch_bounds__(256) void attention_norm_kernel(Bwd
   if (threadIdx.x != 0) return;
   float sq = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sq += fmaxf(fmaxf(s_top[i], s_top[16 + i]), fmaxf(s_top[32 + i], s_top[48 + i]));
+  for (int i = 0; i < (WINDOW ? 1 : 16); ++i) sq += fmaxf(fmaxf(s_top[i], s_top[16 + i]), fmaxf(s_top[32 + i], s_top[48 + i]));
   a.v_norm[head * a.v_slots + blockIdx.x] = sqrtf(sq);
 }
 
@@ -272,7 +380,7 @@ template <DT D, int DC, int W, int CUT, bool SINKS> __device__ __forceinline__ v
     const KeyRows r = key_rows<D, W, CUT, SINKS>(a, wave, l);
     const RowMap qmap{r.q0, r.share_head * r.group, r.group}, kmap{r.k0, r.share_head, 1};
     const int64_t stats = r.share_head * (a.nq * r.group) + r.q0 * r.group;
-    const float f = D == DT::F16 ? unit / 32768.f : 1.f;
+    const float u = D == DT::F16 ? lane_value(unit, l) : 1.f, f = D == DT::F16 ? u / 32768.f : 1.f;
     const float2 kr = row_pair<D>(kmap.at<D>(heads_of<D>(a.k), r.key), a.head_dim, lane);
     const float2 vr = row_pair<D>(kmap.at<D>(heads_of<D>(a.v), r.key), a.head_dim, lane);
     typename Elem<S>::T *dk, *dv;
@@ -297,7 +405,7 @@ template <DT D, int DC, int W, int CUT, bool SINKS> __device__ __forceinline__ v
       add_scaled(ov, to_float<D>(from_float<D>(p)), gr);
       add_scaled(ok, to_float<D>(from_float<D>(e)), qr);
     }
-    const float fk = a.scale / unit, fv = D == DT::F16 ? 1.f / 32768.f : 1.f;
+    const float fk = a.scale / u, fv = D == DT::F16 ? 1.f / 32768.f : 1.f;
     put_pair<S>(dk, mended(was_k, make_float2(ok.x * fk, ok.y * fk)), a.head_dim, lane);
     put_pair<S>(dv, mended(was_v, make_float2(ov.x * fv, ov.y * fv)), a.head_dim, lane);
   }
@@ -358,10 +466,17 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
     a.delta[at] = d;
   }
   float unit = 1.f;
-  if constexpr (D == DT::F16) {
+  const auto scale_rows = [&]() __attribute__((always_inline)) {  // float16
     peak = half_max(peak);
-    const float bound = 2.f * sqrtf(half_sum(sq)) * item_norm<W>(a, head, item, k0, nk, s_norm);
+    float v_norm;
+    // (of the keys that the row sees and no others: a hidden value must not take this row's precision)
+    if constexpr (WINDOW) v_norm = window_norm(a, head, item, k0, nk, (int64_t)(min(row, rows - 1) / group) + nk - nq, lane);
+    else v_norm = item_norm<W>(a, head, item, k0, nk, s_norm);
+    const float bound = 2.f * sqrtf(half_sum(sq)) * v_norm;
     unit = e_scale(peak, bound);
+    if constexpr (WINDOW) {
+      if (first && there && lane < 32) a.row_peak[head * (a.nq * group) + q0 * group + row] = make_float2(peak, bound);
+    }
     const float2 top = make_float2(wave_max(peak), wave_max(bound));
     if (lane == 0) s_peak[wave] = top;
     __syncthreads();
@@ -371,7 +486,10 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
       for (int w = 0; w < W; ++w) all = make_float2(fmaxf(all.x, s_peak[w].x), fmaxf(all.y, s_peak[w].y));
       a.peak[head * a.q_slots + share.slot] = all;
     }
-  }
+  };
+  // (a window's scale takes some dependent loads, which go behind those of the first tiles)
+  constexpr bool kScaleLate = D == DT::F16 && WINDOW;
+  if constexpr (D == DT::F16 && !WINDOW) scale_rows();
   const float c = a.scale * kLog2e;
 
   Loader lk, lv;
@@ -435,13 +553,20 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dq_kernel(BwdArgs a) {
 #pragma unroll
       for (int db = 0; db < DC / 32; ++db) acc[db] = mma<D>(rd.column_frag(slot * kTile, st * 16, db), e[st], acc[db]);
   };
-  if (tiles > 0) {
-    // Step t reads k and v of tile t + 1 and k of tile t - 1 and starts the loads of tile t + 2.
+  // Step t reads k and v of tile t + 1 and k of tile t - 1 and starts the loads of tile t + 2.
+  const auto start = [&]() __attribute__((always_inline)) {
     load_k(0, 0);
     load_v(0, 0);
     load_k(-1, 3);  // (zeros)
     load_k(1, 1);
     load_v(1, 1);
+  };
+  if constexpr (kScaleLate) {
+    if (tiles > 0) start();
+    scale_rows();
+  }
+  if (tiles > 0) {
+    if constexpr (!kScaleLate) start();
     wait_vmcnt<3 * Loader::N>();
     barrier_no_fence();
     f32x16_t s0, dp0, s1, dp1;
@@ -582,11 +707,10 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   const float* delta = a.delta + head * (a.nq * group) + q0 * group;
 
   float unit = 1.f;
-  if constexpr (D == DT::F16) {  // the largest |dout| and bound of the item and head, from its query blocks
+  if constexpr (D == DT::F16 && !WINDOW) {  // the largest |dout| and bound of the item and head, from its query blocks
     const int64_t first = q0 * group / a.q_rows + item;
     float2 top = make_float2(0.f, 0.f);
-    const int t0 = WINDOW ? row0 / a.q_rows : 0;  // (those that the keys are seen by)
-    for (int t = t0 + threadIdx.x; t < (row_end + a.q_rows - 1) / a.q_rows; t += W * 64) {
+    for (int t = threadIdx.x; t < (rows + a.q_rows - 1) / a.q_rows; t += W * 64) {
       const float2 b = a.peak[head * a.q_slots + first + t];
       top = make_float2(fmaxf(top.x, b.x), fmaxf(top.y, b.y));
     }
@@ -596,7 +720,6 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
 #pragma unroll
     for (int w = 0; w < W; ++w) top = make_float2(fmaxf(top.x, s_peak[w].x), fmaxf(top.y, s_peak[w].y));
     unit = e_scale(top.x, top.y);
-    if constexpr (WINDOW) unit = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(unit)));
   }
   const float p_unit = D == DT::F16 ? 1.f / 32768.f : 1.f;
 
@@ -706,6 +829,14 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   };
   if (steps > 0) {
     load(0);
+    if constexpr (D == DT::F16 && WINDOW) {  // the largest |dout| and bound of the rows that see the own key
+      const float2* one = a.row_peak + head * (a.nq * group) + q0 * group;
+      const float2* blocks = a.peak + head * a.q_slots + q0 * group / a.q_rows + item;
+      int from = view.from, to = view.from + (int)view.span;
+      if constexpr (SINKS) from = min(max(from, row0), row_end), to = max(from, min(to, row_end));  // (of the chunk)
+      const float2 top = range_max(from, to, group, a.q_rows, one, blocks, lane);
+      unit = e_scale(top.x, top.y);
+    }
     for (int t = 0; t < steps; t += 2) {  // (an odd end takes a step of zeros: a second exit costs registers)
       step(0);
       step(1);
@@ -713,8 +844,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
   }
   wait_vmcnt<0>();  // (the loads past the end)
   if constexpr (WINDOW) {
-    // (64 channels: what the lane's number gives is not kept over the loop)
-    const int own_lane = DP == 64 ? fresh_lane() : lane, key = tile * kKeys + wave * 32 + (own_lane & 31);
+    // (64 channels and float16: what the lane's number gives is not kept over the loop)
+    const int own_lane = DP == 64 || (D == DT::F16 && !SINKS) ? fresh_lane() : lane, key = tile * kKeys + wave * 32 + (own_lane & 31);
     const bool there = key < nk;
     const uint64_t odd = odd_rows<DC>(dk, there) | odd_rows<DC>(dv, there);
     if constexpr (SINKS) {
@@ -916,11 +1047,14 @@ Status launch(BwdArgs a, hipStream_t stream) {
   a.v_slots = a.nk / kNormKeys + a.items;
   const size_t peak = D == DT::F16 ? padded((size_t)a.q_slots * a.kv_heads * sizeof(float2)) : 0;
   const size_t norm = D == DT::F16 ? padded((size_t)a.v_slots * a.kv_heads * sizeof(float)) : 0;
+  constexpr bool kEach = D == DT::F16 && WINDOW;
+  const size_t row_peak = kEach ? padded((size_t)rows * a.kv_heads * sizeof(float2)) : 0;
+  const size_t key_norm = kEach ? padded((size_t)a.nk * a.kv_heads * sizeof(float)) : 0;
   const size_t part_q = (size_t)cut_places(a.q_cut) * q_rows * DP * sizeof(float);
   const size_t part_k = (size_t)cut_places(a.k_cut) * k_rows * DP * sizeof(float);
   void* scratch = nullptr;
   const size_t part_s = sinks ? (size_t)a.sink_slots * a.kv_heads * a.sink_keys * 2 * DP * sizeof(float) : 0;
-  Status st = lease.take(dev, stream, 2 * stat + peak + norm + part_q + 2 * part_k + part_s, &scratch);
+  Status st = lease.take(dev, stream, 2 * stat + peak + norm + row_peak + key_norm + part_q + 2 * part_k + part_s, &scratch);
   if (!st.ok()) return st;
   unsigned char* p = static_cast<unsigned char*>(scratch);
   a.norm = reinterpret_cast<float*>(p);
@@ -928,6 +1062,9 @@ Status launch(BwdArgs a, hipStream_t stream) {
   a.peak = reinterpret_cast<float2*>(p + 2 * stat);
   a.v_norm = reinterpret_cast<float*>(p + 2 * stat + peak);
   p += 2 * stat + peak + norm;
+  a.row_peak = reinterpret_cast<float2*>(p);
+  a.key_norm = reinterpret_cast<float*>(p + row_peak);
+  p += row_peak + key_norm;
   if (part_q > 0) a.dq_part = reinterpret_cast<float*>(p);
   if (part_k > 0) {
     a.dk_part = reinterpret_cast<float*>(p + part_q);
@@ -936,7 +1073,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
   a.sink_part = reinterpret_cast<float*>(p + part_q + 2 * part_k);
   if constexpr (D == DT::F16) {
     if (a.nk > 0) {
-      attention_norm_kernel<D><<<dim3((unsigned)a.v_slots, (unsigned)a.kv_heads), 256, 0, stream>>>(a);
+      attention_norm_kernel<D, WINDOW><<<dim3((unsigned)a.v_slots, (unsigned)a.kv_heads), 256, 0, stream>>>(a);
       SUBM_HIP_TRY(hipGetLastError());
     }
   }
