@@ -30,10 +30,10 @@ struct BwdArgs {
   Cut q_cut, k_cut;
   float *dq_part, *dk_part, *dv_part;
   // Of the kernels with WINDOW.  The first `sinks` keys of an item are seen by all rows behind them: their
-  // dk and dv come from chunks of `sink_rows` packed rows, [kv_heads][chunk][sinks rounded up to 32][2][DP]
-  // float32 sums, added up by a kernel of their own.
+  // dk and dv come from chunks of `sink_rows` packed rows, [kv_heads][chunk][sinks][2][DP] float32 sums, added up
+  // by a kernel of their own.
   Window window;
-  int sink_rows, sink_keys;
+  int sink_rows;
   int64_t sink_slots;
   float* sink_part;
 };
@@ -385,7 +385,7 @@ template <DT D, int DC, int W, int CUT, bool SINKS> __device__ __forceinline__ v
     const float2 vr = row_pair<D>(kmap.at<D>(heads_of<D>(a.v), r.key), a.head_dim, lane);
     typename Elem<S>::T *dk, *dv;
     if constexpr (SINKS) {
-      dk = a.sink_part + (((int64_t)r.share_head * a.sink_slots + r.share_place) * a.sink_keys + r.key) * 2 * DP;
+      dk = a.sink_part + (((int64_t)r.share_head * a.sink_slots + r.share_place) * a.window.sinks + r.key) * 2 * DP;
       dv = dk + DP;
     } else if constexpr (kPart) {
       const int64_t at = ((int64_t)r.share_place * 32 * W + wave * 32 + l) * DP;
@@ -849,7 +849,7 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     const bool there = key < nk;
     const uint64_t odd = odd_rows<DC>(dk, there) | odd_rows<DC>(dv, there);
     if constexpr (SINKS) {
-      const int64_t at = (((int64_t)head * a.sink_slots + share.slot) * a.sink_keys + key) * 2 * DP;
+      const int64_t at = (((int64_t)head * a.sink_slots + share.slot) * a.window.sinks + key) * 2 * DP;
       if (there) {
         store_part<DC>(a.sink_part + at, dk, a.scale / unit, own_lane);
         store_part<DC>(a.sink_part + at + DP, dv, p_unit, own_lane);
@@ -892,8 +892,8 @@ template <DT D, int DP> __global__ __launch_bounds__(256) void attention_sink_su
   const int chunks = (int)(((int64_t)nq * group + a.sink_rows - 1) / a.sink_rows);
   const int64_t first = (int64_t)head * a.sink_slots + q0 * group / a.sink_rows + item;
   const int at = threadIdx.x % kThreads * 4, mine = threadIdx.x / kThreads;
-  const float* part = a.sink_part + (first * a.sink_keys + key) * 2 * DP + at;
-  const int64_t step = (int64_t)a.sink_keys * 2 * DP;
+  const float* part = a.sink_part + (first * a.window.sinks + key) * 2 * DP + at;
+  const int64_t step = (int64_t)a.window.sinks * 2 * DP;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int s = mine; s < chunks; s += kGroups) {
@@ -1034,7 +1034,6 @@ Status launch(BwdArgs a, hipStream_t stream) {
     const int blocks = (a.window.sinks + 31) / 32;
     const int64_t chunk = rows * a.kv_heads * blocks / (kUnits * 4);
     a.sink_rows = (int)std::min<int64_t>(std::max<int64_t>(chunk, 128), 8192) / group * group;
-    a.sink_keys = blocks * 32;
     a.sink_slots = rows / a.sink_rows + a.items;
   }
 
@@ -1053,7 +1052,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
   const size_t part_q = (size_t)cut_places(a.q_cut) * q_rows * DP * sizeof(float);
   const size_t part_k = (size_t)cut_places(a.k_cut) * k_rows * DP * sizeof(float);
   void* scratch = nullptr;
-  const size_t part_s = sinks ? (size_t)a.sink_slots * a.kv_heads * a.sink_keys * 2 * DP * sizeof(float) : 0;
+  const size_t part_s = sinks ? (size_t)a.sink_slots * a.kv_heads * a.window.sinks * 2 * DP * sizeof(float) : 0;
   Status st = lease.take(dev, stream, 2 * stat + peak + norm + row_peak + key_norm + part_q + 2 * part_k + part_s, &scratch);
   if (!st.ok()) return st;
   unsigned char* p = static_cast<unsigned char*>(scratch);
@@ -1099,7 +1098,7 @@ Status launch(BwdArgs a, hipStream_t stream) {
     if (sinks) {
       a.k_cut = Cut{(int)a.sink_slots, 0, 0, 1, false};
       if (a.nq > 0) {
-        const dim3 grid((unsigned)a.sink_slots, (unsigned)a.kv_heads, (unsigned)a.sink_keys / 32);
+        const dim3 grid((unsigned)a.sink_slots, (unsigned)a.kv_heads, (unsigned)((a.window.sinks + 31) / 32));
         attention_dkv_kernel<D, DC, 1, 1, kNoCut, true, true><<<grid, 64, 0, stream>>>(a);
         SUBM_HIP_TRY(hipGetLastError());
       }
