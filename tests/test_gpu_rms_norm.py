@@ -198,3 +198,19 @@ def test_gradients_against_differences():
     size = sum((g.double() * s).norm().item() for g, s in ((dx, dirs["x"]), (dx, dirs["residual"]), (dg, dirs["gamma"])))
     print(f"  {slope} {got} {size}", flush=True)
     assert abs(slope - got) < 1e-3 * size
+
+
+@pytest.mark.parametrize("n,c", [(600, 1024), (2000, 333), (40, 9000)])
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_8_bits_are_the_quotients(n, c, group):
+    # float32, whose y the other call gives as it is: max |y| / 448 and y / scale in float32, rounded to nearest even,
+    # bit for bit (a product with the scale's reciprocal moves values next to a tie)
+    t = inputs(n, c, "f32", n + c + group)
+    y = sc.sparse_rms_norm_forward(t["x"], t["gamma"], t["residual"], EPS)[0].cpu()
+    q, scales, _, _ = sc.sparse_rms_norm_quantize_forward(t["x"], t["gamma"], t["residual"], EPS, group=group)
+    per = group or c
+    parts = torch.nn.functional.pad(y.abs(), (0, -c % per)).reshape(n, -1, per)
+    want = parts.amax(2) / torch.tensor(448.0)
+    assert torch.equal(scales.cpu(), want)
+    wide = want.repeat_interleave(per, 1)[:, :c]
+    assert torch.equal(q.cpu().view(torch.uint8), (y / wide).to(torch.float8_e4m3fn).view(torch.uint8))
