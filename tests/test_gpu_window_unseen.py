@@ -4,6 +4,8 @@ finite, and large finite hidden values, which scale nothing that does not see th
 Finite hidden values meet only zeros, so results of the rows (and gradients of the keys) that do not see them
 have to be the same bits; those beside values that are not finite may be computed again in another order, within
 the componentwise bounds of oracle.transformer_ref.window_attention_error_bounds."""
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -165,3 +167,42 @@ def test_large_values_that_are_seen(window, nq, nk, heads, kv_heads, d):
         gb = g.clone()
         gb[i] = 200.0 * torch.sign(gb[i])
         compare(k, v, gb, f"row {i}")
+
+
+@functools.lru_cache(maxsize=None)
+def clean_case(dtype, window):
+    """Inputs of 1,600 tokens, their gradients in 64 bits and the componentwise bounds."""
+    n, heads, d = 1600, 2, 64
+    t = make(n, n, heads, heads, d, dtype, 31, g_scale=1.0)
+    a, o, scale = [f64(x) for x in t], [0, n], d ** -0.5
+    want = (*ref.window_attention(*a[:3], o, o, scale, *window), *ref.window_attention_grad(a[3], *a[:3], o, o, scale, *window))
+    bounds = ref.window_attention_error_bounds(*a[:3], o, o, scale, U[dtype], TINY[dtype], 0.0 if dtype == "f32" else U[dtype], a[3], *window)
+    return t, want, bounds, ref.window_mask(n, n, *window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("window", [(255, 0, 4), (None, 0, 0), (100, 100, 0), (300, 0, 40)])
+@pytest.mark.parametrize("bad", ["q", "k", "v", "dout", "all"])
+def test_what_is_computed_again_is_as_exact(dtype, window, bad):
+    # tokens from 700 on, every 301st, are not finite: the rows that see none of them, many of which meet them in
+    # their tiles and are computed again, are within the bounds of any evaluation, component by component
+    t, want, bounds, seen = clean_case(dtype, window)
+    n = len(seen)
+    t, at = [x.clone() for x in t], np.zeros(n, dtype=bool)
+    at[700::301] = True
+    for i, x in enumerate(t):
+        if bad in ("all", ("q", "k", "v", "dout")[i]):
+            x[kept(at), :, ::7] = float("inf") if i == 2 else float("nan")
+    o = torch.tensor([0, n], device=DEV)
+    got = both(*t, o, o, window)
+    rows = np.zeros(n, dtype=bool)  # whose results may be anything
+    if bad in ("q", "dout", "all"):
+        rows |= at
+    if bad in ("k", "v", "all"):
+        rows |= seen[:, at].any(1)
+    keys = seen[rows].any(0)
+    assert (~rows).sum() >= 256
+    for i, what in enumerate(("out", "lse", "dq", "dk", "dv")):
+        keep = ~rows if i < 3 else ~keys
+        error = np.abs(f64(got[i][kept(keep)]) - want[i][keep])
+        assert (error <= bounds[i][keep] + (0.0 if i == 1 else TINY[dtype])).all(), what
