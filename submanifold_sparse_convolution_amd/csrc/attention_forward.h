@@ -156,7 +156,7 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
   int item, tile, nq, nk;
   int64_t q0, k0;
   if constexpr (WINDOW) {
-    const Item it = find_rows<false>(a, a.window, group, kRows, share.slot);
+    const Item it = find_rows(a, a.window, group, kRows, share.slot);
     item = it.index, tile = it.tile, q0 = it.q0, nq = it.nq, k0 = it.k0, nk = it.nk;
   } else {
     item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(FwdArgs a) {
   int item, tile, nq;
   int64_t q0;
   if constexpr (WINDOW) {
-    const Item it = find_rows<false>(a, a.window, group, kRows, share.slot);
+    const Item it = find_rows(a, a.window, group, kRows, share.slot);
     item = it.index, tile = it.tile, q0 = it.q0, nq = it.nq;
   } else {
     item = find_item(a.q_offsets, a.nq, a.items, group, kRows, share.slot, &tile);
@@ -461,7 +461,7 @@ template <DT D, int DP> __global__ __launch_bounds__(256) void attention_join_ro
   __shared__ float2 s_state[kGroups];
   const int group = a.heads / a.kv_heads, parts = a.cut.parts;
   const Share share = tile_share(a.cut, blockIdx.x);
-  const Item it = find_rows<false>(a, a.window, group, 32, share.slot);
+  const Item it = find_rows(a, a.window, group, 32, share.slot);
   const int64_t row = (int64_t)it.tile * 32 + blockIdx.y;
   if (row >= (int64_t)it.nq * group) return;
   const int c = threadIdx.x % kThreads * 4, mine = threadIdx.x / kThreads;
@@ -540,10 +540,9 @@ template <DT D, int DC, int W, int CUT, bool WINDOW, int KG = 1> Status launch_c
   SUBM_HIP_TRY((launch_tiles<D, DC, W, KG, CUT, WINDOW>(a, stream)));
   if constexpr (W == 1) {
     attention_join_rows_kernel<D, DP><<<dim3((unsigned)a.cut.cut, (unsigned)std::min<int64_t>(32, a.nq * (a.heads / a.kv_heads))), 256, 0, stream>>>(a);
-    SUBM_HIP_TRY(hipGetLastError());
-    return Status{};
+  } else {
+    attention_join_kernel<D, DP, W, WINDOW><<<dim3((unsigned)a.cut.cut, 32 * W * (DP / 4) / 256), 256, 0, stream>>>(a);
   }
-  attention_join_kernel<D, DP, W, WINDOW><<<dim3((unsigned)a.cut.cut, 32 * W * (DP / 4) / 256), 256, 0, stream>>>(a);
   SUBM_HIP_TRY(hipGetLastError());
   return Status{};
 }

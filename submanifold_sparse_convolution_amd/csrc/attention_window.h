@@ -63,18 +63,16 @@ __device__ __forceinline__ int64_t lane_value64(int64_t v, int lane) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// find_item and item_rows of slot `slot` in the tiling of the queries (BY_KEYS: of the keys) by `block` packed
-// rows, in one; every lane of the wave calls it.
-template <bool BY_KEYS, typename Args>
+// find_item and item_rows of slot `slot` in the tiling of the queries by `block` packed rows, in one; every lane of
+// the wave calls it.
+template <typename Args>
 __device__ __forceinline__ Item find_rows(const Args& a, const Window& w, int group, int block, int64_t slot) {
   const int lane = threadIdx.x & 63;
-  const int64_t* by = BY_KEYS ? a.k_offsets : a.q_offsets;
-  const int64_t total = BY_KEYS ? a.nk : a.nq;
-  const auto start = [&](int64_t o, int b) { return (o < 0 ? 0 : o > total ? total : o) * group / block + b; };
+  const auto start = [&](int64_t o, int b) { return (o < 0 ? 0 : o > a.nq ? a.nq : o) * group / block + b; };
   int first = 0, count = a.items;  // the item is one of first .. first + count - 1
   while (count > 64) {
     const int stride = (count + 63) / 64, at = lane * stride;
-    const bool before = at < count && start(by[first + min(at, count - 1)], first + at) <= slot;
+    const bool before = at < count && start(a.q_offsets[first + min(at, count - 1)], first + at) <= slot;
     const int n = max(1, (int)__popcll(__builtin_amdgcn_ballot_w64(before)));
     first += (n - 1) * stride;
     count = min(stride, count - (n - 1) * stride);
@@ -82,7 +80,7 @@ __device__ __forceinline__ Item find_rows(const Args& a, const Window& w, int gr
   const int mine = first + min(lane, count - 1);
   const int64_t q_from = a.q_offsets[mine], q_to = a.q_offsets[mine + 1], k_from = a.k_offsets[mine], k_to = a.k_offsets[mine + 1];
   const int64_t there = w.k_lengths != nullptr ? w.k_lengths[mine] : INT64_MAX;
-  const int64_t at = start(BY_KEYS ? k_from : q_from, mine);
+  const int64_t at = start(q_from, mine);
   const int n = max(1, (int)__popcll(__builtin_amdgcn_ballot_w64(lane < count && at <= slot)));
   const auto rows = [&](int64_t from, int64_t to, int64_t most, int64_t* first_row, int* number) {
     const int64_t s = lane_value64(from, n - 1), e = lane_value64(to, n - 1);
@@ -100,7 +98,7 @@ __device__ __forceinline__ Item find_rows(const Args& a, const Window& w, int gr
   return item;
 }
 
-// Host: plan_cut for windows, whose last tiles stay whole (in parts they measured the same).  `resident`: workgroups
+// Host: plan_cut for windows: all tiles in parts, or none (the last ones alone are never cut).  `resident`: workgroups
 // that the machine holds.  Where most of an item is seen the longest tile takes twice the mean, and few tiles
 // leave compute units that wait for it: then in at least four parts (three and six, which the XCDs do not share
 // evenly, measured up to 30 % slower).  16,384 tokens, 8 / 2 heads of 128, causal, backward: 3.48 -> 1.81 ms; 9,000
@@ -119,20 +117,20 @@ inline Cut plan_window_cut(const Window& w, int64_t slots, int kv_heads, int64_t
 // take workgroups in turn and each has its own L2: every XCD gets a run of consecutive tiles, so that what
 // one loads the next finds there (24,576 tokens, 16 heads of 128, 2,048 keys: 493 -> 437 us).  Not with grouped
 // heads, whose tiles are that many times fewer tokens apart as it is (16,384 tokens, 8 / 2 heads: 150 us, 176 in
-// runs).  Where tiles differ in length (an open end) the longest go first (`last_first`: those of the last rows),
-// which walk the same keys from the start on (16,384 tokens, 8 / 2 heads of 128, causal: 673 -> 526 us).
+// runs).  Where tiles differ in length (an open end) each head's go from the last rows' on (`last_first`: an item's
+// last rows walk the most keys, and those the same from the start on; 16,384 tokens, 8 / 2 heads of 128, causal:
+// 673 -> 526 us); heads follow one another, and items from the last one on, whatever their lengths.
 template <int CUT> __device__ __forceinline__ Share window_share(const Cut& c, const Window& w, bool last_first) {
   Share s = share_of<CUT>(c, blockIdx.x);
-  if (CUT == kCutAll || s.part >= 0) return s;
+  if constexpr (CUT != kNoCut) return s;
   if (w.runs) {
     constexpr uint32_t kXcds = 8;
-    const uint32_t block = CUT == kNoCut ? blockIdx.x + gridDim.x * blockIdx.y : blockIdx.x;
-    const uint32_t all = CUT == kNoCut ? gridDim.x * gridDim.y : (uint32_t)c.whole;
+    const uint32_t block = blockIdx.x + gridDim.x * blockIdx.y, all = gridDim.x * gridDim.y;
     const uint32_t xcd = block % kXcds, each = all / kXcds, more = all % kXcds;
     const uint32_t id = xcd * each + min(xcd, more) + block / kXcds;
     s.head = first_lane(id / (uint32_t)c.slots);
     s.slot = (int)(id - (uint32_t)s.head * c.slots);
-  } else if (last_first && CUT == kNoCut) {
+  } else if (last_first) {
     s.slot = c.slots - 1 - s.slot;
   }
   return s;
