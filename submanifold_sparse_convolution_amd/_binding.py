@@ -8,6 +8,7 @@ fallback: when the shared library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -1119,12 +1120,14 @@ def _window_args(left, right, sinks):
     """left, right (None: open) and sinks as the library takes them."""
     ends = []
     for end, what in ((left, "left"), (right, "right")):
-        if end is not None and end < 0:
+        end = 2 ** 31 if end is None else operator.index(end)  # (whole numbers: 2.5 is refused)
+        if end < 0:
             raise ValueError(f"{what} must not be negative (None leaves it open)")
-        ends.append(2 ** 31 if end is None else min(int(end), 2 ** 31))
+        ends.append(min(end, 2 ** 31))
+    sinks = operator.index(sinks)
     if not 0 <= sinks < 2 ** 31:
         raise ValueError("sinks must not be negative")
-    return (*ends, int(sinks))
+    return (*ends, sinks)
 
 
 def sparse_window_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,

@@ -110,3 +110,11 @@ def test_binding_names_the_fault():
     with pytest.raises(ValueError, match="sinks"):
         sc._binding._window_args(0, 0, -2)
     assert sc._binding._window_args(None, 2 ** 70, 3) == (2 ** 31, 2 ** 31, 3)
+
+
+def test_binding_takes_whole_numbers():
+    # a window of 2.5 keys was one of 2
+    for bad in ((2.5, 0, 0), (0, 1.0, 0), (None, None, 0.5), (float("inf"), 0, 0), (0, "1", 0)):
+        with pytest.raises(TypeError):
+            sc._binding._window_args(*bad)
+    assert sc._binding._window_args(np.int64(7), torch.tensor(3), np.int32(2)) == (7, 3, 2)
