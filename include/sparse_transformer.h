@@ -305,7 +305,8 @@ int sparse_window_attention_forward(const subm_heads_t* q, const subm_heads_t* k
  * sparse_window_attention_backward -- gradients of sparse_window_attention_forward without k_lengths: those of
  * sparse_attention_backward, each sum over the keys that a query sees or the queries that see a key.  A key
  * that no query sees gets dk = dv = 0, and a query that sees no key dq = 0; what a query does not see changes
- * neither its dq nor, through it, other keys' gradients.  The sinks' sums go through float32 partial results in
+ * neither its dq nor, through it, other keys' gradients (SUBM_F16: ds is scaled for dq by what its row sees, for
+ * dk by the rows that see its key).  The sinks' sums go through float32 partial results in
  * scratch memory, one a chunk of query rows and at least one an item: with many short items they take 8 bytes times
  * items, kv_heads, sinks and head_dim (rounded up to 64 or 128).
  */

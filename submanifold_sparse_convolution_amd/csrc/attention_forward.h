@@ -281,7 +281,7 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
     // WINDOW: whether the wave sees any key of tile t - 1 (was), t (now) and t + 1 (soon).  It leaves out the
     // steps without any: what it holds of such tiles is masked, and their p is 0, before a step reads it.  In
     // float32, whose products are slow (2,000 tokens, 6 / 3 heads of 80, causal: 121 -> 110 us), and at 64 channels, where
-    // exponentials bound (four items, 9,371 tokens, 12 heads, 256 keys each way: 54 -> 44 us), of whole tiles alone:
+    // vector instructions weigh most (four items, 9,371 tokens, 12 heads, 256 keys each way: 54 -> 44 us), of whole tiles alone:
     // elsewhere the branch costs as much (24,576 tokens, 16 heads of 128: 431 us, 437 with it).
     constexpr bool kSkip = WINDOW && KG == 1 && (D == DT::F32 || (DP == 64 && CUT == kNoCut));
     bool was = false, now = true;
@@ -316,6 +316,8 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
       float shrink;
       const bool moves = softmax_tile<D, KB>(s, c, state, &shrink);
       product(slot ^ 1, p);
+      // (p in the storage type, as the matrix cores take it: each off by half a step, of either sign, while the sum
+      // that divides has all 32 bits; outputs are 1.2 to 1.45 times as far from 64 bits as one rounding leaves them)
 #pragma unroll
       for (int st = 0; st < 2 * KB; ++st) {
         p[st] = to_frag<D>(s[st / 2], st % 2);

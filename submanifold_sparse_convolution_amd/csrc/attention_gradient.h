@@ -816,7 +816,8 @@ __global__ __launch_bounds__(W * 64, OCC) void attention_dkv_kernel(BwdArgs a) {
     if constexpr (WINDOW) {
       if (!view.sees_all(r, kStep)) view.mask(r, lane, [&](int i) { s[i] = dp[i] = 0.f; });
     }
-    // (rows past the end: q, dout, norm and d read 0, so p is 1 and meets a dout of 0, and e is 0)
+    // (rows past the end: q, dout, norm and d read 0, so p is 1 and meets a dout of 0, and e is 0; both in the storage
+    // type, as the matrix cores take them, each off by half a step of either sign)
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       const Frag<D> p = to_frag<D>(s, st), e = to_frag<D>(dp, st);

@@ -4,8 +4,9 @@
 // The kernels of attention.hip over fewer keys: a block of query rows walks the tiles from its first row's
 // first key to its last row's last, and those of the sinks before them (attention_window.h).
 //
-// Bound by the matrix cores, at 64 channels by the exponentials, and with few rows by the latency of a short
-// walk.  Measured: items of 13,001 and 11,575 tokens, 16 heads of 128, bf16, 2,048 keys and 4 sinks: 440 us (0.86
+// Bound by products and exponentials in turn (24,576 tokens at 128 channels: matrix cores busy 50 % of the cycles,
+// vector units 48; at 64 channels 22 and 47, and 900 tiles on 768 places), and with few rows by the latency of a
+// short walk.  Measured: items of 13,001 and 11,575 tokens, 16 heads of 128, bf16, 2,048 keys and 4 sinks: 440 us (0.86
 // PFLOP/s of what the rows see, 0.92 of what the tiles compute); four items, 9,371 tokens, 12 heads of 64, f16,
 // 256 keys each way: 43 us; 8 single tokens, 16 / 4 heads of 128, bf16, 4,096 keys of caches to 32,768: 23 us, 59 MB.
 #include "attention_forward.h"
