@@ -57,8 +57,9 @@ struct RowState {
 };
 
 // Scores (raw) -> probabilities in place; returns the factor that earlier sums shrink by, and
-// whether any row of the wave does shrink.
-template <DT D, int KB>
+// whether any row of the wave does shrink.  All rows of the wave take their maximum then; with WINDOW each by
+// itself, so that what it does not see has no part in its roundings either.
+template <DT D, int KB, bool WINDOW>
 __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowState& st, float* shrink) {
   float top = s[0][0];
 #pragma unroll
@@ -67,9 +68,9 @@ __device__ __forceinline__ bool softmax_tile(f32x16_t (&s)[KB], float c, RowStat
     for (int i = 0; i < 16; i += 2) top = max3(top, s[kb][i], s[kb][i + 1]);
   top = half_max(top);
   top = kLift<D> == 0.f ? top * c : fmaf(top, c, -kLift<D>);
-  const bool moves = __builtin_amdgcn_ballot_w64(top > st.base + kSlack<D>) != 0;
-  // (a scalar gate instead of a branch, which would part the matrix products from the exponentials)
-  const float base = fmaxf(st.base, top + (moves ? 0.f : -INFINITY));
+  const bool rises = top > st.base + kSlack<D>, moves = __builtin_amdgcn_ballot_w64(rises) != 0;
+  // (a gate instead of a branch, which would part the matrix products from the exponentials)
+  const float base = WINDOW ? (rises ? top : st.base) : fmaxf(st.base, top + (moves ? 0.f : -INFINITY));
   *shrink = exp2_fast(st.base - base);
   st.base = base;
   float sum = 0.f;
@@ -314,7 +315,7 @@ __global__ __launch_bounds__(KG * W * 64, OCC) void attention_forward_kernel(Fwd
       }
       scores(slot ^ 1, next);
       float shrink;
-      const bool moves = softmax_tile<D, KB>(s, c, state, &shrink);
+      const bool moves = softmax_tile<D, KB, WINDOW>(s, c, state, &shrink);
       product(slot ^ 1, p);
       // (p in the storage type, as the matrix cores take it: each off by half a step, of either sign, while the sum
       // that divides has all 32 bits; outputs are 1.2 to 1.45 times as far from 64 bits as one rounding leaves them)

@@ -206,3 +206,24 @@ def test_what_is_computed_again_is_as_exact(dtype, window, bad):
         keep = ~rows if i < 3 else ~keys
         error = np.abs(f64(got[i][kept(keep)]) - want[i][keep])
         assert (error <= bounds[i][keep] + (0.0 if i == 1 else TINY[dtype])).all(), what
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("window", [(40, 0, 0), (40, 0, 4), (None, 0, 0), (2, 3, 0), (600, 0, 40)])
+@pytest.mark.parametrize("nq,nk,heads,kv_heads,d", [(700, 700, 2, 2, 64), (500, 900, 6, 2, 128), (3, 900, 12, 1, 96)])
+def test_large_hidden_keys_and_other_queries(dtype, window, nq, nk, heads, kv_heads, d):
+    # a key far above what a row sees, or another row's query: when their maxima rise the row's own stays where it is
+    q, k, v, g = make(nq, nk, heads, kv_heads, d, dtype, nq + d)
+    qo, ko = (torch.tensor([0, n], device=DEV) for n in (nq, nk))
+    seen = ref.window_mask(nq, nk, *window)
+    clean = both(q, k, v, g, qo, ko, window)
+    for which, n in ((0, nq), (1, nk)):
+        for at in sorted({0, n // 2, n - 40, n - 1} & set(range(n))):
+            t = [q.clone(), k.clone()]
+            t[which][at] *= 50.0
+            got = both(*t, v, g, qo, ko, window)
+            rows = np.arange(nq) == at if which == 0 else seen[:, at]
+            keys = seen[rows].any(0)
+            for i, what in enumerate(("out", "lse", "dq", "dk", "dv")):
+                keep = kept(~(rows if i < 3 else keys))
+                assert torch.equal(got[i][keep], clean[i][keep]), (which, at, what)
